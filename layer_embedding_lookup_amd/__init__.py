@@ -34,7 +34,9 @@ __all__ = ["HashParams", "Table", "Layer", "ple_ngram_ids", "ple_gather", "ple_l
            "ple_prefill_fused_noalloc",
            "prefill_conv_input", "prefill_kv",
            "ple_host_alloc", "ple_host_free", "HostBuffer", "ple_stream_create_cu_masked", "ple_stream_destroy",
-           "ple_error_message", "ple_version", "library"]
+           "ple_error_message", "ple_version", "library",
+           "W4Weight", "KV4Cache", "ple_w4_linear", "ple_kv4_append", "ple_kv4_read", "ple_kv4_attention",
+           "ple_kv4_attention_workspace_bytes"]
 
 
 def library() -> ctypes.CDLL:
@@ -619,3 +621,7 @@ def ple_error_message() -> str:
 
 def ple_version() -> str:
     return capi.load().ple_version().decode()
+
+
+from .fp4 import (KV4Cache, W4Weight, ple_kv4_append, ple_kv4_attention, ple_kv4_attention_workspace_bytes,  # noqa: E402
+                  ple_kv4_read, ple_w4_linear)

@@ -1,4 +1,4 @@
-"""ctypes view of libple's C ABI (include/ple.h): structures, prototypes, loader.
+"""ctypes view of libple's C ABI (include/ple.h, include/ple_fp4.h): structures, prototypes, loader.
 
 Argument marshalling only; every step of the path runs in libple's kernels.
 Loading fails loudly when libple.so has not been built.
@@ -14,6 +14,7 @@ import torch  # noqa: F401  (load torch's HIP runtime first so libple binds to t
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libple.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "ple.h")
+FP4_HEADER = os.path.join(os.path.dirname(HERE), "include", "ple_fp4.h")
 
 PLE_OK = 0
 PLE_ERR_INVALID_ARGUMENT = 1
@@ -24,6 +25,8 @@ PLE_DTYPE_BF16 = 0
 PLE_DTYPE_FP8_E4M3 = 1
 PLE_DTYPE_FP8_E4M3_GLOBAL = 2
 PLE_DTYPE_NVFP4 = 3
+PLE_W4_NVFP4 = 0
+PLE_W4_INT4 = 1
 PLE_MAX_HEADS = 32
 PLE_MAX_CONTEXT = 7
 PLE_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -53,6 +56,21 @@ class ple_batch_desc(ctypes.Structure):
 class ple_layer_desc(ctypes.Structure):
     _fields_ = [("hash", ple_hash_desc), ("table", ple_table_desc), ("kv_weight", P), ("hidden", I32),
                 ("eps", ctypes.c_float), ("conv_weight", P), ("conv_kernel", I32), ("conv_dilation", I32)]
+
+
+class ple_w4_weight(ctypes.Structure):
+    _fields_ = [("codes", P), ("scales", P), ("zeros", P), ("tensor_scale", P), ("format", I32), ("out_dim", I32),
+                ("k_dim", I32), ("group", I32)]
+
+
+class ple_kv4_cache(ctypes.Structure):
+    _fields_ = [("k_codes", P), ("k_scales", P), ("v_codes", P), ("v_scales", P), ("k_scale", P), ("v_scale", P),
+                ("num_pages", I64), ("num_kv_heads", I32), ("page_size", I32), ("head_dim", I32), ("reserved", I32)]
+
+
+class ple_kv4_batch(ctypes.Structure):
+    _fields_ = [("query_start_loc", P), ("seq_lens", P), ("page_table", P), ("num_tokens", I64), ("num_reqs", I32),
+                ("table_width", I32), ("max_request_tokens", I32), ("max_seq_len", I32)]
 
 
 _PROTOS = {
@@ -88,6 +106,16 @@ _PROTOS = {
     "ple_version": (ctypes.c_char_p, []),
 }
 
+_CACHE, _BATCH = ctypes.POINTER(ple_kv4_cache), ctypes.POINTER(ple_kv4_batch)
+_FP4_PROTOS = {
+    "ple_w4_linear": (ctypes.c_int, [P, I64, ctypes.POINTER(ple_w4_weight), I64, P, P]),
+    "ple_kv4_append": (ctypes.c_int, [_CACHE, _BATCH, P, I64, P, I64, P, I64, I32, P, P, I32, I32, P]),
+    "ple_kv4_read": (ctypes.c_int, [_CACHE, _BATCH, P, P, P]),
+    "ple_kv4_attention": (ctypes.c_int, [P, I64, I32, _CACHE, _BATCH, I32, ctypes.c_float, P, P, P, ctypes.c_size_t,
+                                         P]),
+    "ple_kv4_attention_workspace_bytes": (ctypes.c_size_t, [I32, _CACHE, _BATCH, I32]),
+}
+
 _lib = None
 
 
@@ -99,7 +127,7 @@ def load() -> ctypes.CDLL:
             raise RuntimeError(f"libple.so is not built ({LIB_PATH}); run "
                                "`python -m layer_embedding_lookup_amd.build` (needs hipcc)")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in _PROTOS.items():
+        for name, (res, args) in (*_PROTOS.items(), *_FP4_PROTOS.items()):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
@@ -107,9 +135,9 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
-def header_functions() -> list[str]:
-    """Names of the functions declared in include/ple.h."""
-    text = open(HEADER).read()
+def header_functions(header: str = HEADER) -> list[str]:
+    """Names of the functions declared in include/ple.h (or another header)."""
+    text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(ple_[a-z_0-9]+)\s*\(", text)))
 

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "ple.h"
+#include "ple_api.h"
 #include "ple_launch.h"
 
 using namespace ple;
@@ -20,8 +21,10 @@ using namespace ple;
 #endif
 
 namespace {
-
 thread_local char g_msg[512];
+}  // namespace
+
+namespace ple {
 
 int fail(int code, const char* fmt, ...) {
     va_list ap;
@@ -39,9 +42,6 @@ int ok() {
 int hip_fail(hipError_t e, const char* what) {
     return fail(PLE_ERR_DEVICE, "%s: %s", what, hipGetErrorString(e));
 }
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 // The current device must be gfx950 (checked once per device).
 int check_device() {
@@ -64,6 +64,10 @@ int check_device() {
     if (state[dev] < 0) return fail(PLE_ERR_UNSUPPORTED, "device %d is not gfx950", dev);
     return PLE_OK;
 }
+
+}  // namespace ple
+
+namespace {
 
 int validate_hash(const ple_hash_desc* h, HashParams* hp) {
     if (h == nullptr) return fail(PLE_ERR_INVALID_ARGUMENT, "hash descriptor is NULL");

@@ -1,0 +1,171 @@
+// New keys and values, rotated by position, into the paged 4-bit cache, and
+// back out of it.
+//
+// Bound by bytes: a token reads its q, k and v rows and writes q and 9/32 of
+// the bytes of k and v.  One block per token: the token's sines and cosines
+// are formed once, in 64 bits (positions of 10^5 and more lose the angle in
+// 32), and shared by all heads; then each lane takes chunks of 8 elements (16
+// bytes in, 4 bytes of codes out), and the two lanes of a 16-element block
+// join their maxima with one exchange.  The rotation itself is 64-bit too and
+// rounded once to fp32, so that a key next to a code's border falls on the
+// side that the definition says.
+#include "ple_fp4_launch.h"
+
+namespace ple {
+
+constexpr int kAppendThreads = 256;
+
+__device__ __forceinline__ void load8(const uint16_t* __restrict__ p, float (&v)[8]) {
+    const u32x4 w = *(const u32x4*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+
+// e4m3 code of a finite or NaN value already clamped to 448, round to nearest even.
+__device__ __forceinline__ uint32_t e4m3_code(float v) {
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v, 0.0f, 0, false) & 0xFFu;
+}
+
+// e2m1 code of t: nearest of 0 .5 1 1.5 2 3 4 6, ties to the even code (zero for NaN).
+__device__ __forceinline__ uint32_t e2m1_code(float t) {
+    const float a = fabsf(t);
+    const uint32_t c = (uint32_t)(a > 0.25f) + (uint32_t)(a >= 0.75f) + (uint32_t)(a > 1.25f) +
+                       (uint32_t)(a >= 1.75f) + (uint32_t)(a > 2.5f) + (uint32_t)(a >= 3.5f) + (uint32_t)(a > 5.0f);
+    return c | (__float_as_uint(t) >> 31 << 3);
+}
+
+__global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArgs a) {
+    __shared__ double2 turn[128];  // cos, sin of the token's angles
+    const int64_t t = blockIdx.x;
+    const int D = a.cache.head_dim, per_head = D / 8, half = a.rot_dim / 2;
+    int r;
+    const int pos = kv4_position(a.cache, a.batch, t, r);
+    for (int i = threadIdx.x; i < half; i += kAppendThreads) {
+        // a position below 2^30 times a 24-bit frequency is exact in 64 bits
+        const double angle = (double)(pos < 0 ? 0 : pos) * (double)a.inv_freq[i];
+        double sn, cs;
+        sincos(angle, &sn, &cs);
+        turn[i] = make_double2(cs, sn);
+    }
+    __syncthreads();
+    const int32_t* row = a.batch.page_table + (int64_t)r * a.batch.table_width;
+    const int nq = a.num_q_heads * per_head, nk = a.cache.num_kv_heads * per_head;
+    for (int c = threadIdx.x; c < nq + 2 * nk; c += kAppendThreads) {
+        const int which = c < nq ? 0 : (c < nq + nk ? 1 : 2);
+        const int at = which == 0 ? c : (which == 1 ? c - nq : c - nq - nk);
+        const int head = at / per_head, d0 = (at - head * per_head) * 8;
+        const uint16_t* src = a.src[which] + t * a.stride[which] + head * D;
+        float v[8];
+        load8(src + d0, v);
+        if (which != 2 && d0 < a.rot_dim) {
+            if (a.interleaved) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const double2 w = turn[d0 / 2 + i];
+                    const double x = v[2 * i], y = v[2 * i + 1];
+                    v[2 * i] = (float)(x * w.x - y * w.y);
+                    v[2 * i + 1] = (float)(y * w.x + x * w.y);
+                }
+            } else {
+                const bool upper = d0 >= half;  // half is a multiple of 8
+                float o[8];
+                load8(src + (upper ? d0 - half : d0 + half), o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const double2 w = turn[(upper ? d0 - half : d0) + i];
+                    const double x = v[i], y = o[i];
+                    v[i] = (float)(upper ? x * w.x + y * w.y : x * w.x - y * w.y);
+                }
+            }
+        }
+        if (which == 0) {
+            u32x4 o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            *(u32x4*)(a.q_out + (t * a.num_q_heads + head) * D + d0) = o;
+            continue;
+        }
+        // chunks 2b and 2b+1 of a head are lanes 2b and 2b+1 of a wave: nq and nk are even
+        float top = 0.f;
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            top = fmaxf(top, fabsf(v[i]));
+            nan |= v[i] != v[i];
+        }
+        if (nan) top = __builtin_nanf("");
+        const float other = __shfl_xor(top, 1, kWave);
+        top = top != top || other != other ? __builtin_nanf("") : fmaxf(top, other);
+        const float g = (which == 1 ? a.cache.k_scale : a.cache.v_scale)[head];
+        float s = top / (6.0f * g);
+        s = s > 448.f ? 448.f : s;  // (keeps a NaN)
+        const uint32_t sc = e4m3_code(s);
+        float step = __builtin_amdgcn_cvt_pk_f32_fp8((int)sc, false)[0] * g;
+        step = step > 0.f ? step : __builtin_inff();
+        uint32_t codes = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) codes |= e2m1_code(v[i] / step) << (4 * i);
+        if (pos < 0) continue;
+        const int grp = kv4_group(a.cache, row, head, pos >> 4);
+        if (grp < 0) continue;
+        const int place = pos & 15;
+        uint8_t* cd = (which == 1 ? a.cache.k_codes : a.cache.v_codes) + (int64_t)grp * (8 * D) + place * (D / 2) + d0 / 2;
+        *(uint32_t*)cd = codes;
+        if ((d0 & 8) == 0)
+            ((which == 1 ? a.cache.k_scales : a.cache.v_scales) + (int64_t)grp * D)[d0 + place] = (uint8_t)sc;
+    }
+}
+
+hipError_t launch_kv4_append(const Kv4AppendArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(kv4_append_kernel, dim3((unsigned)a.batch.num_tokens), dim3(kAppendThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+// One block per token; a lane turns 4 bytes of codes into 16 bytes of bf16.
+__global__ __launch_bounds__(kAppendThreads) void kv4_read_kernel(ple_kv4_cache cache, ple_kv4_batch batch,
+                                                                  uint16_t* __restrict__ k_out,
+                                                                  uint16_t* __restrict__ v_out) {
+    const int64_t t = blockIdx.x;
+    const int D = cache.head_dim, per_head = D / 8;
+    int r;
+    const int pos = kv4_position(cache, batch, t, r);
+    const int32_t* row = batch.page_table + (int64_t)r * batch.table_width;
+    const int nk = cache.num_kv_heads * per_head;
+    for (int c = threadIdx.x; c < 2 * nk; c += kAppendThreads) {
+        const bool val = c >= nk;
+        const int at = val ? c - nk : c;
+        const int head = at / per_head, d0 = (at - head * per_head) * 8;
+        const int grp = pos < 0 ? -1 : kv4_group(cache, row, head, pos >> 4);
+        u32x4 o = {0u, 0u, 0u, 0u};
+        if (grp >= 0) {
+            const int place = pos & 15;
+            const uint32_t w =
+                *(const uint32_t*)((val ? cache.v_codes : cache.k_codes) + (int64_t)grp * (8 * D) + place * (D / 2) + d0 / 2);
+            const uint8_t sc = ((val ? cache.v_scales : cache.k_scales) + (int64_t)grp * D)[(d0 & ~15) + place];
+            const float s = __builtin_amdgcn_cvt_pk_f32_fp8((int)sc, false)[0];
+            const float g = (val ? cache.v_scale : cache.k_scale)[head];
+            const f32x2 e0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+            const f32x2 e1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+            const f32x2 e2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+            const f32x2 e3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+            // code * block scale is exact in fp32
+            o[0] = pack_bf16x2(e0[0] * s * g, e0[1] * s * g);
+            o[1] = pack_bf16x2(e1[0] * s * g, e1[1] * s * g);
+            o[2] = pack_bf16x2(e2[0] * s * g, e2[1] * s * g);
+            o[3] = pack_bf16x2(e3[0] * s * g, e3[1] * s * g);
+        }
+        *(u32x4*)((val ? v_out : k_out) + (t * cache.num_kv_heads + head) * D + d0) = o;
+    }
+}
+
+hipError_t launch_kv4_read(const ple_kv4_cache& cache, const ple_kv4_batch& batch, uint16_t* k_out, uint16_t* v_out,
+                           hipStream_t s) {
+    hipLaunchKernelGGL(kv4_read_kernel, dim3((unsigned)batch.num_tokens), dim3(kAppendThreads), 0, s, cache, batch,
+                       k_out, v_out);
+    return hipGetLastError();
+}
+
+}  // namespace ple
