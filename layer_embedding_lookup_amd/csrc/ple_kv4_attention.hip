@@ -34,6 +34,7 @@ namespace ple {
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * kWave;
 constexpr int kTile = 64;  // cache tokens of a tile
+constexpr int kMostSplits = 1024;
 // Weights are 2^(s - m + kWeightShift): fp16 keeps them above 2^-24, so tokens down to 2^-32 of the heaviest one count.
 constexpr float kWeightShift = 8.0f;
 
@@ -444,12 +445,12 @@ PLE_ATTN_KERNEL(256, 1)
 PLE_ATTN_KERNEL(256, 2)
 #undef PLE_ATTN_KERNEL
 
-// Joins the splits of a row: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top).  One wave a row.
+// Joins the splits of a row: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top).  One block a row, a wave
+// taking every fourth split.
 __global__ __launch_bounds__(kAttnThreads) void kv4_attention_join_kernel(Kv4AttentionArgs a) {
-    const int64_t orow = (int64_t)blockIdx.x * kAttnWaves + (threadIdx.x >> 6);
-    const int64_t rows = a.batch.num_tokens * a.num_q_heads;
-    if (orow >= rows) return;
-    const int lane = threadIdx.x & 63;
+    __shared__ float weight[kMostSplits], sum[kAttnWaves][256];
+    const int64_t orow = blockIdx.x, rows = a.batch.num_tokens * a.num_q_heads;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t t = orow / a.num_q_heads;
     const int hq = (int)(orow - t * a.num_q_heads), head = hq / a.group;
     const int r = find_request(a.batch.query_start_loc, a.batch.num_reqs, t);
@@ -463,31 +464,42 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_attention_join_kernel(Kv4Att
     if (splits == 1) return;
     const int D = a.cache.head_dim;
     const float* lse = a.part + rows * a.splits * D + orow * a.splits;
-    float top = -__builtin_inff();
-    bool nan = false;
-    for (int s = lane; s < splits; s += kWave) {
-        const float x = lse[s];
-        nan |= x != x;
-        top = fmaxf(top, x);
-    }
+    // every wave for itself: the largest lse, and the sum of the weights
+    float top = -__builtin_inff(), total = 0.f;
+    for (int s = lane; s < splits; s += kWave) top = fmaxf(top, lse[s]);
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-    nan = __ballot(nan) != 0;
-    float total = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < splits; ++s) {
-        const float wt = lse[s] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(lse[s] - top);
-        total += wt;
-        const float* src = a.part + (orow * a.splits + s) * D;
+    for (int s = lane; s < splits; s += kWave) {
+        const float x = lse[s], v = x == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(x - top);  // NaN stays
+        total += v;
+        if (wave == 0) weight[s] = v;
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(total, d, kWave);
+    __syncthreads();
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    const float* src = a.part + orow * a.splits * D;
+    const int per = D / kWave;  // elements of a lane
+#pragma unroll 4
+    for (int s = wave; s < splits; s += kAttnWaves) {
+        const float wt = weight[s];
+        const float* p = src + (int64_t)s * D + lane;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (e * kWave < D && wt != 0.f) v[e] += src[e * kWave + lane] * wt;
+            if (e < per) v[e] = fmaf(p[e * kWave], wt, v[e]);
     }
-    const float f = nan ? __builtin_nanf("") : (total == 0.f ? 0.f : a.cache.v_scale[head] / total);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        if (e * kWave < D) a.out[orow * D + e * kWave + lane] = (uint16_t)pack_bf16x2(v[e] * f, 0.f);
-    if (a.lse != nullptr && lane == 0)
-        a.lse[orow] = nan ? __builtin_nanf("") : (total == 0.f ? -__builtin_inff() : (top + log2f(total)) * 0.693147180559945309f);
+        if (e < per) sum[wave][e * kWave + lane] = v[e];
+    __syncthreads();
+    if ((int)threadIdx.x < D) {
+        const int d = threadIdx.x;
+        const float f = total == 0.f ? 0.f : a.cache.v_scale[head] / total;
+        const float x = (sum[0][d] + sum[1][d]) + (sum[2][d] + sum[3][d]);
+        a.out[orow * D + d] = (uint16_t)pack_bf16x2(x * f, 0.f);
+    }
+    if (a.lse != nullptr && threadIdx.x == 0)
+        a.lse[orow] = total == 0.f ? -__builtin_inff() : (top + log2f(total)) * 0.693147180559945309f;
 }
 
 void plan_kv4_attention(Kv4AttentionArgs& a) {
@@ -509,7 +521,7 @@ void plan_kv4_attention(Kv4AttentionArgs& a) {
     int64_t splits = blocks > 0 ? (1024 + blocks - 1) / blocks : 1;
     const int64_t most_splits = (len + kTile * kAttnWaves - 1) / (kTile * kAttnWaves);
     splits = splits < most_splits ? splits : most_splits;
-    splits = splits < 1 ? 1 : splits;
+    splits = splits < 1 ? 1 : (splits < kMostSplits - 1 ? splits : kMostSplits - 1);
     int64_t chunk = (len + splits - 1) / splits;
     chunk = (chunk + kTile * kAttnWaves - 1) / (kTile * kAttnWaves) * (kTile * kAttnWaves);
     // a range starts at a multiple of 16, up to 15 tokens before the first that is seen
@@ -540,8 +552,7 @@ hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits <= 1) return e;
     const int64_t rows = a.batch.num_tokens * a.num_q_heads;
-    hipLaunchKernelGGL(kv4_attention_join_kernel, dim3((unsigned)((rows + kAttnWaves - 1) / kAttnWaves)),
-                       dim3(kAttnThreads), 0, s, a);
+    hipLaunchKernelGGL(kv4_attention_join_kernel, dim3((unsigned)rows), dim3(kAttnThreads), 0, s, a);
     return hipGetLastError();
 }
 

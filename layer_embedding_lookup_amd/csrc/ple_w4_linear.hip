@@ -67,125 +67,396 @@ struct W4Args {
     uint16_t* out;
 };
 
-// MT tiles of 16 tokens; G: 16 for NVFP4, else the INT4 group.
-template <int MT, int G, int WAVES>
+// A step of one wave: 128 inputs of NT x 16 features and of MT x 16 tokens, as loaded.
+template <int MT, int NT, int G>
+struct W4Step {
+    u32x4 w[NT];
+    uint32_t scale[NT][G == 16 ? 1 : 128 / G];  // NVFP4: the lane's two block scales; INT4: bf16 scale | zero point << 16
+    u32x4 x[MT][4];
+};
+
+// MT tiles of 16 tokens, NT tiles of 16 features; G: 16 for NVFP4, else the INT4 group; DEPTH steps are loaded
+// before the first of them is used.
+template <int MT, int NT, int G, int WAVES, int DEPTH>
 __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
     constexpr bool kNv = G == 16;
-    __shared__ __align__(16) float join[WAVES][MT][64][4];
+    constexpr int kGroups = kNv ? 1 : 128 / G;  // groups of a step
+    constexpr int kJoin = WAVES < 4 ? WAVES : 4;  // waves whose sums are in LDS at once
+    __shared__ __align__(16) float join[kJoin][MT * NT][64][4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int n = lane & 15, g = lane >> 4;
-    const int tiles_o = (a.O + 15) / 16, o0 = (blockIdx.x % tiles_o) * 16;
-    const int o = min(o0 + n, a.O - 1);  // features past the end repeat the last and are not stored
+    const int tiles_o = (a.O + 16 * NT - 1) / (16 * NT), o0 = (blockIdx.x % tiles_o) * (16 * NT);
     const int64_t t0 = (int64_t)(blockIdx.x / tiles_o) * (16 * MT);
-    const uint8_t* wrow = a.codes + (int64_t)o * (a.K / 2) + g * 16;
-    const uint8_t* nvs = (const uint8_t*)a.scales + (int64_t)o * (a.K / 16) + g * 2;
-    const uint16_t* i4s = (const uint16_t*)a.scales + (int64_t)o * (a.K / (kNv ? 32 : G));
-    const uint8_t* i4z = a.zeros == nullptr ? nullptr : a.zeros + (int64_t)o * (a.K / (kNv ? 32 : G));
+    const int groups = a.K / (kNv ? 16 : G);
+    // features past the end repeat the last one, tokens past it are zeros (and not fetched: for a single token the
+    // inputs' fetches would outweigh the codes'); neither is stored
+    const uint8_t* wrow[NT];
+    int64_t srow[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int64_t o = min(o0 + nt * 16 + n, a.O - 1);
+        wrow[nt] = a.codes + o * (a.K / 2) + g * 16;
+        srow[nt] = o * groups;
+    }
     const uint16_t* xrow[MT];
+    bool xlive[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const int64_t t = t0 + mt * 16 + n;  // tokens past the end repeat the last and are not stored
-        xrow[mt] = a.x + (t < a.T ? t : a.T - 1) * a.x_stride;
+        const int64_t t = t0 + mt * 16 + n;
+        xlive[mt] = t < a.T;
+        xrow[mt] = a.x + t * a.x_stride;
     }
-    f32x4 acc[MT];
+    f32x4 acc[MT][NT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    for (int k0 = wave * 128; k0 < a.K; k0 += WAVES * 128) {
-        // the last step may be short: lanes past K take zeros
+    using Step = W4Step<MT, NT, G>;
+    const u32x4 zero4 = {0u, 0u, 0u, 0u};
+    // Lanes past K take zeros: NVFP4 products vanish, INT4 steps stop at the last group (K is a multiple of it).
+    auto load = [&](int k0, Step& s) {
         const bool in = k0 + g * 32 < a.K;
-        u32x4 w = in ? *(const u32x4*)(wrow + k0 / 2) : u32x4{0u, 0u, 0u, 0u};
-        if constexpr (kNv) {
-            const uint32_t sc = in ? *(const uint16_t*)(nvs + k0 / 16) : 0u;
-            const f32x2 s = __builtin_amdgcn_cvt_pk_f32_fp8((int)sc, false);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                BFrag f;
-                nvfp4_frag(w[j], s[j >> 1], f);
+        for (int nt = 0; nt < NT; ++nt) {
+            s.w[nt] = in ? *(const u32x4*)(wrow[nt] + k0 / 2) : zero4;
+            if constexpr (kNv) {
+                s.scale[nt][0] = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
+            } else {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    BFrag xf;
-                    xf.q = in ? *(const u32x4*)(xrow[mt] + k0 + g * 32 + j * 8) : u32x4{0u, 0u, 0u, 0u};
-                    acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf.v, f.v, acc[mt], 0, 0, 0);
-                }
-            }
-        } else {
-            transpose4(w);  // word j: inputs k0 + 32 j + 8 g ..
-            f32x4 part[MT];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = k0 + 32 * j;
-                const bool live = k < a.K;  // the same for the whole wave
-                const int at = live ? k / G : 0;
-                const float z = i4z == nullptr ? 8.f : (float)i4z[at];
-                BFrag f;
-                int4_frag(w[j], z, f);
-                if ((j * 32) % G == 0)
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) part[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-                if (live)
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        BFrag xf;
-                        xf.q = *(const u32x4*)(xrow[mt] + k + g * 8);
-                        part[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf.v, f.v, part[mt], 0, 0, 0);
+                for (int j = 0; j < kGroups; ++j) {
+                    const int at = k0 / G + j;
+                    uint32_t v = 8u << 16;
+                    if (at < groups) {
+                        v = ((const uint16_t*)a.scales)[srow[nt] + at];
+                        v |= (a.zeros == nullptr ? 8u : (uint32_t)a.zeros[srow[nt] + at]) << 16;
                     }
-                if ((j * 32 + 32) % G == 0 && live) {
-                    const float s = bf16_lo(i4s[at]);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[mt][e] = fmaf(part[mt][e], s, acc[mt][e]);
+                    s.scale[nt][j] = v;
                 }
             }
         }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = kNv ? k0 + g * 32 + j * 8 : k0 + j * 32 + g * 8;
+                s.x[mt][j] = k < a.K && xlive[mt] ? *(const u32x4*)(xrow[mt] + k) : zero4;
+            }
+    };
+    auto use = [&](int k0, Step& s) {
+        if constexpr (kNv) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const f32x2 sc = __builtin_amdgcn_cvt_pk_f32_fp8((int)s.scale[nt][0], false);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    BFrag f;
+                    nvfp4_frag(s.w[nt][j], sc[j >> 1], f);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, s.x[mt][j]), f.v,
+                                                                              acc[mt][nt], 0, 0, 0);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                transpose4(s.w[nt]);  // word j: inputs k0 + 32 j + 8 g ..
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) {
+                    const float z = (float)(s.scale[nt][i] >> 16), sc = bf16_lo(s.scale[nt][i]);
+                    f32x4 part[MT];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) part[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = i * (G / 32); j < (i + 1) * (G / 32); ++j) {
+                        BFrag f;
+                        int4_frag(s.w[nt][j], z, f);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            part[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, s.x[mt][j]),
+                                                                               f.v, part[mt], 0, 0, 0);
+                    }
+                    // (groups past K hold zero inputs and a zero scale)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[mt][nt][e] = fmaf(part[mt][e], sc, acc[mt][nt][e]);
+                }
+            }
+        }
+    };
+    Step st[DEPTH];
+    for (int k0 = wave * 128; k0 < a.K; k0 += DEPTH * WAVES * 128) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) load(k0 + d * WAVES * 128, st[d]);
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) use(k0 + d * WAVES * 128, st[d]);
     }
 
+    // waves kJoin .. hand their sums to the first kJoin, whose sums are then added up
+    for (int w0 = WAVES - kJoin; w0 > 0; w0 -= kJoin) {
+        if (wave >= w0 && wave < w0 + kJoin)
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) *(f32x4*)join[wave][mt][lane] = acc[mt];
+            for (int i = 0; i < MT * NT; ++i) *(f32x4*)join[wave - w0][i][lane] = acc[i / NT][i % NT];
+        __syncthreads();
+        if (wave < kJoin)
+#pragma unroll
+            for (int i = 0; i < MT * NT; ++i) acc[i / NT][i % NT] += *(const f32x4*)join[wave][i][lane];
+        __syncthreads();
+    }
+    if (wave < kJoin)
+#pragma unroll
+        for (int i = 0; i < MT * NT; ++i) *(f32x4*)join[wave][i][lane] = acc[i / NT][i % NT];
     __syncthreads();
     const float ts = kNv ? a.tensor_scale[0] : 1.f;
-    // lane (n, g) of tile mt holds feature n of tokens 4 g ..
-    for (int c = threadIdx.x; c < MT * 64; c += WAVES * kWave) {
-        const int mt = c >> 6, l = c & 63;
+    // lane (n, g) of tile (mt, nt) holds feature n of tokens 4 g ..
+    for (int c = threadIdx.x; c < MT * NT * 64; c += WAVES * kWave) {
+        const int i = c >> 6, l = c & 63;
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < WAVES; ++k) v += *(const f32x4*)join[k][mt][l];
-        const int col = o0 + (l & 15);
+        for (int k = 0; k < kJoin; ++k) v += *(const f32x4*)join[k][i][l];
+        const int col = o0 + (i % NT) * 16 + (l & 15);
         if (col < a.O)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int64_t t = t0 + mt * 16 + (l >> 4) * 4 + e;
+                const int64_t t = t0 + (i / NT) * 16 + (l >> 4) * 4 + e;
                 if (t < a.T) a.out[t * a.O + col] = (uint16_t)pack_bf16x2(v[e] * ts, 0.f);
             }
     }
 }
 
-#define PLE_W4_KERNEL(MT, G, WAVES)                                                                     \
-    __global__ __launch_bounds__(WAVES * 64) void w4_rows_##MT##_##G##_##WAVES##_kernel(W4Args a) { \
-        w4_rows_body<MT, G, WAVES>(a);                                                                  \
+// Shapes of the few-token kernel: token tiles, feature tiles, waves, steps in flight.
+#define PLE_W4_SHAPES(X) X(1, 1, 8, 4) X(2, 1, 8, 2) X(4, 2, 8, 1) X(4, 4, 8, 1)
+#define PLE_W4_KERNEL(MT, NT, G, WAVES, DEPTH)                                                                        \
+    __global__ __launch_bounds__(WAVES * 64) void w4_rows_##MT##x##NT##_##G##_kernel(W4Args a) {                      \
+        w4_rows_body<MT, NT, G, WAVES, DEPTH>(a);                                                                     \
     }
-#define PLE_W4_KERNELS(MT, WAVES) \
-    PLE_W4_KERNEL(MT, 16, WAVES) PLE_W4_KERNEL(MT, 32, WAVES) PLE_W4_KERNEL(MT, 64, WAVES) PLE_W4_KERNEL(MT, 128, WAVES)
-PLE_W4_KERNELS(1, 8)
-PLE_W4_KERNELS(2, 8)
-PLE_W4_KERNELS(4, 8)
+#define PLE_W4_KERNELS(MT, NT, WAVES, DEPTH)                                              \
+    PLE_W4_KERNEL(MT, NT, 16, WAVES, DEPTH) PLE_W4_KERNEL(MT, NT, 32, WAVES, DEPTH)       \
+    PLE_W4_KERNEL(MT, NT, 64, WAVES, DEPTH) PLE_W4_KERNEL(MT, NT, 128, WAVES, DEPTH)
+PLE_W4_SHAPES(PLE_W4_KERNELS)
+
+// ---------------------------------------------------------------------------
+// Many tokens: bound by the products.  A block of four waves holds 128 tokens
+// x 256 features, a wave 128 x 64 as 8 x 4 accumulators of 16 x 16.  The
+// inputs go through LDS in slices of 128 (two slots), shared by the waves;
+// the codes do not: each wave dequantises its own 64 features in registers,
+// once for its 128 tokens, so LDS carries the inputs alone and dequantising
+// costs half of the VALU time that the products leave.
+//
+// LDS layout of a slice: a token's 256 bytes are 16 chunks of 16 bytes, chunk
+// c at place c ^ (token % 16), so the 16 lanes of a fragment read (16 tokens,
+// one chunk) touch 16 different 16-byte banks.  Fragment j of lane (n, g)
+// takes chunk 4 g + j (NVFP4: the lane's own 16 bytes of codes) or 4 j + g
+// (INT4: words swapped, so that a fragment's inputs lie in one group).
+// ---------------------------------------------------------------------------
+constexpr int kGemmT = 128, kGemmO = 256, kGemmThreads = 256;
+constexpr int kGemmSlot = kGemmT * 256;             // bytes of a slice
+constexpr int kGemmOutRow = kGemmO * 2 + 16;        // bytes of an output row in LDS
+constexpr int kGemmLds = 2 * kGemmSlot > kGemmT * kGemmOutRow ? 2 * kGemmSlot : kGemmT * kGemmOutRow;
+
+template <int G>
+__device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
+    constexpr bool kNv = G == 16;
+    constexpr int kGroups = kNv ? 1 : 128 / G;
+    extern __shared__ __align__(16) char lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int n = lane & 15, g = lane >> 4;
+    const int tiles_t = (int)((a.T + kGemmT - 1) / kGemmT), tiles_o = (a.O + kGemmO - 1) / kGemmO;
+    // neighbouring blocks of an XCD (block number mod 8) share features, so their codes come from its L2
+    const int total = tiles_t * tiles_o;
+    int lin = blockIdx.x;
+    if ((total & 7) == 0) lin = (lin & 7) * (total >> 3) + (lin >> 3);
+    const int to = lin / tiles_t, tt = lin - to * tiles_t;
+    const int64_t t0 = (int64_t)tt * kGemmT;
+    const int o0 = to * kGemmO + wave * 64;
+    const int groups = a.K / (kNv ? 16 : G);
+    const uint8_t* wrow[4];
+    int64_t srow[4];
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+        const int64_t o = min(o0 + nt * 16 + n, a.O - 1);
+        wrow[nt] = a.codes + o * (a.K / 2) + g * 16;
+        srow[nt] = o * groups;
+    }
+    // this thread's chunks of a slice: token tid/16 + 16 i, chunk tid % 16
+    const uint16_t* xsrc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t t = t0 + (tid >> 4) + 16 * i;
+        xsrc[i] = a.x + (t < a.T ? t : a.T - 1) * a.x_stride + (tid & 15) * 8;
+    }
+    char* const xdst = lds + (tid >> 4) * 256 + ((tid & 15) ^ (tid >> 4)) * 16;
+
+    const u32x4 zero4 = {0u, 0u, 0u, 0u};
+    u32x4 w[4], xs[8];
+    uint32_t scale[4][kGroups];
+    auto load = [&](int k0) {
+        const bool in = k0 + g * 32 < a.K;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            w[nt] = in ? *(const u32x4*)(wrow[nt] + k0 / 2) : zero4;
+            if constexpr (kNv) {
+                scale[nt][0] = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
+            } else {
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) {
+                    const int at = k0 / G + j;
+                    uint32_t v = 8u << 16;
+                    if (at < groups) {
+                        v = ((const uint16_t*)a.scales)[srow[nt] + at];
+                        v |= (a.zeros == nullptr ? 8u : (uint32_t)a.zeros[srow[nt] + at]) << 16;
+                    }
+                    scale[nt][j] = v;
+                }
+            }
+        }
+        const bool xin = k0 + (tid & 15) * 8 < a.K;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xs[i] = xin ? *(const u32x4*)(xsrc[i] + k0) : zero4;
+    };
+    auto put = [&](int slot) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *(u32x4*)(xdst + slot * kGemmSlot + i * 4096) = xs[i];
+    };
+
+    f32x4 acc[8][4];
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    load(0);
+    put(0);
+    const int steps = (a.K + 127) / 128;
+    for (int st = 0; st < steps; ++st) {
+        // this slice's codes as bf16
+        BFrag f[4][4];
+        float sc[4][kGroups];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            if constexpr (kNv) {
+                const f32x2 s2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)scale[nt][0], false);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) nvfp4_frag(w[nt][j], s2[j >> 1], f[nt][j]);
+            } else {
+                u32x4 t = w[nt];
+                transpose4(t);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) int4_frag(t[j], (float)(scale[nt][j / (G / 32)] >> 16), f[nt][j]);
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) sc[nt][i] = bf16_lo(scale[nt][i]);
+            }
+        }
+        __syncthreads();  // slice st is whole; every read of the other slot is done
+        if (st + 1 < steps) load((st + 1) * 128);
+        const char* slot = lds + (st & 1) * kGemmSlot + n * 256;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+            BFrag x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = kNv ? 4 * g + j : 4 * j + g;
+                x[j].q = *(const u32x4*)(slot + mt * 4096 + ((c ^ n) * 16));
+            }
+            if constexpr (kNv) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt)
+                        acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j].v, f[nt][j].v, acc[mt][nt], 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) {
+                    f32x4 part[4];
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt) part[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = i * (G / 32); j < (i + 1) * (G / 32); ++j)
+#pragma unroll
+                        for (int nt = 0; nt < 4; ++nt)
+                            part[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j].v, f[nt][j].v, part[nt], 0, 0, 0);
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[mt][nt][e] = fmaf(part[nt][e], sc[nt][i], acc[mt][nt][e]);
+                }
+            }
+        }
+        if (st + 1 < steps) put((st + 1) & 1);
+    }
+
+    // out through LDS: lane (n, g) of tile (mt, nt) holds feature n of tokens 4 g ..
+    const float ts = kNv ? a.tensor_scale[0] : 1.f;
+    __syncthreads();
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *(uint16_t*)(lds + (mt * 16 + g * 4 + e) * kGemmOutRow + (wave * 64 + nt * 16 + n) * 2) =
+                    (uint16_t)pack_bf16x2(acc[mt][nt][e] * ts, 0.f);
+    __syncthreads();
+    const int ob = to * kGemmO;
+    if (a.O % 8 == 0) {
+        for (int c = tid; c < kGemmT * (kGemmO / 8); c += kGemmThreads) {
+            const int row = c / (kGemmO / 8), col = (c % (kGemmO / 8)) * 8;
+            if (t0 + row < a.T && ob + col < a.O)
+                *(u32x4*)(a.out + (t0 + row) * a.O + ob + col) = *(const u32x4*)(lds + row * kGemmOutRow + col * 2);
+        }
+    } else {
+        for (int c = tid; c < kGemmT * kGemmO; c += kGemmThreads) {
+            const int row = c / kGemmO, col = c % kGemmO;
+            if (t0 + row < a.T && ob + col < a.O)
+                a.out[(t0 + row) * a.O + ob + col] = *(const uint16_t*)(lds + row * kGemmOutRow + col * 2);
+        }
+    }
+}
+
+#define PLE_W4_GEMM(G)                                                                     \
+    __global__ __launch_bounds__(kGemmThreads, 1) void w4_gemm_##G##_kernel(W4Args a) { \
+        w4_gemm_body<G>(a);                                                                \
+    }
+PLE_W4_GEMM(16)
+PLE_W4_GEMM(32)
+PLE_W4_GEMM(64)
+PLE_W4_GEMM(128)
+#undef PLE_W4_GEMM
+
+template <void (*FN)(W4Args)>
+static hipError_t launch_gemm(const W4Args& a, hipStream_t s) {
+    static const hipError_t attr =
+        hipFuncSetAttribute((const void*)FN, hipFuncAttributeMaxDynamicSharedMemorySize, kGemmLds);
+    if (attr != hipSuccess) return attr;
+    const int64_t blocks = (a.T + kGemmT - 1) / kGemmT * ((a.O + kGemmO - 1) / kGemmO);
+    hipLaunchKernelGGL(FN, dim3((unsigned)blocks), dim3(kGemmThreads), kGemmLds, s, a);
+    return hipGetLastError();
+}
 
 hipError_t launch_w4_linear(const uint16_t* x, int64_t x_stride, const ple_w4_weight& w, int64_t T, uint16_t* out,
                             hipStream_t s) {
     const W4Args a = {x, x_stride, w.codes, w.scales, w.zeros, w.tensor_scale, T, w.out_dim, w.k_dim, out};
-    const int MT = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
-    const dim3 grid((unsigned)((w.out_dim + 15) / 16 * ((T + 16 * MT - 1) / (16 * MT))));
-#define PLE_W4_LAUNCH(M, GG) \
-    if (MT == M && w.group == GG) hipLaunchKernelGGL(w4_rows_##M##_##GG##_8_kernel, grid, dim3(512), 0, s, a)
-#define PLE_W4_LAUNCHES(M) \
-    PLE_W4_LAUNCH(M, 16);  \
-    PLE_W4_LAUNCH(M, 32);  \
-    PLE_W4_LAUNCH(M, 64);  \
-    PLE_W4_LAUNCH(M, 128)
-    PLE_W4_LAUNCHES(1);
-    PLE_W4_LAUNCHES(2);
-    PLE_W4_LAUNCHES(4);
+    // the wide tiles where they give enough blocks
+    if (T > 64 && (T + kGemmT - 1) / kGemmT * ((w.out_dim + kGemmO - 1) / kGemmO) >= 128) {
+        switch (w.group) {
+            case 16: return launch_gemm<w4_gemm_16_kernel>(a, s);
+            case 32: return launch_gemm<w4_gemm_32_kernel>(a, s);
+            case 64: return launch_gemm<w4_gemm_64_kernel>(a, s);
+            default: return launch_gemm<w4_gemm_128_kernel>(a, s);
+        }
+    }
+    const int mt = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
+    const int nt = mt < 4 ? 1 : ((T + 63) / 64 * ((w.out_dim + 63) / 64) >= 192 ? 4 : 2);
+    const unsigned blocks = (unsigned)((w.out_dim + 16 * nt - 1) / (16 * nt) * ((T + 16 * mt - 1) / (16 * mt)));
+#define PLE_W4_LAUNCH(MT, NT, G, WAVES) \
+    if (mt == MT && nt == NT && w.group == G)  \
+        hipLaunchKernelGGL(w4_rows_##MT##x##NT##_##G##_kernel, dim3(blocks), dim3(WAVES * 64), 0, s, a);
+#define PLE_W4_LAUNCHES(MT, NT, WAVES, DEPTH)                                     \
+    PLE_W4_LAUNCH(MT, NT, 16, WAVES) PLE_W4_LAUNCH(MT, NT, 32, WAVES)             \
+    PLE_W4_LAUNCH(MT, NT, 64, WAVES) PLE_W4_LAUNCH(MT, NT, 128, WAVES)
+    PLE_W4_SHAPES(PLE_W4_LAUNCHES)
     return hipGetLastError();
 }
 

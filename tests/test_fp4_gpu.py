@@ -47,7 +47,8 @@ FORMATS = [("nvfp4", 16, False), ("int4", 32, False), ("int4", 64, True), ("int4
 @pytest.mark.parametrize("fmt,G,zeros", FORMATS)
 @pytest.mark.parametrize("T,O,K", [(1, 1, 128), (1, 300, 512), (2, 17, 384), (5, 515, 1152), (16, 48, 256),
                                    (17, 100, 640), (33, 333, 1280), (64, 130, 512), (65, 257, 896), (129, 65, 384),
-                                   (200, 270, 1024), (257, 520, 2048), (600, 1031, 640), (1024, 2048, 512)])
+                                   (200, 270, 1024), (257, 520, 2048), (600, 1031, 640), (1024, 2048, 512), (2051, 2053, 384),
+                                   (900, 4096, 1152)])
 def test_linear(fmt, G, zeros, T, O, K):
     print(f"linear {fmt} G={G} T={T} O={O} K={K}", flush=True)
     g = gen(T * 7 + O + K)
