@@ -68,6 +68,16 @@ __device__ __forceinline__ int attn_splits(const Kv4AttentionArgs& a, const Attn
     return max(1, min(s, a.splits));
 }
 
+// Request, key head and query tile of a block.  Blocks of one request and head are a multiple of the pairs apart, so
+// with the usual 8 heads they run on one XCD and share its L2; the tiles with the most to see come first.
+__device__ __forceinline__ void attn_block(const Kv4AttentionArgs& a, int& r, int& head, int& tile) {
+    const int heads = a.cache.num_kv_heads, pairs = a.batch.num_reqs * heads;
+    const int back = blockIdx.x / pairs, pair = blockIdx.x - back * pairs;
+    tile = a.tiles - 1 - back;
+    r = pair / heads;
+    head = pair - r * heads;
+}
+
 __device__ __forceinline__ f16x2 fp4_pair(uint32_t w, int byte) {
     switch (byte) {
         case 0: return __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
@@ -100,40 +110,25 @@ struct AttnShape {
     static constexpr int LDS = WAVE_LDS * kAttnWaves > JOIN_LDS ? WAVE_LDS * kAttnWaves : JOIN_LDS;
 };
 
+// The queries of MT x 16 rows from row0 on: lane (n, g) holds, of row 16 mt + n, the elements that its key codes
+// meet (q), what turns the row's products into base-2 exponents (qs), and the tokens it sees.
 template <int D, int MT>
-__device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
-    using Sh = AttnShape<D>;
-    __shared__ __align__(16) char lds[Sh::LDS];
-    __shared__ float join_m[kAttnWaves][16], join_l[kAttnWaves][16];
-    const int heads = a.cache.num_kv_heads;
-    const int pair = blockIdx.x / a.tiles, tile = blockIdx.x - pair * a.tiles;
-    const int r = pair / heads, head = pair - r * heads;
-    const int split = blockIdx.y;
-    AttnTile w;
-    if (!attn_tile(a, r, tile, w)) return;
-    const int splits = attn_splits(a, w);
-    if (split >= splits) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int n = lane & 15, g = lane >> 4;
-    const int begin = w.lo + split * a.chunk;
-    const int end = split == splits - 1 ? w.hi : min(w.hi, begin + a.chunk);
+__device__ __forceinline__ void attn_queries(const Kv4AttentionArgs& a, const AttnTile& w, int row0, int head, int begin,
+                                             int end, f16x8 (&q)[MT][D / 32], float (&qs)[MT], int (&see_lo)[MT],
+                                             int (&see_hi)[MT]) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int before = w.len - w.n;
-
-    // queries: lane (n, g) holds, of row 16 mt + n, the elements that its key codes meet
-    f16x8 q[MT][Sh::KS];
-    float qs[MT];        // what turns a row's products into base-2 exponents
-    int see_lo[MT], see_hi[MT];
     const float base = a.scale * 1.44269504088896341f * a.cache.k_scale[head];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const int row = w.row0 + mt * 16 + n;
+        const int row = row0 + mt * 16 + n;
         const bool live = row < w.row1;
         const int i = row / a.group, hq = head * a.group + (row - i * a.group);
         const uint16_t* src = a.q + (w.first + i) * a.q_stride + hq * D;
-        u32x4 raw[Sh::KS];
+        u32x4 raw[D / 32];
         float top = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < Sh::KS; ++ks) {
+        for (int ks = 0; ks < D / 32; ++ks) {
             // D = 64: 16 elements a lane; else 32 elements of each 128
             const int d = D == 64 ? g * 16 + ks * 8 : (ks / 4) * 128 + g * 32 + (ks % 4) * 8;
             raw[ks] = live ? *(const u32x4*)(src + d) : u32x4{0u, 0u, 0u, 0u};
@@ -149,9 +144,11 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
         // 2^(14 - exponent of top), within fp32 for every bf16 top
         const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 127, -110), 127) : 14;
         const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-        qs[mt] = base * __uint_as_float((uint32_t)(max(e - 14 + 127, 1)) << 23);
+        // (never zero: a masked product, -inf, times it has to stay -inf)
+        const float back = base * __uint_as_float((uint32_t)(max(e - 14 + 127, 1)) << 23);
+        qs[mt] = back < 1.17549435e-38f ? 1.17549435e-38f : back;
 #pragma unroll
-        for (int ks = 0; ks < Sh::KS; ++ks)
+        for (int ks = 0; ks < D / 32; ++ks)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 q[mt][ks][2 * j] = (_Float16)(bf16_lo(raw[ks][j]) * up);
@@ -162,9 +159,76 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
         see_hi[mt] = live ? min(end, p + 1) : end;
         see_lo[mt] = live ? max(begin, a.window > 0 ? p - a.window + 1 : 0) : begin;
     }
+}
+
+// The weights of one tile for a row: s (products, lane (n, g) holding tokens tg .. tg + 15) becomes the fp16 weights
+// p; m, l and o (the row's running maximum, sum and outputs) move on.  `some`: not every row sees the whole tile.
+template <int NB>
+__device__ __forceinline__ void attn_softmax(f32x4 (&s)[4], float qs, bool some, bool bad, int tg, int see_lo, int see_hi,
+                                             float& m, float& l, f32x4 (&o)[NB], Frag (&p)[2]) {
+    if (some) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int tok = tg + 4 * i + e;
+                if (bad || tok < see_lo || tok >= see_hi) s[i][e] = -__builtin_inff();
+            }
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i][e]);
+    top = fmaxf(top, __shfl_xor(top, 16, kWave));
+    top = fmaxf(top, __shfl_xor(top, 32, kWave));
+    const float mn = fmaxf(m, top * qs);  // (qs > 0)
+    if (__ballot(mn > m) != 0) {
+        const float by = m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+        l *= by;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) o[b] *= by;
+        m = mn;
+    }
+    const float sub = m == -__builtin_inff() ? 0.f : kWeightShift - m;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const float x = __builtin_amdgcn_exp2f(fmaf(s[i][e], qs, sub));
+            const float y = __builtin_amdgcn_exp2f(fmaf(s[i][e + 1], qs, sub));
+            sum += x + y;
+            p[i >> 1].p[(i & 1) * 2 + e / 2] = f16x2{(_Float16)x, (_Float16)y};
+        }
+    l += sum;
+}
+
+template <int D, int MT>
+__device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
+    using Sh = AttnShape<D>;
+    __shared__ __align__(16) char lds[Sh::LDS];
+    __shared__ float join_m[kAttnWaves][16], join_l[kAttnWaves][16];
+    const int split = blockIdx.y;
+    int r, head, tile;
+    attn_block(a, r, head, tile);
+    AttnTile w;
+    if (!attn_tile(a, r, tile, w)) return;
+    const int splits = attn_splits(a, w);
+    if (split >= splits) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = lane & 15, g = lane >> 4;
+    const int begin = w.lo + split * a.chunk;
+    const int end = split == splits - 1 ? w.hi : min(w.hi, begin + a.chunk);
+
+    f16x8 q[MT][Sh::KS];
+    float qs[MT];
+    int see_lo[MT], see_hi[MT];
+    attn_queries<D, MT>(a, w, w.row0, head, begin, end, q, qs, see_lo, see_hi);
 
     f32x4 o[MT][Sh::NB];
     float m[MT], l[MT];
+    uint32_t nan_blocks[MT] = {};  // element blocks of the row that a NaN value makes NaN
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         m[mt] = -__builtin_inff();
@@ -260,12 +324,9 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
             *(u32x2*)(dst + 8) = u32x2{vraw[j][2], vraw[j][3]};
         }
         const bool whole = t0 >= w.first_seen && __ballot(bad) == 0 && t0 + kTile <= end;
-        bool all[MT], every = whole;
+        bool every = whole;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            all[mt] = whole && t0 >= see_lo[mt] && t0 + kTile <= see_hi[mt];
-            every = every && all[mt];
-        }
+        for (int mt = 0; mt < MT; ++mt) every = every && t0 >= see_lo[mt] && t0 + kTile <= see_hi[mt];
         // A NaN value would reach, as 0 * NaN, the rows that do not see its token.  Where some row does not see the
         // whole tile, NaN scales enter as zeros and go to the rows that do see them by hand.
         uint32_t nan_scales[D / 64] = {};
@@ -291,44 +352,11 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
             }
         }
 
-        // softmax: lane (n, g) holds tokens 16 g .. 16 g + 15 of its row, in order
+        // lane (n, g) holds tokens 16 g .. 16 g + 15 of its row, in order
         Frag p[MT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            float top = -__builtin_inff();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = s[mt][i][e] * qs[mt];
-                    const int tok = tg + 4 * i + e;
-                    if (!all[mt] && (bad || tok < see_lo[mt] || tok >= see_hi[mt])) x = -__builtin_inff();
-                    s[mt][i][e] = x;
-                    top = fmaxf(top, x);
-                }
-            top = fmaxf(top, __shfl_xor(top, 16, kWave));
-            top = fmaxf(top, __shfl_xor(top, 32, kWave));
-            const float mn = fmaxf(m[mt], top);
-            if (__ballot(mn > m[mt]) != 0) {
-                const float by = m[mt] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m[mt] - mn);
-                l[mt] *= by;
-#pragma unroll
-                for (int b = 0; b < Sh::NB; ++b) o[mt][b] *= by;
-                m[mt] = mn;
-            }
-            const float sub = m[mt] == -__builtin_inff() ? 0.f : m[mt] - kWeightShift;
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const float x = __builtin_amdgcn_exp2f(s[mt][i][e] - sub);
-                    const float y = __builtin_amdgcn_exp2f(s[mt][i][e + 1] - sub);
-                    sum += x + y;
-                    p[mt][i >> 1].p[(i & 1) * 2 + e / 2] = f16x2{(_Float16)x, (_Float16)y};
-                }
-            l[mt] += sum;
-        }
+        for (int mt = 0; mt < MT; ++mt)
+            attn_softmax<Sh::NB>(s[mt], qs[mt], some, bad, tg, see_lo[mt], see_hi[mt], m[mt], l[mt], o[mt], p[mt]);
 
         // O^T += V^T P^T
 #pragma unroll
@@ -361,9 +389,7 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
                         if ((which >> (8 * e + 7) & 1) == 0) continue;
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                            for (int b = 0; b < Sh::NB; ++b)
-                                if (b == at >> 4 && tok >= see_lo[mt] && tok < see_hi[mt]) o[mt][b] += __builtin_nanf("");
+                            if (tok >= see_lo[mt] && tok < see_hi[mt]) nan_blocks[mt] |= 1u << (at >> 4);
                     }
                 }
         }
@@ -384,6 +410,8 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
         float* jo = (float*)lds + (wave * 16 + n) * Sh::OROW;
 #pragma unroll
         for (int b = 0; b < Sh::NB; ++b) *(f32x4*)(jo + b * 16 + g * 4) = o[mt][b];
+        for (uint32_t left = nan_blocks[mt]; left != 0; left &= left - 1)
+            *(f32x4*)(jo + __builtin_ctz(left) * 16 + g * 4) = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
         __syncthreads();
         // 16 threads a row, each with D/16 elements
         const int row = threadIdx.x >> 4, part = threadIdx.x & 15;
@@ -431,29 +459,285 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
     }
 }
 
-#define PLE_ATTN_KERNEL(D, MT)                                                                                  \
-    __global__ __launch_bounds__(kAttnThreads) void kv4_attention_##D##_##MT##_kernel(Kv4AttentionArgs a) {     \
+#define PLE_ATTN_KERNEL(D, MT, OCC)                                                                                \
+    __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_##D##_##MT##_kernel(Kv4AttentionArgs a) { \
         attn_body<D, MT>(a);                                                                                    \
     }
-PLE_ATTN_KERNEL(64, 1)
-PLE_ATTN_KERNEL(64, 2)
-PLE_ATTN_KERNEL(64, 4)
-PLE_ATTN_KERNEL(128, 1)
-PLE_ATTN_KERNEL(128, 2)
-PLE_ATTN_KERNEL(128, 4)
-PLE_ATTN_KERNEL(256, 1)
-PLE_ATTN_KERNEL(256, 2)
+PLE_ATTN_KERNEL(64, 1, 3)
+PLE_ATTN_KERNEL(64, 2, 2)
+PLE_ATTN_KERNEL(64, 4, 2)
+PLE_ATTN_KERNEL(128, 1, 3)
+PLE_ATTN_KERNEL(128, 2, 2)
+PLE_ATTN_KERNEL(128, 4, 1)
+PLE_ATTN_KERNEL(256, 1, 2)
+PLE_ATTN_KERNEL(256, 2, 1)
 #undef PLE_ATTN_KERNEL
 
-// Joins the splits of a row: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top).  One block a row, a wave
-// taking every fourth split.
+// ---------------------------------------------------------------------------
+// Many rows (a chunk of a prefill): bound by the products and the softmax
+// between them.  A block's four waves hold 32 rows each and go through the
+// cache tiles together: each wave dequantises a quarter of a tile (16 tokens
+// of the keys, a quarter of the value elements) and leaves it in LDS as
+// finished MFMA fragments, one 16-byte read per lane each; so a tile is
+// dequantised once for 128 rows.  Two tiles in LDS: the next one is filled
+// while this one is used, with one barrier a tile.  Two blocks per CU cover
+// each other's softmax (D = 256: one).
+// ---------------------------------------------------------------------------
+constexpr int kChunkRows = 128;
+
+template <int D>
+struct ChunkShape {
+    static constexpr int KS = D / 32, NB = D / 16, WB = D / 64;  // WB: element blocks that a wave dequantises
+    static constexpr int K_BYTES = 4 * KS * 1024, V_BYTES = NB * 2 * 1024;
+    static constexpr int BUF = K_BYTES + V_BYTES;
+    static constexpr int STAGE = kTile * WB * 8;  // a wave's value codes on their way through the transposing read
+    static constexpr int NAN_AT = 2 * BUF + kAttnWaves * STAGE;
+    static constexpr int LDS = NAN_AT + 2 * kAttnWaves * kTile;
+};
+
+template <int D>
+__device__ __forceinline__ void attn_chunk_body(const Kv4AttentionArgs& a) {
+    using Sh = ChunkShape<D>;
+    constexpr int MT = 2;
+    extern __shared__ __align__(16) char lds[];
+    const int split = blockIdx.y;
+    int r, head, tile;
+    attn_block(a, r, head, tile);
+    AttnTile w;
+    if (!attn_tile(a, r, tile, w)) return;
+    const int splits = attn_splits(a, w);
+    if (split >= splits) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const int begin = w.lo + split * a.chunk;
+    const int end = split == splits - 1 ? w.hi : min(w.hi, begin + a.chunk);
+    const int before = w.len - w.n;
+    // what every row of the block sees
+    const int common_lo = a.window > 0 ? max(0, before + (w.row1 - 1) / a.group - a.window + 1) : 0;
+    const int common_hi = min(end, before + w.row0 / a.group + 1);
+
+    f16x8 q[MT][Sh::KS];
+    float qs[MT];
+    int see_lo[MT], see_hi[MT];
+    attn_queries<D, MT>(a, w, w.row0 + wave * (16 * MT), head, begin, end, q, qs, see_lo, see_hi);
+    f32x4 o[MT][Sh::NB];
+    float m[MT], l[MT];
+    uint32_t nan_blocks[MT] = {};
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        m[mt] = -__builtin_inff();
+        l[mt] = 0.f;
+#pragma unroll
+        for (int b = 0; b < Sh::NB; ++b) o[mt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int32_t* table_row = a.batch.page_table + (int64_t)r * a.batch.table_width;
+    const uint32_t pick = (uint32_t)((n & 3) | ((4 + (n & 3)) << 8));
+    char* const stage = lds + 2 * Sh::BUF + wave * Sh::STAGE;
+
+    // a tile's quarter, as loaded
+    u32x4 kraw[D == 256 ? 2 : 1], vraw[D == 256 ? 2 : 1], vsc[Sh::WB];
+    uint32_t ksc[D == 64 ? 1 : D / 64];
+    bool bad_next = false;
+    auto load = [&](int t0) {
+        const int tg = t0 + 16 * g;
+        int grp = -1;
+        if (tg < end) grp = kv4_group(a.cache, table_row, head, tg >> 4);
+        bad_next = grp < 0;
+        const int safe = grp < 0 ? 0 : grp;
+        // keys: group n / 4, token 4 wave + n % 4 of it
+        const int64_t kg = __shfl(safe, (n >> 2) * 16, kWave);
+        const uint8_t* kc = a.cache.k_codes + kg * (8 * D) + (4 * wave + (n & 3)) * (D / 2) + g * (D == 64 ? 8 : 16);
+        const uint8_t* ks = a.cache.k_scales + kg * D + (D == 64 ? g * 16 : g * 32) + wave * 4;
+        // values: token `lane`, this wave's 8 WB bytes of it
+        const uint8_t* vc = a.cache.v_codes + (int64_t)safe * (8 * D) + n * (D / 2) + wave * (8 * Sh::WB);
+        if constexpr (D == 64) {
+            const u32x2 x = *(const u32x2*)kc, y = *(const u32x2*)vc;
+            kraw[0] = u32x4{x[0], x[1], 0u, 0u};
+            vraw[0] = u32x4{y[0], y[1], 0u, 0u};
+            ksc[0] = *(const uint32_t*)ks;
+        } else {
+#pragma unroll
+            for (int c = 0; c < D / 128; ++c) {
+                kraw[c] = *(const u32x4*)(kc + c * 64);
+                vraw[c] = *(const u32x4*)(vc + c * 16);
+                ksc[2 * c] = *(const uint32_t*)(ks + c * 128);
+                ksc[2 * c + 1] = *(const uint32_t*)(ks + c * 128 + 16);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < Sh::WB; ++b)
+            vsc[b] = *(const u32x4*)(a.cache.v_scales + (int64_t)safe * D + (wave * Sh::WB + b) * 16);
+    };
+    // whether some row does not see the whole tile (the same for the block: `bad` is the tile's four groups)
+    auto partial = [&](int t0, bool bad) {
+        return t0 < common_lo || t0 < begin || t0 + kTile > common_hi || __ballot(bad) != 0;
+    };
+    auto fill = [&](int t0, int buf) {
+        char* kb = lds + buf * Sh::BUF + (wave * Sh::KS) * 1024 + lane * 16;
+        char* vb = lds + buf * Sh::BUF + Sh::K_BYTES + (wave * Sh::WB * 2) * 1024 + lane * 16;
+        // value codes to LDS first: their way back takes a while
+#pragma unroll
+        for (int b = 0; b < Sh::WB; ++b)
+            *(u32x2*)(stage + lane * (8 * Sh::WB) + b * 8) = u32x2{vraw[b / 2][2 * (b & 1)], vraw[b / 2][2 * (b & 1) + 1]};
+#pragma unroll
+        for (int c = 0; c < (D == 256 ? 2 : 1); ++c) {
+            const uint32_t two = D == 64 ? __builtin_amdgcn_perm(0u, ksc[0], pick)
+                                         : __builtin_amdgcn_perm(ksc[D == 64 ? 0 : 2 * c + 1], ksc[D == 64 ? 0 : 2 * c], pick);
+            const f16x2 sc = fp8_pair(two, false);
+            const f16x2 s0 = {sc[0], sc[0]}, s1 = {sc[1], sc[1]};
+#pragma unroll
+            for (int k = 0; k < (D == 64 ? 2 : 4); ++k) {
+                Frag f;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) f.p[b] = fp4_pair(kraw[c][k], b) * (D == 64 || k < 2 ? s0 : s1);
+                *(u32x4*)(kb + (c * 4 + k) * 1024) = f.u;
+            }
+        }
+        const bool some = partial(t0, bad_next);
+        uint32_t nan_bits = 0;  // of token n of the group, this wave's blocks
+        if (some) {
+#pragma unroll
+            for (int b = 0; b < Sh::WB; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t x = vsc[b][j];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int tok = t0 + 16 * g + 4 * j + e;
+                        if (bad_next || tok < w.first_seen || tok >= end) x &= ~(0xFFu << (8 * e));
+                    }
+                    const uint32_t nan = ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                    vsc[b][j] = x & ~((nan >> 7) * 0xFFu);
+                    if ((n >> 2) == j && (nan >> (8 * (n & 3) + 7) & 1u) != 0) nan_bits |= 1u << b;
+                }
+            *(uint8_t*)(lds + Sh::NAN_AT + (buf * kAttnWaves + wave) * kTile + lane) = (uint8_t)nan_bits;
+        }
+#pragma unroll
+        for (int b = 0; b < Sh::WB; ++b) {
+            typedef int i32x2 __attribute__((ext_vector_type(2)));
+            const i32x2 c = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+                (__attribute__((address_space(3))) i32x2*)(stage + lane * (8 * Sh::WB) + b * 8));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                Frag f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    f.p[e] = fp4_pair((uint32_t)c[h], e) * fp8_pair(vsc[b][2 * h + e / 2], (e & 1) != 0);
+                *(u32x4*)(vb + (b * 2 + h) * 1024) = f.u;
+            }
+        }
+    };
+
+    bool bad = false;
+    if (begin < end) {
+        load(begin);
+        fill(begin, 0);
+        bad = bad_next;
+    }
+    int buf = 0;
+    for (int t0 = begin; t0 < end; t0 += kTile, buf ^= 1) {
+        const bool more = t0 + kTile < end;
+        __syncthreads();  // this tile is whole; every read of the other buffer is done
+        if (more) load(t0 + kTile);
+        const char* kb = lds + buf * Sh::BUF + lane * 16;
+        const char* vb = kb + Sh::K_BYTES;
+        const bool some = partial(t0, bad);
+        f32x4 s[MT][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) s[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < Sh::KS; ++k) {
+                const f16x8 f = *(const f16x8*)(kb + (i * Sh::KS + k) * 1024);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    s[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, q[mt][k], s[mt][i], 0, 0, 0);
+            }
+        }
+        Frag p[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            attn_softmax<Sh::NB>(s[mt], qs[mt], some, bad, t0 + 16 * g, see_lo[mt], see_hi[mt], m[mt], l[mt], o[mt], p[mt]);
+#pragma unroll
+        for (int b = 0; b < Sh::NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f16x8 f = *(const f16x8*)(vb + (b * 2 + h) * 1024);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    o[mt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[mt][h].v, o[mt][b], 0, 0, 0);
+            }
+        if (some) {
+            uint32_t bits = 0;  // of token t0 + lane, all blocks
+#pragma unroll
+            for (int k = 0; k < kAttnWaves; ++k)
+                bits |= (uint32_t)*(const uint8_t*)(lds + Sh::NAN_AT + (buf * kAttnWaves + k) * kTile + lane) << (k * Sh::WB);
+            for (uint64_t left = __ballot(bits != 0); left != 0; left &= left - 1) {
+                const int from = (int)__builtin_ctzll(left);
+                const uint32_t blocks = (uint32_t)__builtin_amdgcn_readlane((int)bits, from);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    if (t0 + from >= see_lo[mt] && t0 + from < see_hi[mt]) nan_blocks[mt] |= blocks;
+            }
+        }
+        if (more) {
+            fill(t0 + kTile, buf ^ 1);
+            bad = bad_next;
+        }
+    }
+
+    const float vscale = a.cache.v_scale[head];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        float total = l[mt];
+        total += __shfl_xor(total, 16, kWave);
+        total += __shfl_xor(total, 32, kWave);
+        const int row = w.row0 + wave * (16 * MT) + mt * 16 + n;
+        if (row >= w.row1) continue;
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const float lse2 = total == 0.f ? -__builtin_inff() : (m[mt] - kWeightShift) + log2f(total);
+        const int i = row / a.group, hq = head * a.group + (row - i * a.group);
+        const int64_t orow = (w.first + i) * a.num_q_heads + hq;
+        const float f = splits == 1 ? inv * vscale : inv;
+#pragma unroll
+        for (int b = 0; b < Sh::NB; ++b) {
+            f32x4 x = o[mt][b] * f;
+            if (nan_blocks[mt] >> b & 1u) x = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+            if (splits == 1)
+                *(u32x2*)(a.out + orow * D + b * 16 + g * 4) = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+            else
+                *(f32x4*)(a.part + (orow * a.splits + split) * D + b * 16 + g * 4) = x;
+        }
+        if (g == 0) {
+            if (splits > 1)
+                a.part[a.batch.num_tokens * a.num_q_heads * a.splits * D + orow * a.splits + split] = lse2;
+            else if (a.lse != nullptr)
+                a.lse[orow] = lse2 * 0.693147180559945309f;
+        }
+    }
+}
+
+#define PLE_ATTN_KERNEL(D, OCC)                                                                                         \
+    __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_chunk_##D##_kernel(Kv4AttentionArgs a) {         \
+        attn_chunk_body<D>(a);                                                                                          \
+    }
+PLE_ATTN_KERNEL(64, 2)
+PLE_ATTN_KERNEL(128, 2)
+PLE_ATTN_KERNEL(256, 1)
+#undef PLE_ATTN_KERNEL
+
+// Joins the splits of a row: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top).  One block a row.
 __global__ __launch_bounds__(kAttnThreads) void kv4_attention_join_kernel(Kv4AttentionArgs a) {
-    __shared__ float weight[kMostSplits], sum[kAttnWaves][256];
+    __shared__ float weight[kMostSplits], sum[kAttnThreads * 4];
     const int64_t orow = blockIdx.x, rows = a.batch.num_tokens * a.num_q_heads;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t t = orow / a.num_q_heads;
     const int hq = (int)(orow - t * a.num_q_heads), head = hq / a.group;
-    const int r = find_request(a.batch.query_start_loc, a.batch.num_reqs, t);
+    int r;
+    int64_t start;
+    wave_find_request(a.batch.query_start_loc, a.batch.num_reqs, t, t, 1, 0, lane, r, start);
     AttnTile w;
     int64_t q0, q1;
     carried_window(a.batch.query_start_loc, a.batch.num_tokens, r, nullptr, q0, q1);
@@ -477,25 +761,24 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_attention_join_kernel(Kv4Att
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(total, d, kWave);
     __syncthreads();
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    const float* src = a.part + orow * a.splits * D;
-    const int per = D / kWave;  // elements of a lane
-#pragma unroll 4
-    for (int s = wave; s < splits; s += kAttnWaves) {
-        const float wt = weight[s];
-        const float* p = src + (int64_t)s * D + lane;
+    // D/4 threads a split, four elements each
+    const int per = D / 4, step = kAttnThreads / per, e4 = (threadIdx.x % per) * 4;
+    const float* src = a.part + orow * a.splits * D + e4;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int k = threadIdx.x / per; k < splits; k += step) {
+        const f32x4 x = *(const f32x4*)(src + (int64_t)k * D);
+        const float wt = weight[k];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < per) v[e] = fmaf(p[e * kWave], wt, v[e]);
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(x[e], wt, v[e]);
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (e < per) sum[wave][e * kWave + lane] = v[e];
+    *(f32x4*)(sum + threadIdx.x / per * D + e4) = v;
     __syncthreads();
     if ((int)threadIdx.x < D) {
         const int d = threadIdx.x;
         const float f = total == 0.f ? 0.f : a.cache.v_scale[head] / total;
-        const float x = (sum[0][d] + sum[1][d]) + (sum[2][d] + sum[3][d]);
+        float x = 0.f;
+        for (int k = 0; k < step; ++k) x += sum[k * D + d];
         a.out[orow * D + d] = (uint16_t)pack_bf16x2(x * f, 0.f);
     }
     if (a.lse != nullptr && threadIdx.x == 0)
@@ -510,23 +793,24 @@ void plan_kv4_attention(Kv4AttentionArgs& a) {
     int64_t len = a.batch.max_seq_len > 0 && a.batch.max_seq_len < cover ? a.batch.max_seq_len : cover;
     const int64_t rows = new_max * a.group;
     const int most = a.cache.head_dim == 256 ? 32 : 64;
-    a.rows = rows <= 16 ? 16 : (rows <= 32 || most == 32 ? 32 : 64);
+    a.rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= most ? 64 : kChunkRows));
     a.tiles = (int)((rows + a.rows - 1) / a.rows);
     if (a.window > 0) {
         const int64_t span = (int64_t)a.window + a.rows / a.group + 1 + 15;
         len = len < span ? len : span;
     }
-    // splits: about 1024 blocks (four per CU), each with at least one tile of 64 tokens per wave
+    // Splits where the query tiles alone leave CUs idle: enough for 512 blocks (two per CU), each with at least 1024
+    // tokens, below which a block's fixed cost and the joining kernel outweigh what a shorter loop saves.
     const int64_t blocks = R * a.cache.num_kv_heads * a.tiles;
-    int64_t splits = blocks > 0 ? (1024 + blocks - 1) / blocks : 1;
-    const int64_t most_splits = (len + kTile * kAttnWaves - 1) / (kTile * kAttnWaves);
+    int64_t splits = blocks > 0 ? (512 + blocks - 1) / blocks : 1;
+    const int64_t most_splits = (len + 1023) / 1024;
     splits = splits < most_splits ? splits : most_splits;
     splits = splits < 1 ? 1 : (splits < kMostSplits - 1 ? splits : kMostSplits - 1);
     int64_t chunk = (len + splits - 1) / splits;
     chunk = (chunk + kTile * kAttnWaves - 1) / (kTile * kAttnWaves) * (kTile * kAttnWaves);
-    // a range starts at a multiple of 16, up to 15 tokens before the first that is seen
     a.chunk = (int)chunk;
-    a.splits = (int)((len + 15 + chunk - 1) / chunk);
+    // (a range starts at a multiple of 16, up to 15 tokens before the first that is seen; the last split takes those)
+    a.splits = (int)((len + chunk - 1) / chunk);
     if (a.splits < 1) a.splits = 1;
 }
 
@@ -535,9 +819,25 @@ size_t kv4_attention_part_bytes(const Kv4AttentionArgs& a) {
     return (size_t)a.batch.num_tokens * a.num_q_heads * a.splits * (a.cache.head_dim + 1) * sizeof(float);
 }
 
+template <void (*FN)(Kv4AttentionArgs), int D>
+static hipError_t launch_chunk(const Kv4AttentionArgs& a, dim3 grid, hipStream_t s) {
+    constexpr int kLds = ChunkShape<D>::LDS;
+    static const hipError_t attr =
+        hipFuncSetAttribute((const void*)FN, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (attr != hipSuccess) return attr;
+    hipLaunchKernelGGL(FN, grid, dim3(kAttnThreads), kLds, s, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)((int64_t)a.batch.num_reqs * a.cache.num_kv_heads * a.tiles), (unsigned)a.splits);
     const int D = a.cache.head_dim, MT = a.rows / 16;
+    if (a.rows == kChunkRows) {
+        const hipError_t e = D == 64    ? launch_chunk<kv4_attention_chunk_64_kernel, 64>(a, grid, s)
+                             : D == 128 ? launch_chunk<kv4_attention_chunk_128_kernel, 128>(a, grid, s)
+                                        : launch_chunk<kv4_attention_chunk_256_kernel, 256>(a, grid, s);
+        if (e != hipSuccess) return e;
+    }
 #define PLE_ATTN_LAUNCH(DD, MM) \
     if (D == DD && MT == MM) hipLaunchKernelGGL(kv4_attention_##DD##_##MM##_kernel, grid, dim3(kAttnThreads), 0, s, a)
     PLE_ATTN_LAUNCH(64, 1);

@@ -20,6 +20,19 @@ from . import capi
 from . import _BF16, _BYTES, _F32, _I32, _nbytes, _ptr, _req, _req_bytes, _same_device, _stream
 
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
+_BF, _INT = torch.bfloat16, torch.int32
+
+
+def _raw_stream(device: int) -> int:
+    """The current stream's handle on the tensors' device (these calls are launch-bound at decode sizes, and building
+    a torch.cuda.Stream object for it costs more than the call)."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _fits(t, dtype, shape, device: int) -> bool:
+    """A contiguous tensor of this type, shape and device: what most calls pass.  Anything else goes through the
+    checks that name the fault."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
 
 
 class W4Weight:
@@ -29,6 +42,7 @@ class W4Weight:
         self.codes, self.scales, self.zeros, self.tensor_scale = codes, scales, zeros, tensor_scale
         self.out_dim, self.k_dim = int(codes.shape[0]), 2 * int(codes.shape[1])
         _same_device(codes, scales, zeros, tensor_scale)
+        self.device = codes.get_device()
         self.desc = capi.ple_w4_weight(_ptr(codes), _ptr(scales), _ptr(zeros), _ptr(tensor_scale), fmt, self.out_dim,
                                        self.k_dim, group)
 
@@ -58,15 +72,21 @@ class W4Weight:
 
 def ple_w4_linear(x, w: W4Weight, *, out=None, stream=None):
     """x bf16 [T][K] (rows may be strided) -> out bf16 [T][O] = x W^T."""
-    if x.dim() != 2 or x.shape[1] != w.k_dim or x.dtype not in _BF16 or (x.shape[0] and x.stride(1) != 1):
-        raise ValueError(f"x must be bf16 [T][{w.k_dim}] with contiguous rows, got {tuple(x.shape)} {x.dtype}")
-    T = x.shape[0]
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != w.k_dim or x.dtype not in _BF16 or (shape[0] and x.stride(1) != 1):
+        raise ValueError(f"x must be bf16 [T][{w.k_dim}] with contiguous rows, got {tuple(shape)} {x.dtype}")
+    T = shape[0]
     if out is None:
-        out = torch.empty((T, w.out_dim), dtype=torch.bfloat16, device=x.device)
-    _req("out", out, (T, w.out_dim), _BF16)
-    _same_device(x, w.codes, out)
-    capi.check(capi.load().ple_w4_linear(x.data_ptr(), x.stride(0) if T > 1 else w.k_dim, ctypes.byref(w.desc), T,
-                                         out.data_ptr(), _stream(stream)), "ple_w4_linear")
+        if x.get_device() != w.device:
+            _same_device(x, w.codes)
+        out = torch.empty((T, w.out_dim), dtype=_BF, device=x.device)
+    else:
+        _req("out", out, (T, w.out_dim), _BF16)
+        _same_device(x, w.codes, out)
+    rc = capi.load().ple_w4_linear(x.data_ptr(), x.stride(0) if T > 1 else w.k_dim, ctypes.byref(w.desc), T,
+                                   out.data_ptr(), _raw_stream(w.device) if stream is None else _stream(stream))
+    if rc:
+        capi.check(rc, "ple_w4_linear")
     return out
 
 
@@ -86,56 +106,77 @@ class KV4Cache:
         _req("v_scale", v_scale, (heads,), _F32)
         _same_device(k_codes, k_scales, v_codes, v_scales, k_scale, v_scale)
         self.tensors = (k_codes, k_scales, v_codes, v_scales, k_scale, v_scale)
+        self.device, self._workspaces = k_codes.get_device(), {}
         self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = pages, heads, size, 2 * half
         self.desc = capi.ple_kv4_cache(*(t.data_ptr() for t in self.tensors), pages, heads, size, 2 * half, 0)
 
 
-def _heads(name: str, t, T, heads, D) -> int:
+def _heads(name: str, t, T, heads, cache) -> int:
     """A [T][heads][D] bf16 tensor whose tokens may be strided (a slice of a fused projection); its token stride."""
     if not isinstance(t, torch.Tensor) or t.dtype not in _BF16:
         raise ValueError(f"{name} must be a bf16 tensor")
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({T}, {'*' if heads is None else heads}, {D})")
+    D, shape = cache.head_dim, t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected ({T}, {'*' if heads is None else heads}, {D})")
     stride = t.stride()
-    if T and (stride[2] != 1 or (t.shape[1] > 1 and stride[1] != D)):
+    if T and (stride[2] != 1 or (shape[1] > 1 and stride[1] != D)):
         raise ValueError(f"{name} must have contiguous heads and elements, got strides {stride}")
-    return stride[0] if T > 1 else t.shape[1] * D
+    return stride[0] if T > 1 else shape[1] * D
 
 
 def _kv4_batch(cache, query_start_loc, seq_lens, page_table, T, max_request_tokens=0, max_seq_len=0):
-    _req("query_start_loc", query_start_loc, (None,), _I32)
-    R = query_start_loc.shape[0] - 1
-    if R < 0:
-        raise ValueError("query_start_loc needs at least one entry")
-    _req("seq_lens", seq_lens, (R,), _I32)
-    _req("page_table", page_table, (R, None), _I32)
-    _same_device(cache.tensors[0], query_start_loc, seq_lens, page_table)
+    R = page_table.shape[0] if page_table.dim() == 2 else -1
+    dev = cache.device
+    if not (_fits(query_start_loc, _INT, (R + 1,), dev) and _fits(seq_lens, _INT, (R,), dev)
+            and _fits(page_table, _INT, page_table.shape, dev)):
+        _req("query_start_loc", query_start_loc, (None,), _I32)
+        R = query_start_loc.shape[0] - 1
+        if R < 0:
+            raise ValueError("query_start_loc needs at least one entry")
+        _req("seq_lens", seq_lens, (R,), _I32)
+        _req("page_table", page_table, (R, None), _I32)
+        _same_device(cache.tensors[0], query_start_loc, seq_lens, page_table)
     return capi.ple_kv4_batch(query_start_loc.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), T, R,
-                              page_table.shape[1], int(max_request_tokens), int(max_seq_len))
+                              page_table.shape[1], max_request_tokens, max_seq_len)
+
+
+def _out(name, t, shape, dtypes, cache):
+    """An output: the caller's, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtypes[0], device=cache.tensors[0].device)
+    _req(name, t, shape, dtypes)
+    _same_device(cache.tensors[0], t)
+    return t
 
 
 def ple_kv4_append(cache: KV4Cache, k, v, query_start_loc, seq_lens, page_table, *, inv_freq=None,
                    interleaved: bool = False, q=None, q_out=None, stream=None):
     """New keys and values bf16 [T][heads][D] into the cache, keys (and q, if given) rotated by their positions over
     the first 2 * len(inv_freq) elements.  Returns the rotated queries bf16 [T][q heads][D], or None without q."""
-    D, T = cache.head_dim, int(k.shape[0])
-    ks, vs = _heads("k", k, T, cache.num_kv_heads, D), _heads("v", v, T, cache.num_kv_heads, D)
-    _req("inv_freq", inv_freq, (None,), _F32, optional=True)
-    qs, hq = 0, 0
+    D, T, H = cache.head_dim, k.shape[0], cache.num_kv_heads
+    ks, vs = _heads("k", k, T, H, cache), _heads("v", v, T, H, cache)
+    qs = hq = rot = 0
+    q_at = out_at = freq_at = None
     if q is not None:
-        qs, hq = _heads("q", q, T, None, D), int(q.shape[1])
-        if q_out is None:
-            q_out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=q.device)
-        _req("q_out", q_out, (T, hq, D), _BF16)
+        qs, hq = _heads("q", q, T, None, cache), q.shape[1]
+        q_out = _out("q_out", q_out, (T, hq, D), _BF16, cache)
+        q_at, out_at = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out given without q")
+    if inv_freq is not None:
+        _req("inv_freq", inv_freq, (None,), _F32)
+        if inv_freq.get_device() != cache.device:
+            _same_device(cache.tensors[0], inv_freq)
+        rot, freq_at = 2 * inv_freq.shape[0], inv_freq.data_ptr()
     b = _kv4_batch(cache, query_start_loc, seq_lens, page_table, T)
-    _same_device(cache.tensors[0], k, v, q, q_out, inv_freq)
-    capi.check(capi.load().ple_kv4_append(
-        ctypes.byref(cache.desc), ctypes.byref(b), k.data_ptr(), ks, v.data_ptr(), vs,
-        None if q is None else q.data_ptr(), qs, hq, None if q is None else q_out.data_ptr(),
-        None if inv_freq is None else inv_freq.data_ptr(), 0 if inv_freq is None else 2 * inv_freq.shape[0],
-        int(interleaved), _stream(stream)), "ple_kv4_append")
+    dev = cache.device
+    if k.get_device() != dev or v.get_device() != dev or (q is not None and q.get_device() != dev):
+        _same_device(cache.tensors[0], k, v, q)
+    rc = capi.load().ple_kv4_append(
+        ctypes.byref(cache.desc), ctypes.byref(b), k.data_ptr(), ks, v.data_ptr(), vs, q_at, qs, hq, out_at, freq_at,
+        rot, 1 if interleaved else 0, _raw_stream(cache.device) if stream is None else _stream(stream))
+    if rc:
+        capi.check(rc, "ple_kv4_append")
     return q_out
 
 
@@ -144,17 +185,13 @@ def ple_kv4_read(cache: KV4Cache, query_start_loc, seq_lens, page_table, num_tok
     """The new tokens' keys and values as the cache holds them: two bf16 [T][heads][D]."""
     T = int(num_tokens)
     shape = (T, cache.num_kv_heads, cache.head_dim)
-    dev = cache.tensors[0].device
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _req("k_out", k_out, shape, _BF16)
-    _req("v_out", v_out, shape, _BF16)
+    k_out = _out("k_out", k_out, shape, _BF16, cache)
+    v_out = _out("v_out", v_out, shape, _BF16, cache)
     b = _kv4_batch(cache, query_start_loc, seq_lens, page_table, T)
-    _same_device(cache.tensors[0], k_out, v_out)
-    capi.check(capi.load().ple_kv4_read(ctypes.byref(cache.desc), ctypes.byref(b), k_out.data_ptr(), v_out.data_ptr(),
-                                        _stream(stream)), "ple_kv4_read")
+    rc = capi.load().ple_kv4_read(ctypes.byref(cache.desc), ctypes.byref(b), k_out.data_ptr(), v_out.data_ptr(),
+                                  _raw_stream(cache.device) if stream is None else _stream(stream))
+    if rc:
+        capi.check(rc, "ple_kv4_read")
     return k_out, v_out
 
 
@@ -176,24 +213,34 @@ def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table,
     scale: 1/sqrt(D) if None.  window: tokens seen, the own one included (0: all).  max_request_tokens and
     max_seq_len (0: unknown) let the call size its launch; pass them.  Returns (out bf16 [T][q heads][D], lse fp32
     [T][q heads] or None)."""
-    D, T = cache.head_dim, int(q.shape[0])
-    qs, hq = _heads("q", q, T, None, D), int(q.shape[1])
-    if out is None:
-        out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
-    _req("out", out, (T, hq, D), _BF16)
-    _req("lse", lse, (T, hq), _F32, optional=True)
+    D, T = cache.head_dim, q.shape[0]
+    qs, hq = _heads("q", q, T, None, cache), q.shape[1]
+    out = _out("out", out, (T, hq, D), _BF16, cache)
+    if lse is not None or want_lse:
+        lse = _out("lse", lse, (T, hq), _F32, cache)
     b = _kv4_batch(cache, query_start_loc, seq_lens, page_table, T, max_request_tokens, max_seq_len)
+    if q.get_device() != cache.device:
+        _same_device(cache.tensors[0], q)
     lib = capi.load()
-    need = int(lib.ple_kv4_attention_workspace_bytes(hq, ctypes.byref(cache.desc), ctypes.byref(b), int(window)))
-    if workspace is None and need > 0:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-    if workspace is not None:
+    # the workspace's size follows from these numbers alone
+    sizes = (T, b.num_reqs, b.table_width, hq, window, max_request_tokens, max_seq_len)
+    need = cache._workspaces.get(sizes)
+    if need is None:
+        if len(cache._workspaces) >= 4096:
+            cache._workspaces.clear()
+        need = int(lib.ple_kv4_attention_workspace_bytes(hq, ctypes.byref(cache.desc), ctypes.byref(b), window))
+        cache._workspaces[sizes] = need
+    if workspace is None:
+        if need > 0:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    else:
         _req_bytes("workspace", workspace, need)
-    _same_device(cache.tensors[0], q, out, lse, workspace)
-    capi.check(lib.ple_kv4_attention(
-        q.data_ptr(), qs, hq, ctypes.byref(cache.desc), ctypes.byref(b), int(window),
-        D ** -0.5 if scale is None else float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
-        _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream(stream)), "ple_kv4_attention")
+        _same_device(cache.tensors[0], workspace)
+    rc = lib.ple_kv4_attention(
+        q.data_ptr(), qs, hq, ctypes.byref(cache.desc), ctypes.byref(b), window,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if workspace is None else _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
+        _raw_stream(cache.device) if stream is None else _stream(stream))
+    if rc:
+        capi.check(rc, "ple_kv4_attention")
     return out, lse

@@ -115,13 +115,14 @@ def no_library(monkeypatch):
 
 
 class _W:
-    k_dim, out_dim, codes, desc = 128, 64, None, None
+    k_dim, out_dim, codes, desc, device = 128, 64, None, None, -1
 
 
 def _view(pages=4, H=2, page=16, D=128):
     """A cache object over host tensors (built without its device check)."""
     c = object.__new__(ple.KV4Cache)
     c.tensors = (torch.zeros((pages, H, page, D // 2), dtype=torch.uint8),)
+    c.device, c._workspaces = 0, {}
     c.num_pages, c.num_kv_heads, c.page_size, c.head_dim = pages, H, page, D
     return c
 
