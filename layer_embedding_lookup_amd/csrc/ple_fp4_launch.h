@@ -40,11 +40,12 @@ struct Kv4AttentionArgs {
     int32_t window;   // 0: none
     float scale;
     int32_t rows;     // rows of a block's query tile
+    int32_t waves;    // of a block
     int32_t tiles;    // query tiles per request and key head (grid)
     int32_t chunk;    // tokens of the cache per split
     int32_t splits;   // most splits of any query tile (grid)
 };
-// The plan part of the arguments (rows, tiles, chunk, splits), from sizes and hints alone.
+// The plan part of the arguments (rows, waves, tiles, chunk, splits), from sizes and hints alone.
 void plan_kv4_attention(Kv4AttentionArgs& a);
 size_t kv4_attention_part_bytes(const Kv4AttentionArgs& a);
 hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t s);

@@ -31,12 +31,14 @@
 
 namespace ple {
 
-constexpr int kAttnWaves = 4;
+constexpr int kAttnWaves = 4;  // of a chunk block, and those whose sums a decode block joins through LDS
 constexpr int kAttnThreads = kAttnWaves * kWave;
 constexpr int kTile = 64;  // cache tokens of a tile
 constexpr int kMostSplits = 1024;
-// Weights are 2^(s - m + kWeightShift): fp16 keeps them above 2^-24, so tokens down to 2^-32 of the heaviest one count.
-constexpr float kWeightShift = 8.0f;
+// Weights are 2^(s - m + kWeightShift) with m a row's largest exponent but for kSlack: m only moves on, and the row's
+// sums are only rescaled, when the maximum has passed it by more than that.  Weights stay below 2^15 and fp16 keeps
+// them above 2^-24, so tokens down to 2^-32 of the heaviest one count.
+constexpr float kWeightShift = 8.0f, kSlack = 7.0f;
 
 // What a block's query tile sees: rows [row0, row1) of request r, cache tokens [lo, hi).
 struct AttnTile {
@@ -78,6 +80,40 @@ __device__ __forceinline__ void attn_block(const Kv4AttentionArgs& a, int& r, in
     head = pair - r * heads;
 }
 
+// A lane's way along its request's pages: the 16-token group at token tg, then `step` groups on at a time.  Table
+// entries are fetched a tile before the group's number is needed, which is a tile before its codes are.
+struct PageWalk {
+    const int32_t* row;
+    int per_page, page, in_page, step_pages, step_in, last;  // last: the page of token end - 1
+    uint32_t pages, heads, head;
+    int entry;
+
+    __device__ __forceinline__ PageWalk(const Kv4AttentionArgs& a, const int32_t* table_row, int h, int tg, int step, int end)
+        : row(table_row), per_page(a.cache.page_size >> 4), pages((uint32_t)a.cache.num_pages),
+          heads((uint32_t)a.cache.num_kv_heads), head((uint32_t)h) {
+        page = (tg >> 4) / per_page;
+        in_page = (tg >> 4) - page * per_page;
+        step_pages = step / per_page;
+        step_in = step - step_pages * per_page;
+        last = (end - 1) / a.cache.page_size;
+        entry = -1;
+    }
+    // the entry of the current group (in bounds even for groups past the end, which `number` turns away)
+    __device__ __forceinline__ void fetch() { entry = row[min(page, last)]; }
+    // the current group's number or -1, and on to the next one
+    __device__ __forceinline__ int number(int tg, int end) {
+        const uint32_t e = (uint32_t)entry;
+        const int grp = tg < end && e < pages ? (int)((e * heads + head) * (uint32_t)per_page) + in_page : -1;
+        page += step_pages;
+        in_page += step_in;
+        if (in_page >= per_page) {
+            in_page -= per_page;
+            ++page;
+        }
+        return grp;
+    }
+};
+
 __device__ __forceinline__ f16x2 fp4_pair(uint32_t w, int byte) {
     switch (byte) {
         case 0: return __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
@@ -97,7 +133,7 @@ union Frag {
     u32x4 u;
 };
 
-template <int D>
+template <int D, int WAVES>
 struct AttnShape {
     static constexpr int KS = D / 32;                   // k-steps of the first product
     static constexpr int NB = D / 16;                   // element blocks
@@ -107,7 +143,7 @@ struct AttnShape {
     static constexpr int WAVE_LDS = kTile * VROW + 4 * SROW;
     static constexpr int OROW = D + 4;                  // the join's rows (fp32)
     static constexpr int JOIN_LDS = kAttnWaves * 16 * OROW * 4;
-    static constexpr int LDS = WAVE_LDS * kAttnWaves > JOIN_LDS ? WAVE_LDS * kAttnWaves : JOIN_LDS;
+    static constexpr int LDS = WAVE_LDS * WAVES > JOIN_LDS ? WAVE_LDS * WAVES : JOIN_LDS;
 };
 
 // The queries of MT x 16 rows from row0 on: lane (n, g) holds, of row 16 mt + n, the elements that its key codes
@@ -183,7 +219,7 @@ __device__ __forceinline__ void attn_softmax(f32x4 (&s)[4], float qs, bool some,
     top = fmaxf(top, __shfl_xor(top, 16, kWave));
     top = fmaxf(top, __shfl_xor(top, 32, kWave));
     const float mn = fmaxf(m, top * qs);  // (qs > 0)
-    if (__ballot(mn > m) != 0) {
+    if (__ballot(mn > m + kSlack) != 0) {
         const float by = m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - mn);
         l *= by;
 #pragma unroll
@@ -204,10 +240,10 @@ __device__ __forceinline__ void attn_softmax(f32x4 (&s)[4], float qs, bool some,
     l += sum;
 }
 
-template <int D, int MT>
+template <int D, int MT, int WAVES>
 __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
-    using Sh = AttnShape<D>;
-    __shared__ __align__(16) char lds[Sh::LDS];
+    using Sh = AttnShape<D, WAVES>;
+    extern __shared__ __align__(16) char lds[];
     __shared__ float join_m[kAttnWaves][16], join_l[kAttnWaves][16];
     const int split = blockIdx.y;
     int r, head, tile;
@@ -242,19 +278,23 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
     const int32_t* table_row = a.batch.page_table + (int64_t)r * a.batch.table_width;
     const uint32_t pick = (uint32_t)((n & 3) | ((4 + (n & 3)) << 8));
 
-    for (int t0 = begin + wave * kTile; t0 < end; t0 += kAttnWaves * kTile) {
-        // this lane's group g of the tile
-        const int tg = t0 + 16 * g;
-        int grp = -1;
-        if (tg < end) grp = kv4_group(a.cache, table_row, head, tg >> 4);
-        const bool bad = grp < 0;
-        const int safe = bad ? 0 : grp;
+    // a tile, as loaded: the next one is on its way while this one's weights and value product are formed
+    bool bad_next = false;
+    u32x4 kraw[4][D == 256 ? 2 : 1];
+    u32x4 kscale[D == 64 ? 1 : D / 64];
+    u32x4 vraw[Sh::NV];
+    uint32_t vsc[D / 64];
+    const int first = begin + wave * kTile;
+    PageWalk walk(a, table_row, head, first + 16 * g, WAVES * kTile / 16, end);
+    auto load = [&](int t0) {
+        const int grp = walk.number(t0 + 16 * g, end);
+        walk.fetch();
+        bad_next = grp < 0;
+        const int safe = grp < 0 ? 0 : grp;
         // keys: group n / 4, token 4 i + n % 4
         const int64_t kg = __shfl(safe, (n >> 2) * 16, kWave);
         const uint8_t* kc = a.cache.k_codes + kg * (8 * D) + (n & 3) * (D / 2) + g * (D == 64 ? 8 : 16);
         const uint8_t* ksc = a.cache.k_scales + kg * D + (D == 64 ? g * 16 : g * 32);
-        u32x4 kraw[4][D == 256 ? 2 : 1];
-        u32x4 kscale[D == 64 ? 1 : D / 64];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (D == 64) {
@@ -275,19 +315,23 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
             }
         }
         // values: codes by 1 KiB a load, scales by D/16 bytes a lane
-        u32x4 vraw[Sh::NV];
 #pragma unroll
         for (int j = 0; j < Sh::NV; ++j) {
             const int at = j * 1024 + lane * 16;
             const int64_t vg = __shfl(safe, (at / (8 * D)) * 16, kWave);
             vraw[j] = *(const u32x4*)(a.cache.v_codes + vg * (8 * D) + at % (8 * D));
         }
-        uint32_t vsc[D / 64];
-        {
-            const uint8_t* p = a.cache.v_scales + (int64_t)safe * D + n * (D / 16);
+        const uint8_t* p = a.cache.v_scales + (int64_t)safe * D + n * (D / 16);
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) vsc[j] = ((const uint32_t*)p)[j];
-        }
+        for (int j = 0; j < D / 64; ++j) vsc[j] = ((const uint32_t*)p)[j];
+    };
+    if (first < end) {
+        walk.fetch();
+        load(first);
+    }
+    for (int t0 = first; t0 < end; t0 += WAVES * kTile) {
+        const int tg = t0 + 16 * g;  // this lane's group g of the tile
+        const bool bad = bad_next;
 
         // S^T
         f32x4 s[MT][4];
@@ -351,6 +395,7 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
                 dst[1] = fp8_pair(x, true);
             }
         }
+        if (t0 + WAVES * kTile < end) load(t0 + WAVES * kTile);
 
         // lane (n, g) holds tokens 16 g .. 16 g + 15 of its row, in order
         Frag p[MT][2];
@@ -402,17 +447,38 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
         float sum = l[mt];
         sum += __shfl_xor(sum, 16, kWave);
         sum += __shfl_xor(sum, 32, kWave);
-        __syncthreads();  // the loop's LDS, or the join before this one
-        if (g == 0) {
-            join_m[wave][n] = m[mt];
-            join_l[wave][n] = sum;
-        }
-        float* jo = (float*)lds + (wave * 16 + n) * Sh::OROW;
+        float* jo = (float*)lds + ((wave & 3) * 16 + n) * Sh::OROW;
+        // the upper four waves hand theirs to the lower ones, lane by lane; then the lower ones write theirs
 #pragma unroll
-        for (int b = 0; b < Sh::NB; ++b) *(f32x4*)(jo + b * 16 + g * 4) = o[mt][b];
-        for (uint32_t left = nan_blocks[mt]; left != 0; left &= left - 1)
-            *(f32x4*)(jo + __builtin_ctz(left) * 16 + g * 4) = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
-        __syncthreads();
+        for (int half = WAVES / kAttnWaves - 1; half >= 0; --half) {
+            __syncthreads();  // the loop's LDS, or what was read of the join before this
+            if (wave / kAttnWaves == half) {
+                if (g == 0) {
+                    join_m[wave & 3][n] = m[mt];
+                    join_l[wave & 3][n] = sum;
+                }
+#pragma unroll
+                for (int b = 0; b < Sh::NB; ++b) *(f32x4*)(jo + b * 16 + g * 4) = o[mt][b];
+                for (uint32_t left = nan_blocks[mt]; left != 0; left &= left - 1)
+                    *(f32x4*)(jo + __builtin_ctz(left) * 16 + g * 4) = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+            }
+            __syncthreads();
+            if (half > 0 && wave / kAttnWaves == half - 1) {
+                const float om = join_m[wave & 3][n], top = fmaxf(m[mt], om);
+                // (one that saw nothing, or only NaN, still counts with its sum: 0, or NaN)
+                const float mine = m[mt] == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[mt] - top);
+                const float theirs = om == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(om - top);
+                sum = sum * mine + join_l[wave & 3][n] * theirs;
+                m[mt] = top;
+#pragma unroll
+                for (int b = 0; b < Sh::NB; ++b) {
+                    const f32x4 x = *(const f32x4*)(jo + b * 16 + g * 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[mt][b][e] = o[mt][b][e] * mine + x[e] * theirs;
+                }
+            }
+        }
+        if (wave >= kAttnWaves) continue;
         // 16 threads a row, each with D/16 elements
         const int row = threadIdx.x >> 4, part = threadIdx.x & 15;
         const int grow = w.row0 + mt * 16 + row;
@@ -459,18 +525,15 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
     }
 }
 
-#define PLE_ATTN_KERNEL(D, MT, OCC)                                                                                \
-    __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_##D##_##MT##_kernel(Kv4AttentionArgs a) { \
-        attn_body<D, MT>(a);                                                                                    \
+// D, row tiles, waves, waves per SIMD that registers allow
+#define PLE_ATTN_SHAPES(X)                                                                                        \
+    X(64, 1, 4, 3) X(64, 1, 8, 2) X(64, 2, 4, 2) X(64, 2, 8, 2) X(128, 1, 4, 3) X(128, 1, 8, 2) X(128, 2, 4, 2) \
+    X(128, 2, 8, 2) X(256, 1, 4, 2) X(256, 1, 8, 2)
+#define PLE_ATTN_KERNEL(D, MT, WAVES, OCC)                                                                                  \
+    __global__ __launch_bounds__(WAVES * kWave, OCC) void kv4_attention_##D##_##MT##x##WAVES##_kernel(Kv4AttentionArgs a) { \
+        attn_body<D, MT, WAVES>(a);                                                                                         \
     }
-PLE_ATTN_KERNEL(64, 1, 3)
-PLE_ATTN_KERNEL(64, 2, 2)
-PLE_ATTN_KERNEL(64, 4, 2)
-PLE_ATTN_KERNEL(128, 1, 3)
-PLE_ATTN_KERNEL(128, 2, 2)
-PLE_ATTN_KERNEL(128, 4, 1)
-PLE_ATTN_KERNEL(256, 1, 2)
-PLE_ATTN_KERNEL(256, 2, 1)
+PLE_ATTN_SHAPES(PLE_ATTN_KERNEL)
 #undef PLE_ATTN_KERNEL
 
 // ---------------------------------------------------------------------------
@@ -539,10 +602,10 @@ __device__ __forceinline__ void attn_chunk_body(const Kv4AttentionArgs& a) {
     u32x4 kraw[D == 256 ? 2 : 1], vraw[D == 256 ? 2 : 1], vsc[Sh::WB];
     uint32_t ksc[D == 64 ? 1 : D / 64];
     bool bad_next = false;
+    PageWalk walk(a, table_row, head, begin + 16 * g, kTile / 16, end);
     auto load = [&](int t0) {
-        const int tg = t0 + 16 * g;
-        int grp = -1;
-        if (tg < end) grp = kv4_group(a.cache, table_row, head, tg >> 4);
+        const int grp = walk.number(t0 + 16 * g, end);
+        walk.fetch();
         bad_next = grp < 0;
         const int safe = grp < 0 ? 0 : grp;
         // keys: group n / 4, token 4 wave + n % 4 of it
@@ -631,6 +694,7 @@ __device__ __forceinline__ void attn_chunk_body(const Kv4AttentionArgs& a) {
 
     bool bad = false;
     if (begin < end) {
+        walk.fetch();
         load(begin);
         fill(begin, 0);
         bad = bad_next;
@@ -656,6 +720,14 @@ __device__ __forceinline__ void attn_chunk_body(const Kv4AttentionArgs& a) {
                     s[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, q[mt][k], s[mt][i], 0, 0, 0);
             }
         }
+        // four fragments on their way from LDS while a fifth is used
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int i = 0; i < 4 * Sh::KS - 4; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, MT, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 4 * MT, 0);
         Frag p[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -728,11 +800,16 @@ PLE_ATTN_KERNEL(128, 2)
 PLE_ATTN_KERNEL(256, 1)
 #undef PLE_ATTN_KERNEL
 
-// Joins the splits of a row: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top).  One block a row.
-__global__ __launch_bounds__(kAttnThreads) void kv4_attention_join_kernel(Kv4AttentionArgs a) {
-    __shared__ float weight[kMostSplits], sum[kAttnThreads * 4];
-    const int64_t orow = blockIdx.x, rows = a.batch.num_tokens * a.num_q_heads;
+// Joins the splits of a row: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top).  Few splits: a wave a row
+// (WAVES = 1), four rows a block; many: four waves a row, each with a quarter of the splits, joined through LDS.
+template <int D, int WAVES>
+__device__ __forceinline__ void attn_join_body(const Kv4AttentionArgs& a) {
+    constexpr int E = D / 64;  // elements of a lane
+    __shared__ float part[WAVES == 1 ? 1 : WAVES * D], part_l[WAVES];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t rows = a.batch.num_tokens * a.num_q_heads;
+    const int64_t orow = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
+    if (orow >= rows) return;
     const int64_t t = orow / a.num_q_heads;
     const int hq = (int)(orow - t * a.num_q_heads), head = hq / a.group;
     int r;
@@ -746,44 +823,61 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_attention_join_kernel(Kv4Att
     if (!attn_tile(a, r, row / a.rows, w)) return;
     const int splits = attn_splits(a, w);
     if (splits == 1) return;
-    const int D = a.cache.head_dim;
     const float* lse = a.part + rows * a.splits * D + orow * a.splits;
-    // every wave for itself: the largest lse, and the sum of the weights
-    float top = -__builtin_inff(), total = 0.f;
+    const float* src = a.part + orow * a.splits * D + lane * E;
+    float top = -__builtin_inff();
     for (int s = lane; s < splits; s += kWave) top = fmaxf(top, lse[s]);
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-    for (int s = lane; s < splits; s += kWave) {
-        const float x = lse[s], v = x == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(x - top);  // NaN stays
-        total += v;
-        if (wave == 0) weight[s] = v;
-    }
+    float total = 0.f, v[E];
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(total, d, kWave);
-    __syncthreads();
-    // D/4 threads a split, four elements each
-    const int per = D / 4, step = kAttnThreads / per, e4 = (threadIdx.x % per) * 4;
-    const float* src = a.part + orow * a.splits * D + e4;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int e = 0; e < E; ++e) v[e] = 0.f;
 #pragma unroll 8
-    for (int k = threadIdx.x / per; k < splits; k += step) {
-        const f32x4 x = *(const f32x4*)(src + (int64_t)k * D);
-        const float wt = weight[k];
+    for (int s = WAVES == 1 ? 0 : wave; s < splits; s += WAVES) {
+        const float l = lse[s], by = l == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(l - top);  // NaN stays
+        total += by;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = fmaf(x[e], wt, v[e]);
+        for (int e = 0; e < E; ++e) v[e] = fmaf(src[(int64_t)s * D + e], by, v[e]);
     }
-    *(f32x4*)(sum + threadIdx.x / per * D + e4) = v;
-    __syncthreads();
-    if ((int)threadIdx.x < D) {
-        const int d = threadIdx.x;
-        const float f = total == 0.f ? 0.f : a.cache.v_scale[head] / total;
-        float x = 0.f;
-        for (int k = 0; k < step; ++k) x += sum[k * D + d];
-        a.out[orow * D + d] = (uint16_t)pack_bf16x2(x * f, 0.f);
+    if constexpr (WAVES > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[wave * D + lane * E + e] = v[e];
+        if (lane == 0) part_l[wave] = total;
+        __syncthreads();
+        if (wave != 0) return;
+        total = 0.f;
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k) total += part_l[k];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            v[e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < WAVES; ++k) v[e] += part[k * D + lane * E + e];
+        }
     }
-    if (a.lse != nullptr && threadIdx.x == 0)
+    const float f = total == 0.f ? 0.f : a.cache.v_scale[head] / total;
+    uint16_t* dst = a.out + orow * D + lane * E;
+    if constexpr (E == 1) {
+        dst[0] = (uint16_t)pack_bf16x2(v[0] * f, 0.f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) ((uint32_t*)dst)[e / 2] = pack_bf16x2(v[e] * f, v[e + 1] * f);
+    }
+    if (a.lse != nullptr && lane == 0)
         a.lse[orow] = total == 0.f ? -__builtin_inff() : (top + log2f(total)) * 0.693147180559945309f;
 }
+
+#define PLE_ATTN_KERNEL(D, WAVES)                                                                          \
+    __global__ __launch_bounds__(256) void kv4_attention_join_##D##_##WAVES##_kernel(Kv4AttentionArgs a) { \
+        attn_join_body<D, WAVES>(a);                                                                       \
+    }
+PLE_ATTN_KERNEL(64, 1)
+PLE_ATTN_KERNEL(64, 4)
+PLE_ATTN_KERNEL(128, 1)
+PLE_ATTN_KERNEL(128, 4)
+PLE_ATTN_KERNEL(256, 1)
+PLE_ATTN_KERNEL(256, 4)
+#undef PLE_ATTN_KERNEL
 
 void plan_kv4_attention(Kv4AttentionArgs& a) {
     const int64_t T = a.batch.num_tokens, R = a.batch.num_reqs;
@@ -792,22 +886,25 @@ void plan_kv4_attention(Kv4AttentionArgs& a) {
     new_max = new_max < T ? new_max : T;
     int64_t len = a.batch.max_seq_len > 0 && a.batch.max_seq_len < cover ? a.batch.max_seq_len : cover;
     const int64_t rows = new_max * a.group;
-    const int most = a.cache.head_dim == 256 ? 32 : 64;
-    a.rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= most ? 64 : kChunkRows));
+    // up to 64 rows in tiles whose state fits the registers of two waves per SIMD
+    a.rows = rows <= 16 || (rows <= 64 && a.cache.head_dim == 256) ? 16 : (rows <= 64 ? 32 : kChunkRows);
     a.tiles = (int)((rows + a.rows - 1) / a.rows);
     if (a.window > 0) {
         const int64_t span = (int64_t)a.window + a.rows / a.group + 1 + 15;
         len = len < span ? len : span;
     }
-    // Splits where the query tiles alone leave CUs idle: enough for 512 blocks (two per CU), each with at least 1024
-    // tokens, below which a block's fixed cost and the joining kernel outweigh what a shorter loop saves.
+    // Splits where the query tiles alone leave CUs idle, each of at least 1024 tokens, below which a block's fixed cost
+    // and the joining kernel outweigh what a shorter loop saves.  Up to one block per CU: blocks of eight waves.
     const int64_t blocks = R * a.cache.num_kv_heads * a.tiles;
-    int64_t splits = blocks > 0 ? (512 + blocks - 1) / blocks : 1;
+    a.waves = blocks <= 256 && a.rows < kChunkRows ? 8 : 4;
+    const int64_t slots = a.waves == 8 ? 256 : (a.rows == 16 && a.cache.head_dim < 256 ? 768 : 512);
+    int64_t splits = blocks <= 0 ? 1 : (a.rows == kChunkRows ? (slots + blocks - 1) / blocks : slots / blocks);
     const int64_t most_splits = (len + 1023) / 1024;
     splits = splits < most_splits ? splits : most_splits;
     splits = splits < 1 ? 1 : (splits < kMostSplits - 1 ? splits : kMostSplits - 1);
     int64_t chunk = (len + splits - 1) / splits;
-    chunk = (chunk + kTile * kAttnWaves - 1) / (kTile * kAttnWaves) * (kTile * kAttnWaves);
+    const int64_t round = a.rows == kChunkRows ? kTile : kTile * a.waves;  // what a block goes through at a time
+    chunk = (chunk + round - 1) / round * round;
     a.chunk = (int)chunk;
     // (a range starts at a multiple of 16, up to 15 tokens before the first that is seen; the last split takes those)
     a.splits = (int)((len + chunk - 1) / chunk);
@@ -819,40 +916,42 @@ size_t kv4_attention_part_bytes(const Kv4AttentionArgs& a) {
     return (size_t)a.batch.num_tokens * a.num_q_heads * a.splits * (a.cache.head_dim + 1) * sizeof(float);
 }
 
-template <void (*FN)(Kv4AttentionArgs), int D>
-static hipError_t launch_chunk(const Kv4AttentionArgs& a, dim3 grid, hipStream_t s) {
-    constexpr int kLds = ChunkShape<D>::LDS;
-    static const hipError_t attr =
-        hipFuncSetAttribute((const void*)FN, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+template <void (*FN)(Kv4AttentionArgs), int LDS>
+static hipError_t launch_attention(const Kv4AttentionArgs& a, int threads, hipStream_t s) {
+    static const hipError_t attr = hipFuncSetAttribute((const void*)FN, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
     if (attr != hipSuccess) return attr;
-    hipLaunchKernelGGL(FN, grid, dim3(kAttnThreads), kLds, s, a);
+    const dim3 grid((unsigned)((int64_t)a.batch.num_reqs * a.cache.num_kv_heads * a.tiles), (unsigned)a.splits);
+    hipLaunchKernelGGL(FN, grid, dim3(threads), LDS, s, a);
     return hipGetLastError();
 }
 
 hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)a.batch.num_reqs * a.cache.num_kv_heads * a.tiles), (unsigned)a.splits);
-    const int D = a.cache.head_dim, MT = a.rows / 16;
-    if (a.rows == kChunkRows) {
-        const hipError_t e = D == 64    ? launch_chunk<kv4_attention_chunk_64_kernel, 64>(a, grid, s)
-                             : D == 128 ? launch_chunk<kv4_attention_chunk_128_kernel, 128>(a, grid, s)
-                                        : launch_chunk<kv4_attention_chunk_256_kernel, 256>(a, grid, s);
-        if (e != hipSuccess) return e;
-    }
-#define PLE_ATTN_LAUNCH(DD, MM) \
-    if (D == DD && MT == MM) hipLaunchKernelGGL(kv4_attention_##DD##_##MM##_kernel, grid, dim3(kAttnThreads), 0, s, a)
-    PLE_ATTN_LAUNCH(64, 1);
-    PLE_ATTN_LAUNCH(64, 2);
-    PLE_ATTN_LAUNCH(64, 4);
-    PLE_ATTN_LAUNCH(128, 1);
-    PLE_ATTN_LAUNCH(128, 2);
-    PLE_ATTN_LAUNCH(128, 4);
-    PLE_ATTN_LAUNCH(256, 1);
-    PLE_ATTN_LAUNCH(256, 2);
+    const int D = a.cache.head_dim, mt = a.rows / 16;
+    hipError_t e = hipErrorInvalidValue;
+    if (a.rows == kChunkRows)
+        e = D == 64    ? launch_attention<kv4_attention_chunk_64_kernel, ChunkShape<64>::LDS>(a, kAttnThreads, s)
+            : D == 128 ? launch_attention<kv4_attention_chunk_128_kernel, ChunkShape<128>::LDS>(a, kAttnThreads, s)
+                       : launch_attention<kv4_attention_chunk_256_kernel, ChunkShape<256>::LDS>(a, kAttnThreads, s);
+#define PLE_ATTN_LAUNCH(DD, MT, WAVES, OCC)                                                                             \
+    if (D == DD && mt == MT && a.waves == WAVES)                                                                        \
+        e = launch_attention<kv4_attention_##DD##_##MT##x##WAVES##_kernel, AttnShape<DD, WAVES>::LDS>(a, WAVES * kWave, s);
+    PLE_ATTN_SHAPES(PLE_ATTN_LAUNCH)
 #undef PLE_ATTN_LAUNCH
-    hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits <= 1) return e;
     const int64_t rows = a.batch.num_tokens * a.num_q_heads;
-    hipLaunchKernelGGL(kv4_attention_join_kernel, dim3((unsigned)rows), dim3(kAttnThreads), 0, s, a);
+    const bool few = a.splits <= 8;
+    const dim3 grid((unsigned)(few ? (rows + 3) / 4 : rows));
+#define PLE_ATTN_LAUNCH(DD)                                                                                          \
+    if (D == DD) {                                                                                                   \
+        if (few)                                                                                                     \
+            hipLaunchKernelGGL(kv4_attention_join_##DD##_1_kernel, grid, dim3(256), 0, s, a);                        \
+        else                                                                                                         \
+            hipLaunchKernelGGL(kv4_attention_join_##DD##_4_kernel, grid, dim3(256), 0, s, a);                        \
+    }
+    PLE_ATTN_LAUNCH(64)
+    PLE_ATTN_LAUNCH(128)
+    PLE_ATTN_LAUNCH(256)
+#undef PLE_ATTN_LAUNCH
     return hipGetLastError();
 }
 
