@@ -34,7 +34,7 @@ struct Kv4AttentionArgs {
     int64_t q_stride;
     uint16_t* out;
     float* lse;       // or NULL
-    float* part;      // partial outputs [rows][splits][D], then their lse [rows][splits] (splits > 1)
+    float* part;      // partial outputs and their lse: [rows][splits] (splits > 1) or [2 flat][128]
     int32_t num_q_heads;
     int32_t group;    // query heads per key head
     int32_t window;   // 0: none
@@ -42,10 +42,11 @@ struct Kv4AttentionArgs {
     int32_t rows;     // rows of a block's query tile
     int32_t waves;    // of a block
     int32_t tiles;    // query tiles per request and key head (grid)
+    int32_t flat;     // blocks that share the work of a few query tiles evenly (0: a block per query tile and split)
     int32_t chunk;    // tokens of the cache per split
     int32_t splits;   // most splits of any query tile (grid)
 };
-// The plan part of the arguments (rows, waves, tiles, chunk, splits), from sizes and hints alone.
+// The plan part of the arguments (rows, waves, tiles, flat, chunk, splits), from sizes and hints alone.
 void plan_kv4_attention(Kv4AttentionArgs& a);
 size_t kv4_attention_part_bytes(const Kv4AttentionArgs& a);
 hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t s);

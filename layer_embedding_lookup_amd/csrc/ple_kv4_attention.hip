@@ -49,12 +49,17 @@ struct AttnTile {
     int lo, hi;      // lo: first_seen rounded down to a group of 16
 };
 
-__device__ __forceinline__ bool attn_tile(const Kv4AttentionArgs& a, int r, int tile, AttnTile& w) {
+// Request r of the batch, its query tiles not yet looked at.
+__device__ __forceinline__ void attn_request(const Kv4AttentionArgs& a, int r, AttnTile& w) {
     int64_t q0, q1;
     carried_window(a.batch.query_start_loc, a.batch.num_tokens, r, nullptr, q0, q1);
     w.first = q0;
     w.n = (int)(q1 - q0);
     w.len = min(a.batch.seq_lens[r], a.batch.table_width * a.cache.page_size);
+}
+
+// Its query tile; false if it has no such tile.
+__device__ __forceinline__ bool attn_tile(const Kv4AttentionArgs& a, int tile, AttnTile& w) {
     w.row0 = tile * a.rows;
     w.row1 = min(w.row0 + a.rows, w.n * a.group);
     if (w.row0 >= w.row1) return false;
@@ -249,7 +254,8 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
     int r, head, tile;
     attn_block(a, r, head, tile);
     AttnTile w;
-    if (!attn_tile(a, r, tile, w)) return;
+    attn_request(a, r, w);
+    if (!attn_tile(a, tile, w)) return;
     const int splits = attn_splits(a, w);
     if (split >= splits) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -547,6 +553,9 @@ PLE_ATTN_SHAPES(PLE_ATTN_KERNEL)
 // each other's softmax (D = 256: one).
 // ---------------------------------------------------------------------------
 constexpr int kChunkRows = 128;
+constexpr int kFlatLeast = 8;        // cache tiles of a share at least
+constexpr int kFlatUnits = 4096;     // query tiles (of all heads and requests) up to which the work is cut into shares
+constexpr int kFlatJoinRows = 32;    // rows of a block of the joining kernel
 
 template <int D>
 struct ChunkShape {
@@ -558,22 +567,96 @@ struct ChunkShape {
     static constexpr int LDS = NAN_AT + 2 * kAttnWaves * kTile;
 };
 
+// Few query tiles, of requests of different lengths, leave CUs idle at the end.  Then the cache tiles of all query
+// tiles (at least one each), in the order request, key head, query tile, are one line that `flat` blocks cut into equal
+// shares.  A query tile that a cut goes through is joined by a second kernel: of its pieces the one that begins it is
+// partial result 2 * share + 1, every other 2 * share of its share.
+// A chunk of 1289 + 1455 tokens at 5403 and 2004: 308 us with a block a query tile (CUs busy for 53% of it).
+struct AttnFlat {
+    int tiles_of;  // lane r: the cache tiles of one head of request r
+    int before;    // and those of all heads of the requests before it
+    int total, quota;
+
+    static __device__ __forceinline__ int count(const AttnTile& w) { return max(1, (w.hi - w.lo + kTile - 1) / kTile); }
+    // the cache tiles of query tile t of w's request (0: it has no such tile)
+    static __device__ __forceinline__ int count(const Kv4AttentionArgs& a, int t, AttnTile& w) {
+        return t < a.tiles && attn_tile(a, t, w) ? count(w) : 0;
+    }
+
+    __device__ __forceinline__ explicit AttnFlat(const Kv4AttentionArgs& a) {
+        const int lane = threadIdx.x & 63;
+        tiles_of = 0;
+        if (a.tiles < 4 * a.batch.num_reqs) {  // a lane a request, or the wave for one after the other: what is shorter
+            if (lane < a.batch.num_reqs) {
+                AttnTile w;
+                attn_request(a, lane, w);
+                for (int t = 0, c; (c = count(a, t, w)) > 0; ++t) tiles_of += c;
+            }
+        } else {
+            for (int r = 0; r < a.batch.num_reqs; ++r) {
+                AttnTile w;
+                attn_request(a, r, w);
+                int sum = 0;
+                for (int t = lane, c; (c = count(a, t, w)) > 0; t += kWave) sum += c;
+#pragma unroll
+                for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
+                if (lane == r) tiles_of = sum;
+            }
+        }
+        const int heads = a.cache.num_kv_heads;
+        int sum = tiles_of * heads;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int x = __shfl_up(sum, d, kWave);
+            if (lane >= d) sum += x;
+        }
+        before = sum - tiles_of * heads;
+        total = __shfl(sum, kWave - 1, kWave);
+        quota = max(kFlatLeast, (total + a.flat - 1) / a.flat);
+    }
+    // The query tile that place `at` of the line lies in, how far in, and its number of cache tiles.
+    __device__ __forceinline__ void find(const Kv4AttentionArgs& a, int at, int& r, int& head, AttnTile& w, int& k0,
+                                         int& cnt) const {
+        const int lane = threadIdx.x & 63;
+        // the last request that begins at or before it and has tiles
+        r = 63 - (int)__builtin_clzll(__ballot(tiles_of > 0 && before <= at));
+        const int per = __builtin_amdgcn_readlane(tiles_of, r);
+        int in = at - __builtin_amdgcn_readlane(before, r);
+        head = in / per;
+        in -= head * per;
+        attn_request(a, r, w);
+        for (int t0 = 0;; t0 += kWave) {
+            const int c = count(a, t0 + lane, w);
+            int sum = c;
+#pragma unroll
+            for (int d = 1; d < kWave; d <<= 1) {
+                const int x = __shfl_up(sum, d, kWave);
+                if (lane >= d) sum += x;
+            }
+            const uint64_t past = __ballot(sum > in);
+            if (past != 0 || t0 + kWave >= a.tiles) {  // (always found: `in` lies below the request's sum)
+                const int l = past != 0 ? (int)__builtin_ctzll(past) : 0;
+                cnt = __builtin_amdgcn_readlane(c, l);
+                k0 = in - (__builtin_amdgcn_readlane(sum, l) - cnt);
+                attn_tile(a, t0 + l, w);
+                return;
+            }
+            in -= __builtin_amdgcn_readlane(sum, kWave - 1);
+        }
+    }
+};
+
+// Rows [w.row0, w.row1) against the cache's tokens [begin, end).  Results go to the call's outputs, or, with `part`, to
+// partial results: of row i (within the tile, or the output row if `by_row`) at place i * stride + at.
 template <int D>
-__device__ __forceinline__ void attn_chunk_body(const Kv4AttentionArgs& a) {
+__device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, const AttnTile& w, int r, int head, int begin,
+                                                 int end, float* part, float* part_lse, bool by_row, int64_t stride,
+                                                 int64_t at) {
     using Sh = ChunkShape<D>;
     constexpr int MT = 2;
     extern __shared__ __align__(16) char lds[];
-    const int split = blockIdx.y;
-    int r, head, tile;
-    attn_block(a, r, head, tile);
-    AttnTile w;
-    if (!attn_tile(a, r, tile, w)) return;
-    const int splits = attn_splits(a, w);
-    if (split >= splits) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    const int begin = w.lo + split * a.chunk;
-    const int end = split == splits - 1 ? w.hi : min(w.hi, begin + a.chunk);
     const int before = w.len - w.n;
     // what every row of the block sees
     const int common_lo = a.window > 0 ? max(0, before + (w.row1 - 1) / a.group - a.window + 1) : 0;
@@ -772,22 +855,59 @@ __device__ __forceinline__ void attn_chunk_body(const Kv4AttentionArgs& a) {
         const float lse2 = total == 0.f ? -__builtin_inff() : (m[mt] - kWeightShift) + log2f(total);
         const int i = row / a.group, hq = head * a.group + (row - i * a.group);
         const int64_t orow = (w.first + i) * a.num_q_heads + hq;
-        const float f = splits == 1 ? inv * vscale : inv;
+        const float f = part == nullptr ? inv * vscale : inv;
+        const int64_t place = (by_row ? orow : (int64_t)(row - w.row0)) * stride + at;
 #pragma unroll
         for (int b = 0; b < Sh::NB; ++b) {
             f32x4 x = o[mt][b] * f;
             if (nan_blocks[mt] >> b & 1u) x = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
-            if (splits == 1)
+            if (part == nullptr)
                 *(u32x2*)(a.out + orow * D + b * 16 + g * 4) = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
             else
-                *(f32x4*)(a.part + (orow * a.splits + split) * D + b * 16 + g * 4) = x;
+                *(f32x4*)(part + place * D + b * 16 + g * 4) = x;
         }
         if (g == 0) {
-            if (splits > 1)
-                a.part[a.batch.num_tokens * a.num_q_heads * a.splits * D + orow * a.splits + split] = lse2;
+            if (part != nullptr)
+                part_lse[place] = lse2;
             else if (a.lse != nullptr)
                 a.lse[orow] = lse2 * 0.693147180559945309f;
         }
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void attn_chunk_body(const Kv4AttentionArgs& a) {
+    AttnTile w;
+    if (a.flat == 0) {
+        const int split = blockIdx.y;
+        int r, head, tile;
+        attn_block(a, r, head, tile);
+        attn_request(a, r, w);
+        if (!attn_tile(a, tile, w)) return;
+        const int splits = attn_splits(a, w);
+        if (split >= splits) return;
+        const int begin = w.lo + split * a.chunk;
+        const int end = split == splits - 1 ? w.hi : min(w.hi, begin + a.chunk);
+        attn_chunk_piece<D>(a, w, r, head, begin, end, splits > 1 ? a.part : nullptr,
+                            a.part + a.batch.num_tokens * a.num_q_heads * a.splits * D, true, a.splits, split);
+        return;
+    }
+    const AttnFlat f(a);
+    // blocks of an XCD (block number mod 8) take neighbouring shares, which read the same heads
+    const int share = (a.flat & 7) == 0 ? (int)(blockIdx.x & 7) * (a.flat >> 3) + (int)(blockIdx.x >> 3) : (int)blockIdx.x;
+    int at = share * f.quota;
+    const int stop = min(f.total, at + f.quota);
+    float* const lse = a.part + (int64_t)2 * a.flat * kChunkRows * D;
+    for (bool again = false; at < stop; again = true) {
+        int r, head, k0, count;
+        f.find(a, at, r, head, w, k0, count);
+        const int take = max(1, min(count - k0, stop - at));
+        const int begin = w.lo + k0 * kTile, end = min(w.hi, begin + take * kTile);
+        const bool whole = take == count;
+        if (again) __syncthreads();  // the last piece's reads of LDS
+        attn_chunk_piece<D>(a, w, r, head, begin, end, whole ? nullptr : a.part, lse, false, 1,
+                            (int64_t)(2 * share + (k0 == 0)) * kChunkRows);
+        at += take;
     }
 }
 
@@ -799,6 +919,24 @@ PLE_ATTN_KERNEL(64, 2)
 PLE_ATTN_KERNEL(128, 2)
 PLE_ATTN_KERNEL(256, 1)
 #undef PLE_ATTN_KERNEL
+
+// A joined row: v (E elements of each lane) over the weights' sum.
+template <int D>
+__device__ __forceinline__ void attn_join_store(const Kv4AttentionArgs& a, int64_t orow, float top, float total, float vscale,
+                                                const float (&v)[D / 64]) {
+    constexpr int E = D / 64;
+    const int lane = threadIdx.x & 63;
+    const float f = total == 0.f ? 0.f : vscale / total;
+    uint16_t* dst = a.out + orow * D + lane * E;
+    if constexpr (E == 1) {
+        dst[0] = (uint16_t)pack_bf16x2(v[0] * f, 0.f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) ((uint32_t*)dst)[e / 2] = pack_bf16x2(v[e] * f, v[e + 1] * f);
+    }
+    if (a.lse != nullptr && lane == 0)
+        a.lse[orow] = total == 0.f ? -__builtin_inff() : (top + log2f(total)) * 0.693147180559945309f;
+}
 
 // Joins the splits of a row: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top).  Few splits: a wave a row
 // (WAVES = 1), four rows a block; many: four waves a row, each with a quarter of the splits, joined through LDS.
@@ -816,11 +954,10 @@ __device__ __forceinline__ void attn_join_body(const Kv4AttentionArgs& a) {
     int64_t start;
     wave_find_request(a.batch.query_start_loc, a.batch.num_reqs, t, t, 1, 0, lane, r, start);
     AttnTile w;
-    int64_t q0, q1;
-    carried_window(a.batch.query_start_loc, a.batch.num_tokens, r, nullptr, q0, q1);
-    if (t < q0 || t >= q1) return;
-    const int row = (int)(t - q0) * a.group + (hq - head * a.group);
-    if (!attn_tile(a, r, row / a.rows, w)) return;
+    attn_request(a, r, w);
+    if (t < w.first || t >= w.first + w.n) return;
+    const int row = (int)(t - w.first) * a.group + (hq - head * a.group);
+    if (!attn_tile(a, row / a.rows, w)) return;
     const int splits = attn_splits(a, w);
     if (splits == 1) return;
     const float* lse = a.part + rows * a.splits * D + orow * a.splits;
@@ -855,16 +992,7 @@ __device__ __forceinline__ void attn_join_body(const Kv4AttentionArgs& a) {
             for (int k = 0; k < WAVES; ++k) v[e] += part[k * D + lane * E + e];
         }
     }
-    const float f = total == 0.f ? 0.f : a.cache.v_scale[head] / total;
-    uint16_t* dst = a.out + orow * D + lane * E;
-    if constexpr (E == 1) {
-        dst[0] = (uint16_t)pack_bf16x2(v[0] * f, 0.f);
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; e += 2) ((uint32_t*)dst)[e / 2] = pack_bf16x2(v[e] * f, v[e + 1] * f);
-    }
-    if (a.lse != nullptr && lane == 0)
-        a.lse[orow] = total == 0.f ? -__builtin_inff() : (top + log2f(total)) * 0.693147180559945309f;
+    attn_join_store<D>(a, orow, top, total, a.cache.v_scale[head], v);
 }
 
 #define PLE_ATTN_KERNEL(D, WAVES)                                                                          \
@@ -877,6 +1005,61 @@ PLE_ATTN_KERNEL(128, 1)
 PLE_ATTN_KERNEL(128, 4)
 PLE_ATTN_KERNEL(256, 1)
 PLE_ATTN_KERNEL(256, 4)
+#undef PLE_ATTN_KERNEL
+
+// Joins the pieces of the query tiles that the shares' borders cut.  Blocks: query tile, 32 of its rows; a wave a row.
+template <int D>
+__device__ __forceinline__ void attn_flat_join_body(const Kv4AttentionArgs& a) {
+    constexpr int E = D / 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int r, head, tile;
+    attn_block(a, r, head, tile);
+    AttnTile w;
+    attn_request(a, r, w);
+    if (!attn_tile(a, tile, w)) return;
+    if (w.row0 + (int)blockIdx.y * kFlatJoinRows >= w.row1) return;
+    const int count = AttnFlat::count(w);
+    const AttnFlat f(a);
+    int sum = 0;
+    {
+        AttnTile u = w;
+        for (int t = lane; t < tile; t += kWave) sum += AttnFlat::count(a, t, u);
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
+    }
+    const int at = __builtin_amdgcn_readlane(f.before, r) + head * __builtin_amdgcn_readlane(f.tiles_of, r) + sum;
+    const int s0 = at / f.quota, pieces = (at + count - 1) / f.quota - s0 + 1;
+    if (pieces == 1) return;
+    const float* const all_lse = a.part + (int64_t)2 * a.flat * kChunkRows * D;
+    const float vscale = a.cache.v_scale[head];
+    for (int i = wave; i < kFlatJoinRows; i += kAttnWaves) {
+        const int in = (int)blockIdx.y * kFlatJoinRows + i, row = w.row0 + in;
+        if (row >= w.row1) break;
+        float top = -__builtin_inff();
+        for (int k = 0; k < pieces; ++k)
+            top = fmaxf(top, all_lse[(int64_t)(2 * (s0 + k) + (k == 0)) * kChunkRows + in]);
+        float total = 0.f, v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = 0.f;
+        for (int k = 0; k < pieces; ++k) {
+            const int64_t place = (int64_t)(2 * (s0 + k) + (k == 0)) * kChunkRows + in;
+            const float l = all_lse[place], by = l == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(l - top);  // NaN stays
+            total += by;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = fmaf(a.part[place * D + lane * E + e], by, v[e]);
+        }
+        const int t = row / a.group, hq = head * a.group + (row - t * a.group);
+        attn_join_store<D>(a, (w.first + t) * a.num_q_heads + hq, top, total, vscale, v);
+    }
+}
+
+#define PLE_ATTN_KERNEL(D)                                                                            \
+    __global__ __launch_bounds__(256) void kv4_attention_flat_join_##D##_kernel(Kv4AttentionArgs a) { \
+        attn_flat_join_body<D>(a);                                                                    \
+    }
+PLE_ATTN_KERNEL(64)
+PLE_ATTN_KERNEL(128)
+PLE_ATTN_KERNEL(256)
 #undef PLE_ATTN_KERNEL
 
 void plan_kv4_attention(Kv4AttentionArgs& a) {
@@ -896,6 +1079,16 @@ void plan_kv4_attention(Kv4AttentionArgs& a) {
     // Splits where the query tiles alone leave CUs idle, each of at least 1024 tokens, below which a block's fixed cost
     // and the joining kernel outweigh what a shorter loop saves.  Up to one block per CU: blocks of eight waves.
     const int64_t blocks = R * a.cache.num_kv_heads * a.tiles;
+    // (the line's length has to fit 32 bits whatever the hints say)
+    if (a.rows == kChunkRows && R <= kWave && blocks > 0 && blocks <= kFlatUnits &&
+        blocks * (cover / kTile + 2) < ((int64_t)1 << 31)) {
+        const int64_t most = blocks * ((len + kTile - 1) / kTile + 1), slots = a.cache.head_dim == 256 ? 256 : 512;
+        const int64_t shares = (most + kFlatLeast - 1) / kFlatLeast;
+        a.flat = (int)(shares < slots ? shares : slots);
+        a.waves = kAttnWaves;
+        a.splits = 1;
+        return;
+    }
     a.waves = blocks <= 256 && a.rows < kChunkRows ? 8 : 4;
     const int64_t slots = a.waves == 8 ? 256 : (a.rows == 16 && a.cache.head_dim < 256 ? 768 : 512);
     int64_t splits = blocks <= 0 ? 1 : (a.rows == kChunkRows ? (slots + blocks - 1) / blocks : slots / blocks);
@@ -912,6 +1105,7 @@ void plan_kv4_attention(Kv4AttentionArgs& a) {
 }
 
 size_t kv4_attention_part_bytes(const Kv4AttentionArgs& a) {
+    if (a.flat > 0) return (size_t)2 * a.flat * kChunkRows * (a.cache.head_dim + 1) * sizeof(float);
     if (a.splits <= 1) return 0;
     return (size_t)a.batch.num_tokens * a.num_q_heads * a.splits * (a.cache.head_dim + 1) * sizeof(float);
 }
@@ -920,7 +1114,8 @@ template <void (*FN)(Kv4AttentionArgs), int LDS>
 static hipError_t launch_attention(const Kv4AttentionArgs& a, int threads, hipStream_t s) {
     static const hipError_t attr = hipFuncSetAttribute((const void*)FN, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
     if (attr != hipSuccess) return attr;
-    const dim3 grid((unsigned)((int64_t)a.batch.num_reqs * a.cache.num_kv_heads * a.tiles), (unsigned)a.splits);
+    const int64_t units = (int64_t)a.batch.num_reqs * a.cache.num_kv_heads * a.tiles;
+    const dim3 grid((unsigned)(a.flat > 0 ? a.flat : units), (unsigned)a.splits);
     hipLaunchKernelGGL(FN, grid, dim3(threads), LDS, s, a);
     return hipGetLastError();
 }
@@ -937,6 +1132,16 @@ hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t s) {
         e = launch_attention<kv4_attention_##DD##_##MT##x##WAVES##_kernel, AttnShape<DD, WAVES>::LDS>(a, WAVES * kWave, s);
     PLE_ATTN_SHAPES(PLE_ATTN_LAUNCH)
 #undef PLE_ATTN_LAUNCH
+    if (e == hipSuccess && a.flat > 0) {
+        const dim3 grid((unsigned)((int64_t)a.batch.num_reqs * a.cache.num_kv_heads * a.tiles), kChunkRows / kFlatJoinRows);
+        if (D == 64)
+            hipLaunchKernelGGL(kv4_attention_flat_join_64_kernel, grid, dim3(256), 0, s, a);
+        else if (D == 128)
+            hipLaunchKernelGGL(kv4_attention_flat_join_128_kernel, grid, dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL(kv4_attention_flat_join_256_kernel, grid, dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
     if (e != hipSuccess || a.splits <= 1) return e;
     const int64_t rows = a.batch.num_tokens * a.num_q_heads;
     const bool few = a.splits <= 8;

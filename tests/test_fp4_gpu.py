@@ -242,6 +242,36 @@ def test_attention(D, Hq, H, page, news, lens, window, hints):
     check_attention(cache, q, qsl, seq, window, **kw)
 
 
+@pytest.mark.parametrize("D,Hq,H,page,news,lens,window", [
+    (128, 8, 2, 64, [150, 0, 40, 129], [2500, 3, 1700, 129], 0), (64, 4, 1, 16, [300, 70], [1900, 2600], 0),
+    (256, 4, 2, 32, [33, 200], [2049, 260], 0), (128, 16, 2, 48, [90, 41], [1500, 2200], 700),
+    (128, 8, 1, 16, [20] * 65, [20 + 9 * i for i in range(65)], 0), (64, 4, 2, 16, [3, 40] * 20, [64, 200] * 20, 0),
+    (128, 2, 1, 16, [100], [4500], 0)])
+def test_attention_chunks_of_ragged_lengths(D, Hq, H, page, news, lens, window):
+    """Query tiles cut into pieces at any place, whole ones between them, requests without tokens; more requests than
+    lanes of a wave."""
+    print(f"chunks D={D} Hq={Hq} H={H} page={page} news={news[:4]} lens={lens[:4]} window={window}", flush=True)
+    g = gen(D + Hq + sum(lens))
+    cache = U.Cache(g, lens, H=H, D=D, page=page)
+    qsl, seq, _ = batch(news, lens, cache)
+    q = (1.5 * torch.randn((int(qsl[-1]), Hq, D), generator=g)).to(BF)
+    check_attention(cache, q, qsl, seq, window, max_request_tokens=max(news), max_seq_len=max(lens))
+
+
+def test_attention_chunk_rows_that_see_nothing():
+    """As below, with enough new tokens for the many-row kernel."""
+    g = gen(20)
+    lens = [30, 0, 700, -5]
+    cache = U.Cache(g, lens, H=1, D=128, page=16)
+    cache.table[2, :] = -1
+    qsl, seq = torch.tensor([0, 60, 80, 150, 190], dtype=torch.int32), torch.tensor(lens, dtype=torch.int32)
+    q = torch.randn((190, 4, 128), generator=g).to(BF)
+    out, lse = run_attention(cache, q, qsl, seq)
+    assert (lse[:30] == -math.inf).all() and (lse[60:] == -math.inf).all() and (out[:30] == 0).all() and (out[60:] == 0).all()
+    want, want_lse, tol, tol_lse = U.attention(cache, q[30:60], torch.tensor([0, 30]), seq[:1])
+    assert ((out[30:60] - want).abs() <= tol).all() and ((lse[30:60] - want_lse).abs() <= tol_lse).all()
+
+
 def test_attention_rows_that_see_nothing():
     """More new tokens than the sequence holds (rows before position 0), an empty sequence, a sequence of bad pages."""
     g = gen(11)
