@@ -202,47 +202,69 @@ __device__ __forceinline__ void attn_queries(const Kv4AttentionArgs& a, const At
     }
 }
 
-// The weights of one tile for a row: s (products, lane (n, g) holding tokens tg .. tg + 15) becomes the fp16 weights
-// p; m, l and o (the row's running maximum, sum and outputs) move on.  `some`: not every row sees the whole tile.
-template <int NB>
-__device__ __forceinline__ void attn_softmax(f32x4 (&s)[4], float qs, bool some, bool bad, int tg, int see_lo, int see_hi,
-                                             float& m, float& l, f32x4 (&o)[NB], Frag (&p)[2]) {
+// max over the four lanes n, n + 16, n + 32, n + 48
+__device__ __forceinline__ float quad_max(float x) {
+    typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+    u2 w = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    w = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+}
+
+// The weights of one tile: s (products, lane (n, g) holding tokens tg .. tg + 15 of MT rows) becomes the fp16 weights p;
+// m, l and o (the rows' running maxima, sums and outputs) move on.  `some`: not every row sees the whole tile.
+template <int NB, int MT>
+__device__ __forceinline__ void attn_softmax(f32x4 (&s)[MT][4], const float (&qs)[MT], bool some, bool bad, int tg,
+                                             const int (&see_lo)[MT], const int (&see_hi)[MT], float (&m)[MT], float (&l)[MT],
+                                             f32x4 (&o)[MT][NB], Frag (&p)[MT][2]) {
     if (some) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int tok = tg + 4 * i + e;
+                    if (bad || tok < see_lo[mt] || tok >= see_hi[mt]) s[mt][i][e] = -__builtin_inff();
+                }
+    }
+    float mn[MT];
+    bool up = false;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        float top = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int tok = tg + 4 * i + e;
-                if (bad || tok < see_lo || tok >= see_hi) s[i][e] = -__builtin_inff();
-            }
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, s[mt][i][e]);
+        mn[mt] = fmaxf(m[mt], quad_max(top) * qs[mt]);  // (qs > 0)
+        up |= mn[mt] > m[mt] + kSlack;
     }
-    float top = -__builtin_inff();
+    if (__ballot(up) != 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int mt = 0; mt < MT; ++mt) {
+            const float by = m[mt] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m[mt] - mn[mt]);
+            l[mt] *= by;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i][e]);
-    top = fmaxf(top, __shfl_xor(top, 16, kWave));
-    top = fmaxf(top, __shfl_xor(top, 32, kWave));
-    const float mn = fmaxf(m, top * qs);  // (qs > 0)
-    if (__ballot(mn > m + kSlack) != 0) {
-        const float by = m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - mn);
-        l *= by;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) o[b] *= by;
-        m = mn;
-    }
-    const float sub = m == -__builtin_inff() ? 0.f : kWeightShift - m;
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-            const float x = __builtin_amdgcn_exp2f(fmaf(s[i][e], qs, sub));
-            const float y = __builtin_amdgcn_exp2f(fmaf(s[i][e + 1], qs, sub));
-            sum += x + y;
-            p[i >> 1].p[(i & 1) * 2 + e / 2] = f16x2{(_Float16)x, (_Float16)y};
+            for (int b = 0; b < NB; ++b) o[mt][b] *= by;
+            m[mt] = mn[mt];
         }
-    l += sum;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const float sub = m[mt] == -__builtin_inff() ? 0.f : kWeightShift - m[mt];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(s[mt][i][e], qs[mt], sub));
+                const float y = __builtin_amdgcn_exp2f(fmaf(s[mt][i][e + 1], qs[mt], sub));
+                sum += x + y;
+                p[mt][i >> 1].p[(i & 1) * 2 + e / 2] = f16x2{(_Float16)x, (_Float16)y};
+            }
+        l[mt] += sum;
+    }
 }
 
 template <int D, int MT, int WAVES>
@@ -405,9 +427,7 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
 
         // lane (n, g) holds tokens 16 g .. 16 g + 15 of its row, in order
         Frag p[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            attn_softmax<Sh::NB>(s[mt], qs[mt], some, bad, tg, see_lo[mt], see_hi[mt], m[mt], l[mt], o[mt], p[mt]);
+        attn_softmax<Sh::NB, MT>(s, qs, some, bad, tg, see_lo, see_hi, m, l, o, p);
 
         // O^T += V^T P^T
 #pragma unroll
@@ -553,7 +573,8 @@ PLE_ATTN_SHAPES(PLE_ATTN_KERNEL)
 // each other's softmax (D = 256: one).
 // ---------------------------------------------------------------------------
 constexpr int kChunkRows = 128;
-constexpr int kFlatLeast = 8;        // cache tiles of a share at least
+constexpr int kFlatLeast = 8;        // places of a share at least
+constexpr int kFlatStart = 4;        // places that beginning a query tile counts for (queries in, results out)
 constexpr int kFlatUnits = 4096;     // query tiles (of all heads and requests) up to which the work is cut into shares
 constexpr int kFlatJoinRows = 32;    // rows of a block of the joining kernel
 
@@ -569,35 +590,44 @@ struct ChunkShape {
 
 // Few query tiles, of requests of different lengths, leave CUs idle at the end.  Then the cache tiles of all query
 // tiles (at least one each), in the order request, key head, query tile, are one line that `flat` blocks cut into equal
-// shares.  A query tile that a cut goes through is joined by a second kernel: of its pieces the one that begins it is
-// partial result 2 * share + 1, every other 2 * share of its share.
+// shares; a query tile has kFlatStart places in front of its cache tiles.  A query tile whose cache tiles a cut goes
+// through is joined by a second kernel: of its pieces the one that begins it is partial result 2 * share + 1, every
+// other 2 * share of its share.
 // A chunk of 1289 + 1455 tokens at 5403 and 2004: 308 us with a block a query tile (CUs busy for 53% of it).
 struct AttnFlat {
-    int tiles_of;  // lane r: the cache tiles of one head of request r
-    int before;    // and those of all heads of the requests before it
+    // of lane r:
+    int first, n, len;  // request r's first new token, new tokens, length
+    int tiles_of;       // the places of one of its heads
+    int before;         // and those of all heads of the requests before it
     int total, quota;
 
-    static __device__ __forceinline__ int count(const AttnTile& w) { return max(1, (w.hi - w.lo + kTile - 1) / kTile); }
-    // the cache tiles of query tile t of w's request (0: it has no such tile)
-    static __device__ __forceinline__ int count(const Kv4AttentionArgs& a, int t, AttnTile& w) {
-        return t < a.tiles && attn_tile(a, t, w) ? count(w) : 0;
+    __device__ __forceinline__ void request(int r, AttnTile& w) const {
+        w.first = __builtin_amdgcn_readlane(first, r);
+        w.n = __builtin_amdgcn_readlane(n, r);
+        w.len = __builtin_amdgcn_readlane(len, r);
     }
 
-    __device__ __forceinline__ explicit AttnFlat(const Kv4AttentionArgs& a) {
+    static __device__ __forceinline__ int count(const AttnTile& w) { return max(1, (w.hi - w.lo + kTile - 1) / kTile); }
+    // the places of query tile t of w's request (0: it has no such tile)
+    static __device__ __forceinline__ int places(const Kv4AttentionArgs& a, int t, AttnTile& w) {
+        return t < a.tiles && attn_tile(a, t, w) ? kFlatStart + count(w) : 0;
+    }
+
+    __device__ __forceinline__ void lay_out(const Kv4AttentionArgs& a) {
         const int lane = threadIdx.x & 63;
+        AttnTile w = {};
+        if (lane < a.batch.num_reqs) attn_request(a, lane, w);
+        first = (int)w.first;
+        n = w.n;
+        len = w.len;
         tiles_of = 0;
         if (a.tiles < 4 * a.batch.num_reqs) {  // a lane a request, or the wave for one after the other: what is shorter
-            if (lane < a.batch.num_reqs) {
-                AttnTile w;
-                attn_request(a, lane, w);
-                for (int t = 0, c; (c = count(a, t, w)) > 0; ++t) tiles_of += c;
-            }
+            for (int t = 0, c; (c = places(a, t, w)) > 0; ++t) tiles_of += c;
         } else {
             for (int r = 0; r < a.batch.num_reqs; ++r) {
-                AttnTile w;
-                attn_request(a, r, w);
+                request(r, w);
                 int sum = 0;
-                for (int t = lane, c; (c = count(a, t, w)) > 0; t += kWave) sum += c;
+                for (int t = lane, c; (c = places(a, t, w)) > 0; t += kWave) sum += c;
 #pragma unroll
                 for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
                 if (lane == r) tiles_of = sum;
@@ -614,7 +644,8 @@ struct AttnFlat {
         total = __shfl(sum, kWave - 1, kWave);
         quota = max(kFlatLeast, (total + a.flat - 1) / a.flat);
     }
-    // The query tile that place `at` of the line lies in, how far in, and its number of cache tiles.
+    // The query tile that place `at` of the line lies in, how far in (below 0: before its cache tiles), and the number
+    // of its cache tiles.
     __device__ __forceinline__ void find(const Kv4AttentionArgs& a, int at, int& r, int& head, AttnTile& w, int& k0,
                                          int& cnt) const {
         const int lane = threadIdx.x & 63;
@@ -624,9 +655,9 @@ struct AttnFlat {
         int in = at - __builtin_amdgcn_readlane(before, r);
         head = in / per;
         in -= head * per;
-        attn_request(a, r, w);
+        request(r, w);
         for (int t0 = 0;; t0 += kWave) {
-            const int c = count(a, t0 + lane, w);
+            const int c = places(a, t0 + lane, w);
             int sum = c;
 #pragma unroll
             for (int d = 1; d < kWave; d <<= 1) {
@@ -637,7 +668,8 @@ struct AttnFlat {
             if (past != 0 || t0 + kWave >= a.tiles) {  // (always found: `in` lies below the request's sum)
                 const int l = past != 0 ? (int)__builtin_ctzll(past) : 0;
                 cnt = __builtin_amdgcn_readlane(c, l);
-                k0 = in - (__builtin_amdgcn_readlane(sum, l) - cnt);
+                k0 = in - (__builtin_amdgcn_readlane(sum, l) - cnt) - kFlatStart;
+                cnt -= kFlatStart;
                 attn_tile(a, t0 + l, w);
                 return;
             }
@@ -646,12 +678,23 @@ struct AttnFlat {
     }
 };
 
-// Rows [w.row0, w.row1) against the cache's tokens [begin, end).  Results go to the call's outputs, or, with `part`, to
-// partial results: of row i (within the tile, or the output row if `by_row`) at place i * stride + at.
+// Instruction order for N fragments, each read from LDS and used by MT products: four reads go ahead of the products.
+template <int N, int MT>
+__device__ __forceinline__ void reads_ahead() {
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+    for (int i = 0; i < N - 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, MT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 4 * MT, 0);
+}
+
+// Rows [w.row0, w.row1) against the cache's tokens [begin, end).  Results go to the call's outputs (at < 0), or to the
+// partial results from row `at` on.
 template <int D>
 __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, const AttnTile& w, int r, int head, int begin,
-                                                 int end, float* part, float* part_lse, bool by_row, int64_t stride,
-                                                 int64_t at) {
+                                                 int end, int at) {
     using Sh = ChunkShape<D>;
     constexpr int MT = 2;
     extern __shared__ __align__(16) char lds[];
@@ -662,21 +705,6 @@ __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, cons
     const int common_lo = a.window > 0 ? max(0, before + (w.row1 - 1) / a.group - a.window + 1) : 0;
     const int common_hi = min(end, before + w.row0 / a.group + 1);
 
-    f16x8 q[MT][Sh::KS];
-    float qs[MT];
-    int see_lo[MT], see_hi[MT];
-    attn_queries<D, MT>(a, w, w.row0 + wave * (16 * MT), head, begin, end, q, qs, see_lo, see_hi);
-    f32x4 o[MT][Sh::NB];
-    float m[MT], l[MT];
-    uint32_t nan_blocks[MT] = {};
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        m[mt] = -__builtin_inff();
-        l[mt] = 0.f;
-#pragma unroll
-        for (int b = 0; b < Sh::NB; ++b) o[mt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-
     const int32_t* table_row = a.batch.page_table + (int64_t)r * a.batch.table_width;
     const uint32_t pick = (uint32_t)((n & 3) | ((4 + (n & 3)) << 8));
     char* const stage = lds + 2 * Sh::BUF + wave * Sh::STAGE;
@@ -686,13 +714,17 @@ __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, cons
     uint32_t ksc[D == 64 ? 1 : D / 64];
     bool bad_next = false;
     PageWalk walk(a, table_row, head, begin + 16 * g, kTile / 16, end);
-    auto load = [&](int t0) {
-        const int grp = walk.number(t0 + 16 * g, end);
+    int grp = -1;
+    int64_t kg = 0;  // of the tile to load next: this lane's group, and group n / 4 of the tile
+    auto aim = [&](int t0) {
+        grp = walk.number(t0 + 16 * g, end);
         walk.fetch();
+        kg = __shfl(max(grp, 0), (n >> 2) * 16, kWave);
+    };
+    auto load = [&]() {
         bad_next = grp < 0;
-        const int safe = grp < 0 ? 0 : grp;
-        // keys: group n / 4, token 4 wave + n % 4 of it
-        const int64_t kg = __shfl(safe, (n >> 2) * 16, kWave);
+        const int safe = max(grp, 0);
+        // keys: token 4 wave + n % 4 of the group
         const uint8_t* kc = a.cache.k_codes + kg * (8 * D) + (4 * wave + (n & 3)) * (D / 2) + g * (D == 64 ? 8 : 16);
         const uint8_t* ks = a.cache.k_scales + kg * D + (D == 64 ? g * 16 : g * 32) + wave * 4;
         // values: token `lane`, this wave's 8 WB bytes of it
@@ -715,6 +747,28 @@ __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, cons
         for (int b = 0; b < Sh::WB; ++b)
             vsc[b] = *(const u32x4*)(a.cache.v_scales + (int64_t)safe * D + (wave * Sh::WB + b) * 16);
     };
+    // the first tile is on its way before the queries are
+    if (begin < end) {
+        walk.fetch();
+        aim(begin);
+        load();
+        aim(begin + kTile);
+    }
+    f16x8 q[MT][Sh::KS];
+    float qs[MT];
+    int see_lo[MT], see_hi[MT];
+    attn_queries<D, MT>(a, w, w.row0 + wave * (16 * MT), head, begin, end, q, qs, see_lo, see_hi);
+    f32x4 o[MT][Sh::NB];
+    float m[MT], l[MT];
+    uint32_t nan_blocks[MT] = {};
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        m[mt] = -__builtin_inff();
+        l[mt] = 0.f;
+#pragma unroll
+        for (int b = 0; b < Sh::NB; ++b) o[mt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
     // whether some row does not see the whole tile (the same for the block: `bad` is the tile's four groups)
     auto partial = [&](int t0, bool bad) {
         return t0 < common_lo || t0 < begin || t0 + kTile > common_hi || __ballot(bad) != 0;
@@ -726,6 +780,12 @@ __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, cons
 #pragma unroll
         for (int b = 0; b < Sh::WB; ++b)
             *(u32x2*)(stage + lane * (8 * Sh::WB) + b * 8) = u32x2{vraw[b / 2][2 * (b & 1)], vraw[b / 2][2 * (b & 1) + 1]};
+        typedef int i32x2 __attribute__((ext_vector_type(2)));
+        i32x2 vc[Sh::WB];
+#pragma unroll
+        for (int b = 0; b < Sh::WB; ++b)
+            vc[b] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+                (__attribute__((address_space(3))) i32x2*)(stage + lane * (8 * Sh::WB) + b * 8));
 #pragma unroll
         for (int c = 0; c < (D == 256 ? 2 : 1); ++c) {
             const uint32_t two = D == 64 ? __builtin_amdgcn_perm(0u, ksc[0], pick)
@@ -761,15 +821,12 @@ __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, cons
         }
 #pragma unroll
         for (int b = 0; b < Sh::WB; ++b) {
-            typedef int i32x2 __attribute__((ext_vector_type(2)));
-            const i32x2 c = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-                (__attribute__((address_space(3))) i32x2*)(stage + lane * (8 * Sh::WB) + b * 8));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 Frag f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    f.p[e] = fp4_pair((uint32_t)c[h], e) * fp8_pair(vsc[b][2 * h + e / 2], (e & 1) != 0);
+                    f.p[e] = fp4_pair((uint32_t)vc[b][h], e) * fp8_pair(vsc[b][2 * h + e / 2], (e & 1) != 0);
                 *(u32x4*)(vb + (b * 2 + h) * 1024) = f.u;
             }
         }
@@ -777,8 +834,6 @@ __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, cons
 
     bool bad = false;
     if (begin < end) {
-        walk.fetch();
-        load(begin);
         fill(begin, 0);
         bad = bad_next;
     }
@@ -786,7 +841,7 @@ __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, cons
     for (int t0 = begin; t0 < end; t0 += kTile, buf ^= 1) {
         const bool more = t0 + kTile < end;
         __syncthreads();  // this tile is whole; every read of the other buffer is done
-        if (more) load(t0 + kTile);
+        if (more) load();
         const char* kb = lds + buf * Sh::BUF + lane * 16;
         const char* vb = kb + Sh::K_BYTES;
         const bool some = partial(t0, bad);
@@ -803,18 +858,10 @@ __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, cons
                     s[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, q[mt][k], s[mt][i], 0, 0, 0);
             }
         }
-        // four fragments on their way from LDS while a fifth is used
-        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-#pragma unroll
-        for (int i = 0; i < 4 * Sh::KS - 4; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, MT, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, 4 * MT, 0);
+        reads_ahead<4 * Sh::KS, MT>();
+        aim(t0 + 2 * kTile);
         Frag p[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            attn_softmax<Sh::NB>(s[mt], qs[mt], some, bad, t0 + 16 * g, see_lo[mt], see_hi[mt], m[mt], l[mt], o[mt], p[mt]);
+        attn_softmax<Sh::NB, MT>(s, qs, some, bad, t0 + 16 * g, see_lo, see_hi, m, l, o, p);
 #pragma unroll
         for (int b = 0; b < Sh::NB; ++b)
 #pragma unroll
@@ -824,6 +871,7 @@ __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, cons
                 for (int mt = 0; mt < MT; ++mt)
                     o[mt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[mt][h].v, o[mt][b], 0, 0, 0);
             }
+        reads_ahead<2 * Sh::NB, MT>();
         if (some) {
             uint32_t bits = 0;  // of token t0 + lane, all blocks
 #pragma unroll
@@ -855,59 +903,60 @@ __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, cons
         const float lse2 = total == 0.f ? -__builtin_inff() : (m[mt] - kWeightShift) + log2f(total);
         const int i = row / a.group, hq = head * a.group + (row - i * a.group);
         const int64_t orow = (w.first + i) * a.num_q_heads + hq;
-        const float f = part == nullptr ? inv * vscale : inv;
-        const int64_t place = (by_row ? orow : (int64_t)(row - w.row0)) * stride + at;
+        const float f = at < 0 ? inv * vscale : inv;
+        const int64_t place = at + (row - w.row0);
 #pragma unroll
         for (int b = 0; b < Sh::NB; ++b) {
             f32x4 x = o[mt][b] * f;
             if (nan_blocks[mt] >> b & 1u) x = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
-            if (part == nullptr)
+            if (at < 0)
                 *(u32x2*)(a.out + orow * D + b * 16 + g * 4) = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
             else
-                *(f32x4*)(part + place * D + b * 16 + g * 4) = x;
+                *(f32x4*)(a.part + place * D + b * 16 + g * 4) = x;
         }
         if (g == 0) {
-            if (part != nullptr)
-                part_lse[place] = lse2;
+            if (at >= 0)
+                a.part[(int64_t)2 * a.flat * kChunkRows * D + place] = lse2;
             else if (a.lse != nullptr)
                 a.lse[orow] = lse2 * 0.693147180559945309f;
         }
     }
 }
 
+// The pieces of share b of the line; the line without shares (flat = 0): one whole query tile.
 template <int D>
 __device__ __forceinline__ void attn_chunk_body(const Kv4AttentionArgs& a) {
     AttnTile w;
+    int r, head, tile, count, k0 = 0, line = 0, stop = 1;
+    // blocks of an XCD (block number mod 8) take neighbouring shares, which read the same heads
+    const int share = (a.flat & 7) == 0 ? (int)(blockIdx.x & 7) * (a.flat >> 3) + (int)(blockIdx.x >> 3) : (int)blockIdx.x;
+    AttnFlat f;
     if (a.flat == 0) {
-        const int split = blockIdx.y;
-        int r, head, tile;
         attn_block(a, r, head, tile);
         attn_request(a, r, w);
         if (!attn_tile(a, tile, w)) return;
-        const int splits = attn_splits(a, w);
-        if (split >= splits) return;
-        const int begin = w.lo + split * a.chunk;
-        const int end = split == splits - 1 ? w.hi : min(w.hi, begin + a.chunk);
-        attn_chunk_piece<D>(a, w, r, head, begin, end, splits > 1 ? a.part : nullptr,
-                            a.part + a.batch.num_tokens * a.num_q_heads * a.splits * D, true, a.splits, split);
-        return;
+    } else {
+        f.lay_out(a);
+        line = share * f.quota;
+        stop = min(f.total, line + f.quota);
     }
-    const AttnFlat f(a);
-    // blocks of an XCD (block number mod 8) take neighbouring shares, which read the same heads
-    const int share = (a.flat & 7) == 0 ? (int)(blockIdx.x & 7) * (a.flat >> 3) + (int)(blockIdx.x >> 3) : (int)blockIdx.x;
-    int at = share * f.quota;
-    const int stop = min(f.total, at + f.quota);
-    float* const lse = a.part + (int64_t)2 * a.flat * kChunkRows * D;
-    for (bool again = false; at < stop; again = true) {
-        int r, head, k0, count;
-        f.find(a, at, r, head, w, k0, count);
-        const int take = max(1, min(count - k0, stop - at));
-        const int begin = w.lo + k0 * kTile, end = min(w.hi, begin + take * kTile);
-        const bool whole = take == count;
-        if (again) __syncthreads();  // the last piece's reads of LDS
-        attn_chunk_piece<D>(a, w, r, head, begin, end, whole ? nullptr : a.part, lse, false, 1,
-                            (int64_t)(2 * share + (k0 == 0)) * kChunkRows);
-        at += take;
+    while (line < stop) {
+        int begin = w.lo, end = w.hi, at = -1, take = 1;
+        if (a.flat != 0) {
+            f.find(a, line, r, head, w, k0, count);
+            if (k0 < 0) {
+                line -= k0;
+                k0 = 0;
+                if (line >= stop) break;
+            }
+            take = max(1, min(count - k0, stop - line));
+            begin = w.lo + k0 * kTile;
+            end = min(w.hi, begin + take * kTile);
+            if (take != count) at = (2 * share + (k0 == 0)) * kChunkRows;
+        }
+        __syncthreads();  // the last piece's reads of LDS
+        attn_chunk_piece<D>(a, w, r, head, begin, end, at);
+        line += take;
     }
 }
 
@@ -1019,37 +1068,51 @@ __device__ __forceinline__ void attn_flat_join_body(const Kv4AttentionArgs& a) {
     if (!attn_tile(a, tile, w)) return;
     if (w.row0 + (int)blockIdx.y * kFlatJoinRows >= w.row1) return;
     const int count = AttnFlat::count(w);
-    const AttnFlat f(a);
+    AttnFlat f;
+    f.lay_out(a);
     int sum = 0;
     {
         AttnTile u = w;
-        for (int t = lane; t < tile; t += kWave) sum += AttnFlat::count(a, t, u);
+        for (int t = lane; t < tile; t += kWave) sum += AttnFlat::places(a, t, u);
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
     }
     const int at = __builtin_amdgcn_readlane(f.before, r) + head * __builtin_amdgcn_readlane(f.tiles_of, r) + sum;
-    const int s0 = at / f.quota, pieces = (at + count - 1) / f.quota - s0 + 1;
+    const int s0 = (at + kFlatStart) / f.quota, pieces = (at + kFlatStart + count - 1) / f.quota - s0 + 1;
     if (pieces == 1) return;
     const float* const all_lse = a.part + (int64_t)2 * a.flat * kChunkRows * D;
     const float vscale = a.cache.v_scale[head];
-    for (int i = wave; i < kFlatJoinRows; i += kAttnWaves) {
-        const int in = (int)blockIdx.y * kFlatJoinRows + i, row = w.row0 + in;
-        if (row >= w.row1) break;
-        float top = -__builtin_inff();
-        for (int k = 0; k < pieces; ++k)
-            top = fmaxf(top, all_lse[(int64_t)(2 * (s0 + k) + (k == 0)) * kChunkRows + in]);
-        float total = 0.f, v[E];
+    // a wave takes eight rows at once, so that their loads are in flight together (rows past the tile's end repeat its last)
+    constexpr int N = kFlatJoinRows / kAttnWaves;
+    const int in0 = (int)blockIdx.y * kFlatJoinRows + wave * N, most = w.row1 - w.row0 - 1;
+    float top[N], total[N], v[N][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = 0.f;
-        for (int k = 0; k < pieces; ++k) {
-            const int64_t place = (int64_t)(2 * (s0 + k) + (k == 0)) * kChunkRows + in;
-            const float l = all_lse[place], by = l == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(l - top);  // NaN stays
-            total += by;
+    for (int i = 0; i < N; ++i) {
+        top[i] = -__builtin_inff();
+        total[i] = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = fmaf(a.part[place * D + lane * E + e], by, v[e]);
+        for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+    }
+    for (int k = 0; k < pieces; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            top[i] = fmaxf(top[i], all_lse[(int64_t)(2 * (s0 + k) + (k == 0)) * kChunkRows + min(in0 + i, most)]);
+    for (int k = 0; k < pieces; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int64_t place = (int64_t)(2 * (s0 + k) + (k == 0)) * kChunkRows + min(in0 + i, most);
+            const float l = all_lse[place];
+            const float by = l == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(l - top[i]);  // NaN stays
+            total[i] += by;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[i][e] = fmaf(a.part[place * D + lane * E + e], by, v[i][e]);
         }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int row = w.row0 + in0 + i;
+        if (row >= w.row1) break;
         const int t = row / a.group, hq = head * a.group + (row - t * a.group);
-        attn_join_store<D>(a, (w.first + t) * a.num_q_heads + hq, top, total, vscale, v);
+        attn_join_store<D>(a, (w.first + t) * a.num_q_heads + hq, top[i], total[i], vscale, v[i]);
     }
 }
 
@@ -1081,8 +1144,8 @@ void plan_kv4_attention(Kv4AttentionArgs& a) {
     const int64_t blocks = R * a.cache.num_kv_heads * a.tiles;
     // (the line's length has to fit 32 bits whatever the hints say)
     if (a.rows == kChunkRows && R <= kWave && blocks > 0 && blocks <= kFlatUnits &&
-        blocks * (cover / kTile + 2) < ((int64_t)1 << 31)) {
-        const int64_t most = blocks * ((len + kTile - 1) / kTile + 1), slots = a.cache.head_dim == 256 ? 256 : 512;
+        blocks * (cover / kTile + 2 + kFlatStart) < ((int64_t)1 << 30)) {
+        const int64_t most = blocks * ((len + kTile - 1) / kTile + 1 + kFlatStart), slots = a.cache.head_dim == 256 ? 256 : 512;
         const int64_t shares = (most + kFlatLeast - 1) / kFlatLeast;
         a.flat = (int)(shares < slots ? shares : slots);
         a.waves = kAttnWaves;
@@ -1091,7 +1154,7 @@ void plan_kv4_attention(Kv4AttentionArgs& a) {
     }
     a.waves = blocks <= 256 && a.rows < kChunkRows ? 8 : 4;
     const int64_t slots = a.waves == 8 ? 256 : (a.rows == 16 && a.cache.head_dim < 256 ? 768 : 512);
-    int64_t splits = blocks <= 0 ? 1 : (a.rows == kChunkRows ? (slots + blocks - 1) / blocks : slots / blocks);
+    int64_t splits = blocks <= 0 || a.rows == kChunkRows ? 1 : slots / blocks;
     const int64_t most_splits = (len + 1023) / 1024;
     splits = splits < most_splits ? splits : most_splits;
     splits = splits < 1 ? 1 : (splits < kMostSplits - 1 ? splits : kMostSplits - 1);
