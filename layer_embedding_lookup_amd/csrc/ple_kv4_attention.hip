@@ -427,7 +427,11 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
 
         // lane (n, g) holds tokens 16 g .. 16 g + 15 of its row, in order
         Frag p[MT][2];
-        attn_softmax<Sh::NB, MT>(s, qs, some, bad, tg, see_lo, see_hi, m, l, o, p);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)  // (one after the other: fewer registers than all of them together)
+            attn_softmax<Sh::NB, 1>((f32x4(&)[1][4])s[mt], (float(&)[1])qs[mt], some, bad, tg, (int(&)[1])see_lo[mt],
+                                    (int(&)[1])see_hi[mt], (float(&)[1])m[mt], (float(&)[1])l[mt],
+                                    (f32x4(&)[1][Sh::NB])o[mt], (Frag(&)[1][2])p[mt]);
 
         // O^T += V^T P^T
 #pragma unroll

@@ -55,6 +55,34 @@ __device__ __forceinline__ void transpose4(u32x4& w) {
     w = u32x4{p[0], p[1], q[0], q[1]};
 }
 
+// The INT4 group scales of a step of 128 inputs.  Lane group g fetches only the one of inputs 32 g .. (scale | zero point
+// << 16; nothing past the last group), since a fetch touches 16 rows whatever its width; `groups_of` gives every lane all.
+template <int G>
+__device__ __forceinline__ uint32_t group_fetch(const void* scales, const uint8_t* zeros, int64_t row, int at, int groups) {
+    if (at >= groups) return 8u << 16;
+    return ((const uint16_t*)scales)[row + at] | (zeros == nullptr ? 8u : (uint32_t)zeros[row + at]) << 16;
+}
+template <int G>
+__device__ __forceinline__ void groups_of(uint32_t mine, uint32_t (&all)[128 / G]) {
+    typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+    if constexpr (G == 128) {
+        all[0] = mine;
+    } else {
+        const u2 h = __builtin_amdgcn_permlane32_swap(mine, mine, false, false);  // lane groups 0 1 0 1 and 2 3 2 3
+        if constexpr (G == 64) {
+            all[0] = h[0];
+            all[1] = h[1];
+        } else {
+            const u2 a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+            const u2 b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+            all[0] = a[0];
+            all[1] = a[1];
+            all[2] = b[0];
+            all[3] = b[1];
+        }
+    }
+}
+
 struct W4Args {
     const uint16_t* x;
     int64_t x_stride;
@@ -71,7 +99,7 @@ struct W4Args {
 template <int MT, int NT, int G>
 struct W4Step {
     u32x4 w[NT];
-    uint32_t scale[NT][G == 16 ? 1 : 128 / G];  // NVFP4: the lane's two block scales; INT4: bf16 scale | zero point << 16
+    uint32_t scale[NT];  // NVFP4: the lane's two block scales; INT4: group_fetch
     u32x4 x[MT][4];
 };
 
@@ -121,18 +149,9 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
         for (int nt = 0; nt < NT; ++nt) {
             s.w[nt] = in ? *(const u32x4*)(wrow[nt] + k0 / 2) : zero4;
             if constexpr (kNv) {
-                s.scale[nt][0] = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
+                s.scale[nt] = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
             } else {
-#pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
-                    const int at = k0 / G + j;
-                    uint32_t v = 8u << 16;
-                    if (at < groups) {
-                        v = ((const uint16_t*)a.scales)[srow[nt] + at];
-                        v |= (a.zeros == nullptr ? 8u : (uint32_t)a.zeros[srow[nt] + at]) << 16;
-                    }
-                    s.scale[nt][j] = v;
-                }
+                s.scale[nt] = group_fetch<G>(a.scales, a.zeros, srow[nt], (k0 + 32 * g) / G, groups);
             }
         }
 #pragma unroll
@@ -147,7 +166,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
         if constexpr (kNv) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const f32x2 sc = __builtin_amdgcn_cvt_pk_f32_fp8((int)s.scale[nt][0], false);
+                const f32x2 sc = __builtin_amdgcn_cvt_pk_f32_fp8((int)s.scale[nt], false);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     BFrag f;
@@ -162,9 +181,11 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 transpose4(s.w[nt]);  // word j: inputs k0 + 32 j + 8 g ..
+                uint32_t all[kGroups];
+                groups_of<G>(s.scale[nt], all);
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
-                    const float z = (float)(s.scale[nt][i] >> 16), sc = bf16_lo(s.scale[nt][i]);
+                    const float z = (float)(all[i] >> 16), sc = bf16_lo(all[i]);
                     f32x4 part[MT];
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) part[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -226,24 +247,26 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
     }
 }
 
-// Shapes of the few-token kernel: token tiles, feature tiles, waves, steps in flight.
-#define PLE_W4_SHAPES(X) X(1, 1, 8, 4) X(2, 1, 8, 2) X(4, 2, 8, 1) X(4, 4, 8, 1)
-#define PLE_W4_KERNEL(MT, NT, G, WAVES, DEPTH)                                                                        \
-    __global__ __launch_bounds__(WAVES * 64) void w4_rows_##MT##x##NT##_##G##_kernel(W4Args a) {                      \
+// Shapes of the few-token kernel: token tiles, feature tiles, waves, steps in flight, waves per SIMD that registers are
+// kept to (two blocks per CU for up to 32 tokens: 8192 x 4096 INT4, one token, 10.5 us, with four steps in flight and one block 14.1).
+#define PLE_W4_SHAPES(X) X(1, 1, 8, 2, 4) X(2, 1, 8, 1, 4) X(4, 1, 8, 2, 2) X(4, 2, 8, 1, 2) X(4, 4, 8, 1, 2)
+#define PLE_W4_KERNEL(MT, NT, G, WAVES, DEPTH, OCC)                                                                   \
+    __global__ __launch_bounds__(WAVES * 64, OCC) void w4_rows_##MT##x##NT##_##G##_kernel(W4Args a) {                 \
         w4_rows_body<MT, NT, G, WAVES, DEPTH>(a);                                                                     \
     }
-#define PLE_W4_KERNELS(MT, NT, WAVES, DEPTH)                                              \
-    PLE_W4_KERNEL(MT, NT, 16, WAVES, DEPTH) PLE_W4_KERNEL(MT, NT, 32, WAVES, DEPTH)       \
-    PLE_W4_KERNEL(MT, NT, 64, WAVES, DEPTH) PLE_W4_KERNEL(MT, NT, 128, WAVES, DEPTH)
+#define PLE_W4_KERNELS(MT, NT, WAVES, DEPTH, OCC)                                                   \
+    PLE_W4_KERNEL(MT, NT, 16, WAVES, DEPTH, OCC) PLE_W4_KERNEL(MT, NT, 32, WAVES, DEPTH, OCC)       \
+    PLE_W4_KERNEL(MT, NT, 64, WAVES, DEPTH, OCC) PLE_W4_KERNEL(MT, NT, 128, WAVES, DEPTH, OCC)
 PLE_W4_SHAPES(PLE_W4_KERNELS)
 
 // ---------------------------------------------------------------------------
-// Many tokens: bound by the products.  A block of four waves holds 128 tokens
-// x 256 features, a wave 128 x 64 as 8 x 4 accumulators of 16 x 16.  The
-// inputs go through LDS in slices of 128 (two slots), shared by the waves;
-// the codes do not: each wave dequantises its own 64 features in registers,
-// once for its 128 tokens, so LDS carries the inputs alone and dequantising
-// costs half of the VALU time that the products leave.
+// Many tokens: bound by the products and by dequantising between them.  A
+// block of four waves holds MT x 16 tokens x NT x 64 features, a wave all of
+// the tokens and NT x 16 features.  The inputs go through LDS in slices of
+// 128 (two slots), shared by the waves; the codes do not: each wave
+// dequantises its own features in registers, once for the block's tokens.
+// 64 tokens leave room for two blocks per CU, which cover each other's waits
+// and let one dequantise while the other multiplies.
 //
 // LDS layout of a slice: a token's 256 bytes are 16 chunks of 16 bytes, chunk
 // c at place c ^ (token % 16), so the 16 lanes of a fragment read (16 tokens,
@@ -251,109 +274,107 @@ PLE_W4_SHAPES(PLE_W4_KERNELS)
 // takes chunk 4 g + j (NVFP4: the lane's own 16 bytes of codes) or 4 j + g
 // (INT4: words swapped, so that a fragment's inputs lie in one group).
 // ---------------------------------------------------------------------------
-constexpr int kGemmT = 128, kGemmO = 256, kGemmThreads = 256;
-constexpr int kGemmSlot = kGemmT * 256;             // bytes of a slice
-constexpr int kGemmOutRow = kGemmO * 2 + 16;        // bytes of an output row in LDS
-constexpr int kGemmLds = 2 * kGemmSlot > kGemmT * kGemmOutRow ? 2 * kGemmSlot : kGemmT * kGemmOutRow;
+constexpr int kGemmThreads = 256;
+template <int MT, int NT>
+struct GemmShape {
+    static constexpr int T = 16 * MT, O = 64 * NT;
+    static constexpr int SLOT = T * 256;          // bytes of a slice
+    static constexpr int OUT_ROW = O * 2 + 16;    // bytes of an output row in LDS
+    static constexpr int LDS = 2 * SLOT > T * OUT_ROW ? 2 * SLOT : T * OUT_ROW;
+};
 
-template <int G>
+template <int G, int MT, int NT>
 __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
+    using Sh = GemmShape<MT, NT>;
     constexpr bool kNv = G == 16;
     constexpr int kGroups = kNv ? 1 : 128 / G;
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = lane & 15, g = lane >> 4;
-    const int tiles_t = (int)((a.T + kGemmT - 1) / kGemmT), tiles_o = (a.O + kGemmO - 1) / kGemmO;
+    const int tiles_t = (int)((a.T + Sh::T - 1) / Sh::T), tiles_o = (a.O + Sh::O - 1) / Sh::O;
     // neighbouring blocks of an XCD (block number mod 8) share features, so their codes come from its L2
     const int total = tiles_t * tiles_o;
     int lin = blockIdx.x;
     if ((total & 7) == 0) lin = (lin & 7) * (total >> 3) + (lin >> 3);
     const int to = lin / tiles_t, tt = lin - to * tiles_t;
-    const int64_t t0 = (int64_t)tt * kGemmT;
-    const int o0 = to * kGemmO + wave * 64;
+    const int64_t t0 = (int64_t)tt * Sh::T;
+    const int o0 = to * Sh::O + wave * (16 * NT);
     const int groups = a.K / (kNv ? 16 : G);
-    const uint8_t* wrow[4];
-    int64_t srow[4];
+    const uint8_t* wrow[NT];
+    int64_t srow[NT];
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
+    for (int nt = 0; nt < NT; ++nt) {
         const int64_t o = min(o0 + nt * 16 + n, a.O - 1);
         wrow[nt] = a.codes + o * (a.K / 2) + g * 16;
         srow[nt] = o * groups;
     }
     // this thread's chunks of a slice: token tid/16 + 16 i, chunk tid % 16
-    const uint16_t* xsrc[8];
+    const uint16_t* xsrc[MT];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < MT; ++i) {
         const int64_t t = t0 + (tid >> 4) + 16 * i;
         xsrc[i] = a.x + (t < a.T ? t : a.T - 1) * a.x_stride + (tid & 15) * 8;
     }
     char* const xdst = lds + (tid >> 4) * 256 + ((tid & 15) ^ (tid >> 4)) * 16;
 
     const u32x4 zero4 = {0u, 0u, 0u, 0u};
-    u32x4 w[4], xs[8];
-    uint32_t scale[4][kGroups];
+    u32x4 w[NT], xs[MT];
+    uint32_t scale[NT];
     auto load = [&](int k0) {
         const bool in = k0 + g * 32 < a.K;
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
             w[nt] = in ? *(const u32x4*)(wrow[nt] + k0 / 2) : zero4;
             if constexpr (kNv) {
-                scale[nt][0] = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
+                scale[nt] = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
             } else {
-#pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
-                    const int at = k0 / G + j;
-                    uint32_t v = 8u << 16;
-                    if (at < groups) {
-                        v = ((const uint16_t*)a.scales)[srow[nt] + at];
-                        v |= (a.zeros == nullptr ? 8u : (uint32_t)a.zeros[srow[nt] + at]) << 16;
-                    }
-                    scale[nt][j] = v;
-                }
+                scale[nt] = group_fetch<G>(a.scales, a.zeros, srow[nt], (k0 + 32 * g) / G, groups);
             }
         }
         const bool xin = k0 + (tid & 15) * 8 < a.K;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xs[i] = xin ? *(const u32x4*)(xsrc[i] + k0) : zero4;
+        for (int i = 0; i < MT; ++i) xs[i] = xin ? *(const u32x4*)(xsrc[i] + k0) : zero4;
     };
     auto put = [&](int slot) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) *(u32x4*)(xdst + slot * kGemmSlot + i * 4096) = xs[i];
+        for (int i = 0; i < MT; ++i) *(u32x4*)(xdst + slot * Sh::SLOT + i * 4096) = xs[i];
     };
 
-    f32x4 acc[8][4];
+    f32x4 acc[MT][NT];
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     load(0);
     put(0);
     const int steps = (a.K + 127) / 128;
     for (int st = 0; st < steps; ++st) {
         // this slice's codes as bf16
-        BFrag f[4][4];
-        float sc[4][kGroups];
+        BFrag f[NT][4];
+        float sc[NT][kGroups];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
             if constexpr (kNv) {
-                const f32x2 s2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)scale[nt][0], false);
+                const f32x2 s2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)scale[nt], false);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) nvfp4_frag(w[nt][j], s2[j >> 1], f[nt][j]);
             } else {
                 u32x4 t = w[nt];
                 transpose4(t);
+                uint32_t all[kGroups];
+                groups_of<G>(scale[nt], all);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) int4_frag(t[j], (float)(scale[nt][j / (G / 32)] >> 16), f[nt][j]);
+                for (int j = 0; j < 4; ++j) int4_frag(t[j], (float)(all[j / (G / 32)] >> 16), f[nt][j]);
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i) sc[nt][i] = bf16_lo(scale[nt][i]);
+                for (int i = 0; i < kGroups; ++i) sc[nt][i] = bf16_lo(all[i]);
             }
         }
         __syncthreads();  // slice st is whole; every read of the other slot is done
         if (st + 1 < steps) load((st + 1) * 128);
-        const char* slot = lds + (st & 1) * kGemmSlot + n * 256;
+        const char* slot = lds + (st & 1) * Sh::SLOT + n * 256;
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
+        for (int mt = 0; mt < MT; ++mt) {
             BFrag x[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -364,24 +385,27 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
                         acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j].v, f[nt][j].v, acc[mt][nt], 0, 0, 0);
             } else {
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
-                    f32x4 part[4];
+                    f32x4 part[NT];
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt) part[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int nt = 0; nt < NT; ++nt) part[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int j = i * (G / 32); j < (i + 1) * (G / 32); ++j)
 #pragma unroll
-                        for (int nt = 0; nt < 4; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
                             part[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j].v, f[nt][j].v, part[nt], 0, 0, 0);
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[mt][nt][e] = fmaf(part[nt][e], sc[nt][i], acc[mt][nt][e]);
                 }
+                // (few token tiles at a time: the partial sums of all of them would not fit the registers)
+                if constexpr (G < 128)
+                    if (mt % (G / 32) == G / 32 - 1) __builtin_amdgcn_sched_barrier(0);
             }
         }
         if (st + 1 < steps) put((st + 1) & 1);
@@ -391,69 +415,80 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
     const float ts = kNv ? a.tensor_scale[0] : 1.f;
     __syncthreads();
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                *(uint16_t*)(lds + (mt * 16 + g * 4 + e) * kGemmOutRow + (wave * 64 + nt * 16 + n) * 2) =
+                *(uint16_t*)(lds + (mt * 16 + g * 4 + e) * Sh::OUT_ROW + (wave * (16 * NT) + nt * 16 + n) * 2) =
                     (uint16_t)pack_bf16x2(acc[mt][nt][e] * ts, 0.f);
     __syncthreads();
-    const int ob = to * kGemmO;
+    const int ob = to * Sh::O;
     if (a.O % 8 == 0) {
-        for (int c = tid; c < kGemmT * (kGemmO / 8); c += kGemmThreads) {
-            const int row = c / (kGemmO / 8), col = (c % (kGemmO / 8)) * 8;
+        for (int c = tid; c < Sh::T * (Sh::O / 8); c += kGemmThreads) {
+            const int row = c / (Sh::O / 8), col = (c % (Sh::O / 8)) * 8;
             if (t0 + row < a.T && ob + col < a.O)
-                *(u32x4*)(a.out + (t0 + row) * a.O + ob + col) = *(const u32x4*)(lds + row * kGemmOutRow + col * 2);
+                *(u32x4*)(a.out + (t0 + row) * a.O + ob + col) = *(const u32x4*)(lds + row * Sh::OUT_ROW + col * 2);
         }
     } else {
-        for (int c = tid; c < kGemmT * kGemmO; c += kGemmThreads) {
-            const int row = c / kGemmO, col = c % kGemmO;
+        for (int c = tid; c < Sh::T * Sh::O; c += kGemmThreads) {
+            const int row = c / Sh::O, col = c % Sh::O;
             if (t0 + row < a.T && ob + col < a.O)
-                a.out[(t0 + row) * a.O + ob + col] = *(const uint16_t*)(lds + row * kGemmOutRow + col * 2);
+                a.out[(t0 + row) * a.O + ob + col] = *(const uint16_t*)(lds + row * Sh::OUT_ROW + col * 2);
         }
     }
 }
 
-#define PLE_W4_GEMM(G)                                                                     \
-    __global__ __launch_bounds__(kGemmThreads, 1) void w4_gemm_##G##_kernel(W4Args a) { \
-        w4_gemm_body<G>(a);                                                                \
+#define PLE_W4_GEMM(G, MT, NT, OCC)                                                                      \
+    __global__ __launch_bounds__(kGemmThreads, OCC) void w4_gemm_##MT##x##NT##_##G##_kernel(W4Args a) { \
+        w4_gemm_body<G, MT, NT>(a);                                                                      \
     }
-PLE_W4_GEMM(16)
-PLE_W4_GEMM(32)
-PLE_W4_GEMM(64)
-PLE_W4_GEMM(128)
+PLE_W4_GEMM(16, 4, 2, 2)
+PLE_W4_GEMM(32, 4, 2, 2)
+PLE_W4_GEMM(64, 4, 2, 2)
+PLE_W4_GEMM(128, 4, 2, 2)
+// 128 tokens; with groups of 32 or 64 their partial sums would not fit the registers of two blocks per CU
+PLE_W4_GEMM(16, 8, 2, 2)
+PLE_W4_GEMM(128, 8, 2, 2)
 #undef PLE_W4_GEMM
 
-template <void (*FN)(W4Args)>
+template <void (*FN)(W4Args), int MT, int NT>
 static hipError_t launch_gemm(const W4Args& a, hipStream_t s) {
+    using Sh = GemmShape<MT, NT>;
     static const hipError_t attr =
-        hipFuncSetAttribute((const void*)FN, hipFuncAttributeMaxDynamicSharedMemorySize, kGemmLds);
+        hipFuncSetAttribute((const void*)FN, hipFuncAttributeMaxDynamicSharedMemorySize, Sh::LDS);
     if (attr != hipSuccess) return attr;
-    const int64_t blocks = (a.T + kGemmT - 1) / kGemmT * ((a.O + kGemmO - 1) / kGemmO);
-    hipLaunchKernelGGL(FN, dim3((unsigned)blocks), dim3(kGemmThreads), kGemmLds, s, a);
+    const int64_t blocks = (a.T + Sh::T - 1) / Sh::T * ((a.O + Sh::O - 1) / Sh::O);
+    hipLaunchKernelGGL(FN, dim3((unsigned)blocks), dim3(kGemmThreads), Sh::LDS, s, a);
     return hipGetLastError();
 }
 
 hipError_t launch_w4_linear(const uint16_t* x, int64_t x_stride, const ple_w4_weight& w, int64_t T, uint16_t* out,
                             hipStream_t s) {
     const W4Args a = {x, x_stride, w.codes, w.scales, w.zeros, w.tensor_scale, T, w.out_dim, w.k_dim, out};
-    // the wide tiles where they give enough blocks
-    if (T > 64 && (T + kGemmT - 1) / kGemmT * ((w.out_dim + kGemmO - 1) / kGemmO) >= 128) {
+    // Tiles through LDS where there are enough of them for the CUs, below that blocks that split K between their waves
+    // (T = 256, K = 4096: 160 tiles NVFP4 35 us against 54, INT4 66..71 against 63..65; 192 tiles INT4 37 against 38).
+    const int64_t features = (w.out_dim + 127) / 128;
+    if (T > 64 && (T + 63) / 64 * features >= (w.group == 16 ? 144 : 192)) {
+        // 128 tokens a block where that leaves two blocks per CU (8192 x 4096 NVFP4: T = 1024 70 us against 92, T = 500,
+        // 256 blocks, 57 against 48)
+        const bool tall = (T + 127) / 128 * features >= 512;
         switch (w.group) {
-            case 16: return launch_gemm<w4_gemm_16_kernel>(a, s);
-            case 32: return launch_gemm<w4_gemm_32_kernel>(a, s);
-            case 64: return launch_gemm<w4_gemm_64_kernel>(a, s);
-            default: return launch_gemm<w4_gemm_128_kernel>(a, s);
+            case 16: return tall ? launch_gemm<w4_gemm_8x2_16_kernel, 8, 2>(a, s) : launch_gemm<w4_gemm_4x2_16_kernel, 4, 2>(a, s);
+            case 32: return launch_gemm<w4_gemm_4x2_32_kernel, 4, 2>(a, s);
+            case 64: return launch_gemm<w4_gemm_4x2_64_kernel, 4, 2>(a, s);
+            default: return tall ? launch_gemm<w4_gemm_8x2_128_kernel, 8, 2>(a, s) : launch_gemm<w4_gemm_4x2_128_kernel, 4, 2>(a, s);
         }
     }
     const int mt = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
-    const int nt = mt < 4 ? 1 : ((T + 63) / 64 * ((w.out_dim + 63) / 64) >= 192 ? 4 : 2);
+    // feature tiles of a block of 64 tokens: as many as still leave blocks for the CUs
+    const int64_t rows = (T + 63) / 64;
+    const int nt = mt < 4 || rows * ((w.out_dim + 31) / 32) <= 128 ? 1 : (rows * ((w.out_dim + 63) / 64) >= 192 ? 4 : 2);
     const unsigned blocks = (unsigned)((w.out_dim + 16 * nt - 1) / (16 * nt) * ((T + 16 * mt - 1) / (16 * mt)));
 #define PLE_W4_LAUNCH(MT, NT, G, WAVES) \
     if (mt == MT && nt == NT && w.group == G)  \
         hipLaunchKernelGGL(w4_rows_##MT##x##NT##_##G##_kernel, dim3(blocks), dim3(WAVES * 64), 0, s, a);
-#define PLE_W4_LAUNCHES(MT, NT, WAVES, DEPTH)                                     \
+#define PLE_W4_LAUNCHES(MT, NT, WAVES, DEPTH, OCC)                                \
     PLE_W4_LAUNCH(MT, NT, 16, WAVES) PLE_W4_LAUNCH(MT, NT, 32, WAVES)             \
     PLE_W4_LAUNCH(MT, NT, 64, WAVES) PLE_W4_LAUNCH(MT, NT, 128, WAVES)
     PLE_W4_SHAPES(PLE_W4_LAUNCHES)
