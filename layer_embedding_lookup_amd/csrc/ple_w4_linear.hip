@@ -55,12 +55,18 @@ __device__ __forceinline__ void transpose4(u32x4& w) {
     w = u32x4{p[0], p[1], q[0], q[1]};
 }
 
-// The INT4 group scales of a step of 128 inputs.  Lane group g fetches only the one of inputs 32 g .. (scale | zero point
-// << 16; nothing past the last group), since a fetch touches 16 rows whatever its width; `groups_of` gives every lane all.
-template <int G>
-__device__ __forceinline__ uint32_t group_fetch(const void* scales, const uint8_t* zeros, int64_t row, int at, int groups) {
-    if (at >= groups) return 8u << 16;
-    return ((const uint16_t*)scales)[row + at] | (zeros == nullptr ? 8u : (uint32_t)zeros[row + at]) << 16;
+// The INT4 group scales of a step of 128 inputs.  Lane group g fetches only the one of inputs 32 g .. (the last one past
+// the end), since a fetch touches 16 rows whatever its width.  Nothing waits in the fetch: `group_word` puts scale and
+// zero point together later (scale | zero point << 16; zero past the end), and `groups_of` gives every lane all of them.
+struct GroupRaw {
+    uint32_t scale, zero;
+};
+__device__ __forceinline__ GroupRaw group_fetch(const void* scales, const uint8_t* zeros, int64_t row, int at, int groups) {
+    const int64_t i = row + min(at, groups - 1);
+    return {((const uint16_t*)scales)[i], zeros == nullptr ? 8u : (uint32_t)zeros[i]};
+}
+__device__ __forceinline__ uint32_t group_word(GroupRaw r, int at, int groups) {
+    return at < groups ? r.scale | r.zero << 16 : 8u << 16;
 }
 template <int G>
 __device__ __forceinline__ void groups_of(uint32_t mine, uint32_t (&all)[128 / G]) {
@@ -95,12 +101,20 @@ struct W4Args {
     uint16_t* out;
 };
 
-// A step of one wave: 128 inputs of NT x 16 features and of MT x 16 tokens, as loaded.
-template <int MT, int NT, int G>
+// A step of one wave: 128 inputs of NT x 16 features, as loaded.
+template <int NT>
 struct W4Step {
     u32x4 w[NT];
-    uint32_t scale[NT];  // NVFP4: the lane's two block scales; INT4: group_fetch
-    u32x4 x[MT][4];
+    GroupRaw scale[NT];  // NVFP4: the lane's two block scales
+};
+
+// The few-token kernel's LDS: a step's inputs of every wave, then the joined sums.
+template <int MT, int NT, int WAVES, int DEPTH>
+struct RowsShape {
+    static constexpr int STEP = MT * 4096;               // 16 MT tokens x 256 bytes
+    static constexpr int JOIN = WAVES < 4 ? WAVES : 4;   // waves whose sums are in LDS at once
+    static constexpr int LDS = WAVES * DEPTH * STEP > JOIN * MT * NT * 1024 ? WAVES * DEPTH * STEP : JOIN * MT * NT * 1024;
+    static_assert(LDS <= 160 * 1024, "more LDS than a CU has");
 };
 
 // MT tiles of 16 tokens, NT tiles of 16 features; G: 16 for NVFP4, else the INT4 group; DEPTH steps are loaded
@@ -109,15 +123,16 @@ template <int MT, int NT, int G, int WAVES, int DEPTH>
 __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
     constexpr bool kNv = G == 16;
     constexpr int kGroups = kNv ? 1 : 128 / G;  // groups of a step
-    constexpr int kJoin = WAVES < 4 ? WAVES : 4;  // waves whose sums are in LDS at once
-    __shared__ __align__(16) float join[kJoin][MT * NT][64][4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    using Sh = RowsShape<MT, NT, WAVES, DEPTH>;
+    constexpr int kJoin = Sh::JOIN;
+    extern __shared__ __align__(16) char lds[];
+    float(*const join)[MT * NT][64][4] = (float(*)[MT * NT][64][4])lds;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int tiles_o = (a.O + 16 * NT - 1) / (16 * NT), o0 = (blockIdx.x % tiles_o) * (16 * NT);
     const int64_t t0 = (int64_t)(blockIdx.x / tiles_o) * (16 * MT);
     const int groups = a.K / (kNv ? 16 : G);
-    // features past the end repeat the last one, tokens past it are zeros (and not fetched: for a single token the
-    // inputs' fetches would outweigh the codes'); neither is stored
+    // features past the end repeat the last one, tokens past it hold anything; neither is stored
     const uint8_t* wrow[NT];
     int64_t srow[NT];
 #pragma unroll
@@ -126,54 +141,62 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
         wrow[nt] = a.codes + o * (a.K / 2) + g * 16;
         srow[nt] = o * groups;
     }
-    const uint16_t* xrow[MT];
-    bool xlive[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int64_t t = t0 + mt * 16 + n;
-        xlive[mt] = t < a.T;
-        xrow[mt] = a.x + t * a.x_stride;
-    }
+    // Inputs go straight to LDS, 4 tokens x 256 contiguous bytes an instruction (as fragments they would be 64 separate
+    // 16-byte reads of the cache, which bound this kernel before: 8192 x 4096 NVFP4, 64 tokens, 22.7 us): token r's 16
+    // chunks of 16 bytes, chunk c at place c ^ (r % 16), read back without bank conflicts.
+    char* const xlds = lds + wave * (DEPTH * Sh::STEP);
+    const int live = (int)(a.T - t0 < 16 * MT ? a.T - t0 : 16 * MT);
     f32x4 acc[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    using Step = W4Step<MT, NT, G>;
+    using Step = W4Step<NT>;
     const u32x4 zero4 = {0u, 0u, 0u, 0u};
     // Lanes past K take zeros: NVFP4 products vanish, INT4 steps stop at the last group (K is a multiple of it).
-    auto load = [&](int k0, Step& s) {
+    auto load = [&](int k0, Step& s, int d) {
+#pragma unroll
+        for (int i = 0; i < 4 * MT; ++i) {
+            if (4 * i >= live) break;
+            const int r = 4 * i + g, c = n ^ (r & 15);
+            const int64_t t = t0 + (r < live ? r : live - 1);
+            const uint16_t* src = a.x + t * a.x_stride + (k0 + c * 8 < a.K ? k0 + c * 8 : 0);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                             (__attribute__((address_space(3))) void*)(xlds + d * Sh::STEP + i * 1024), 16, 0, 0);
+        }
         const bool in = k0 + g * 32 < a.K;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             s.w[nt] = in ? *(const u32x4*)(wrow[nt] + k0 / 2) : zero4;
             if constexpr (kNv) {
-                s.scale[nt] = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
+                s.scale[nt].scale = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
             } else {
-                s.scale[nt] = group_fetch<G>(a.scales, a.zeros, srow[nt], (k0 + 32 * g) / G, groups);
+                s.scale[nt] = group_fetch(a.scales, a.zeros, srow[nt], (k0 + 32 * g) / G, groups);
             }
         }
+    };
+    auto use = [&](int k0, Step& s, int d) {
+        u32x4 x[MT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int k = kNv ? k0 + g * 32 + j * 8 : k0 + j * 32 + g * 8;
-                s.x[mt][j] = k < a.K && xlive[mt] ? *(const u32x4*)(xrow[mt] + k) : zero4;
+                const int c = kNv ? 4 * g + j : 4 * j + g;
+                x[mt][j] = *(const u32x4*)(xlds + d * Sh::STEP + mt * 4096 + n * 256 + (c ^ n) * 16);
+                if (k0 + 128 > a.K && k0 + c * 8 >= a.K) x[mt][j] = zero4;
             }
-    };
-    auto use = [&](int k0, Step& s) {
         if constexpr (kNv) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const f32x2 sc = __builtin_amdgcn_cvt_pk_f32_fp8((int)s.scale[nt], false);
+                const f32x2 sc = __builtin_amdgcn_cvt_pk_f32_fp8((int)s.scale[nt].scale, false);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     BFrag f;
                     nvfp4_frag(s.w[nt][j], sc[j >> 1], f);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
-                        acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, s.x[mt][j]), f.v,
+                        acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[mt][j]), f.v,
                                                                               acc[mt][nt], 0, 0, 0);
                 }
             }
@@ -182,7 +205,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
             for (int nt = 0; nt < NT; ++nt) {
                 transpose4(s.w[nt]);  // word j: inputs k0 + 32 j + 8 g ..
                 uint32_t all[kGroups];
-                groups_of<G>(s.scale[nt], all);
+                groups_of<G>(group_word(s.scale[nt], (k0 + 32 * g) / G, groups), all);
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
                     const float z = (float)(all[i] >> 16), sc = bf16_lo(all[i]);
@@ -195,7 +218,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
                         int4_frag(s.w[nt][j], z, f);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt)
-                            part[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, s.x[mt][j]),
+                            part[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[mt][j]),
                                                                                f.v, part[mt], 0, 0, 0);
                     }
                     // (groups past K hold zero inputs and a zero scale)
@@ -210,10 +233,15 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
     Step st[DEPTH];
     for (int k0 = wave * 128; k0 < a.K; k0 += DEPTH * WAVES * 128) {
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) load(k0 + d * WAVES * 128, st[d]);
+        for (int d = 0; d < DEPTH; ++d)
+            if (k0 + d * WAVES * 128 < a.K) load(k0 + d * WAVES * 128, st[d], d);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) use(k0 + d * WAVES * 128, st[d]);
+        for (int d = 0; d < DEPTH; ++d)
+            if (k0 + d * WAVES * 128 < a.K) use(k0 + d * WAVES * 128, st[d], d);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the inputs are read before the next ones come in
     }
+    __syncthreads();  // the sums take the inputs' place
 
     // waves kJoin .. hand their sums to the first kJoin, whose sums are then added up
     for (int w0 = WAVES - kJoin; w0 > 0; w0 -= kJoin) {
@@ -249,7 +277,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
 
 // Shapes of the few-token kernel: token tiles, feature tiles, waves, steps in flight, waves per SIMD that registers are
 // kept to (two blocks per CU for up to 32 tokens: 8192 x 4096 INT4, one token, 10.5 us, with four steps in flight and one block 14.1).
-#define PLE_W4_SHAPES(X) X(1, 1, 8, 2, 4) X(2, 1, 8, 1, 4) X(4, 1, 8, 2, 2) X(4, 2, 8, 1, 2) X(4, 4, 8, 1, 2)
+#define PLE_W4_SHAPES(X) X(1, 1, 8, 1, 4) X(2, 1, 8, 1, 4) X(4, 1, 8, 1, 2) X(4, 2, 8, 1, 2) X(4, 4, 8, 1, 2)
 #define PLE_W4_KERNEL(MT, NT, G, WAVES, DEPTH, OCC)                                                                   \
     __global__ __launch_bounds__(WAVES * 64, OCC) void w4_rows_##MT##x##NT##_##G##_kernel(W4Args a) {                 \
         w4_rows_body<MT, NT, G, WAVES, DEPTH>(a);                                                                     \
@@ -319,16 +347,16 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
 
     const u32x4 zero4 = {0u, 0u, 0u, 0u};
     u32x4 w[NT], xs[MT];
-    uint32_t scale[NT];
+    GroupRaw scale[NT];
     auto load = [&](int k0) {
         const bool in = k0 + g * 32 < a.K;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             w[nt] = in ? *(const u32x4*)(wrow[nt] + k0 / 2) : zero4;
             if constexpr (kNv) {
-                scale[nt] = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
+                scale[nt].scale = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
             } else {
-                scale[nt] = group_fetch<G>(a.scales, a.zeros, srow[nt], (k0 + 32 * g) / G, groups);
+                scale[nt] = group_fetch(a.scales, a.zeros, srow[nt], (k0 + 32 * g) / G, groups);
             }
         }
         const bool xin = k0 + (tid & 15) * 8 < a.K;
@@ -356,14 +384,14 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if constexpr (kNv) {
-                const f32x2 s2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)scale[nt], false);
+                const f32x2 s2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)scale[nt].scale, false);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) nvfp4_frag(w[nt][j], s2[j >> 1], f[nt][j]);
             } else {
                 u32x4 t = w[nt];
                 transpose4(t);
                 uint32_t all[kGroups];
-                groups_of<G>(scale[nt], all);
+                groups_of<G>(group_word(scale[nt], (st * 128 + 32 * g) / G, groups), all);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) int4_frag(t[j], (float)(all[j / (G / 32)] >> 16), f[nt][j]);
 #pragma unroll
@@ -452,15 +480,18 @@ PLE_W4_GEMM(16, 8, 2, 2)
 PLE_W4_GEMM(128, 8, 2, 2)
 #undef PLE_W4_GEMM
 
+template <void (*FN)(W4Args), int LDS>
+static hipError_t launch_blocks(const W4Args& a, unsigned blocks, int threads, hipStream_t s) {
+    static const hipError_t attr = hipFuncSetAttribute((const void*)FN, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+    if (attr != hipSuccess) return attr;
+    hipLaunchKernelGGL(FN, dim3(blocks), dim3(threads), LDS, s, a);
+    return hipGetLastError();
+}
+
 template <void (*FN)(W4Args), int MT, int NT>
 static hipError_t launch_gemm(const W4Args& a, hipStream_t s) {
     using Sh = GemmShape<MT, NT>;
-    static const hipError_t attr =
-        hipFuncSetAttribute((const void*)FN, hipFuncAttributeMaxDynamicSharedMemorySize, Sh::LDS);
-    if (attr != hipSuccess) return attr;
-    const int64_t blocks = (a.T + Sh::T - 1) / Sh::T * ((a.O + Sh::O - 1) / Sh::O);
-    hipLaunchKernelGGL(FN, dim3((unsigned)blocks), dim3(kGemmThreads), Sh::LDS, s, a);
-    return hipGetLastError();
+    return launch_blocks<FN, Sh::LDS>(a, (unsigned)((a.T + Sh::T - 1) / Sh::T * ((a.O + Sh::O - 1) / Sh::O)), kGemmThreads, s);
 }
 
 hipError_t launch_w4_linear(const uint16_t* x, int64_t x_stride, const ple_w4_weight& w, int64_t T, uint16_t* out,
@@ -485,14 +516,14 @@ hipError_t launch_w4_linear(const uint16_t* x, int64_t x_stride, const ple_w4_we
     const int64_t rows = (T + 63) / 64;
     const int nt = mt < 4 || rows * ((w.out_dim + 31) / 32) <= 128 ? 1 : (rows * ((w.out_dim + 63) / 64) >= 192 ? 4 : 2);
     const unsigned blocks = (unsigned)((w.out_dim + 16 * nt - 1) / (16 * nt) * ((T + 16 * mt - 1) / (16 * mt)));
-#define PLE_W4_LAUNCH(MT, NT, G, WAVES) \
+#define PLE_W4_LAUNCH(MT, NT, G, WAVES, DEPTH) \
     if (mt == MT && nt == NT && w.group == G)  \
-        hipLaunchKernelGGL(w4_rows_##MT##x##NT##_##G##_kernel, dim3(blocks), dim3(WAVES * 64), 0, s, a);
-#define PLE_W4_LAUNCHES(MT, NT, WAVES, DEPTH, OCC)                                \
-    PLE_W4_LAUNCH(MT, NT, 16, WAVES) PLE_W4_LAUNCH(MT, NT, 32, WAVES)             \
-    PLE_W4_LAUNCH(MT, NT, 64, WAVES) PLE_W4_LAUNCH(MT, NT, 128, WAVES)
+        return launch_blocks<w4_rows_##MT##x##NT##_##G##_kernel, RowsShape<MT, NT, WAVES, DEPTH>::LDS>(a, blocks, WAVES * 64, s);
+#define PLE_W4_LAUNCHES(MT, NT, WAVES, DEPTH, OCC)                                            \
+    PLE_W4_LAUNCH(MT, NT, 16, WAVES, DEPTH) PLE_W4_LAUNCH(MT, NT, 32, WAVES, DEPTH)           \
+    PLE_W4_LAUNCH(MT, NT, 64, WAVES, DEPTH) PLE_W4_LAUNCH(MT, NT, 128, WAVES, DEPTH)
     PLE_W4_SHAPES(PLE_W4_LAUNCHES)
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 
 }  // namespace ple
