@@ -308,7 +308,9 @@ struct GemmShape {
     static constexpr int T = 16 * MT, O = 64 * NT;
     static constexpr int SLOT = T * 256;          // bytes of a slice
     static constexpr int OUT_ROW = O * 2 + 16;    // bytes of an output row in LDS
-    static constexpr int LDS = 2 * SLOT > T * OUT_ROW ? 2 * SLOT : T * OUT_ROW;
+    static constexpr int CODES = NT * 1024;       // bytes of a wave's codes of a slice
+    static constexpr int CODES_AT = 2 * SLOT;
+    static constexpr int LDS = CODES_AT + 8 * CODES > T * OUT_ROW ? CODES_AT + 8 * CODES : T * OUT_ROW;
 };
 
 template <int G, int MT, int NT>
@@ -317,7 +319,7 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
     constexpr bool kNv = G == 16;
     constexpr int kGroups = kNv ? 1 : 128 / G;
     extern __shared__ __align__(16) char lds[];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int tiles_t = (int)((a.T + Sh::T - 1) / Sh::T), tiles_o = (a.O + Sh::O - 1) / Sh::O;
     // neighbouring blocks of an XCD (block number mod 8) share features, so their codes come from its L2
@@ -328,14 +330,18 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
     const int64_t t0 = (int64_t)tt * Sh::T;
     const int o0 = to * Sh::O + wave * (16 * NT);
     const int groups = a.K / (kNv ? 16 : G);
+    // Codes go to LDS as 16 rows x 64 contiguous bytes an instruction, two slots per wave (read by lane (n, g) from memory
+    // they would be 64 separate accesses): row r's chunk c at place c ^ (r / 4).
     const uint8_t* wrow[NT];
     int64_t srow[NT];
+    const int wchunk = ((lane & 3) ^ (lane >> 4)) * 16;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int64_t o = min(o0 + nt * 16 + n, a.O - 1);
-        wrow[nt] = a.codes + o * (a.K / 2) + g * 16;
-        srow[nt] = o * groups;
+        wrow[nt] = a.codes + (int64_t)min(o0 + nt * 16 + (lane >> 2), a.O - 1) * (a.K / 2);
+        srow[nt] = (int64_t)min(o0 + nt * 16 + n, a.O - 1) * groups;
     }
+    char* const wlds = lds + Sh::CODES_AT + wave * (2 * Sh::CODES);
+    const int wat = n * 64 + (g ^ (n >> 2)) * 16;
     // this thread's chunks of a slice: token tid/16 + 16 i, chunk tid % 16
     const uint16_t* xsrc[MT];
 #pragma unroll
@@ -346,13 +352,18 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
     char* const xdst = lds + (tid >> 4) * 256 + ((tid & 15) ^ (tid >> 4)) * 16;
 
     const u32x4 zero4 = {0u, 0u, 0u, 0u};
-    u32x4 w[NT], xs[MT];
+    u32x4 xs[MT];
     GroupRaw scale[NT];
     auto load = [&](int k0) {
         const bool in = k0 + g * 32 < a.K;
+        const int at = k0 / 2 + wchunk < a.K / 2 ? k0 / 2 + wchunk : 0;  // (past K: anything, against zero inputs)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(wrow[nt] + at),
+                                             (__attribute__((address_space(3))) void*)(wlds + (k0 >> 7 & 1) * Sh::CODES + nt * 1024),
+                                             16, 0, 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            w[nt] = in ? *(const u32x4*)(wrow[nt] + k0 / 2) : zero4;
             if constexpr (kNv) {
                 scale[nt].scale = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
             } else {
@@ -376,9 +387,13 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
 
     load(0);
     put(0);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the codes
     const int steps = (a.K + 127) / 128;
     for (int st = 0; st < steps; ++st) {
         // this slice's codes as bf16
+        u32x4 w[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) w[nt] = *(const u32x4*)(wlds + (st & 1) * Sh::CODES + nt * 1024 + wat);
         BFrag f[NT][4];
         float sc[NT][kGroups];
 #pragma unroll
@@ -437,6 +452,7 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
             }
         }
         if (st + 1 < steps) put((st + 1) & 1);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the next codes
     }
 
     // out through LDS: lane (n, g) of tile (mt, nt) holds feature n of tokens 4 g ..
