@@ -101,17 +101,11 @@ struct W4Args {
     uint16_t* out;
 };
 
-// A step of one wave: 128 inputs of NT x 16 features, as loaded.
-template <int NT>
-struct W4Step {
-    u32x4 w[NT];
-    GroupRaw scale[NT];  // NVFP4: the lane's two block scales
-};
-
-// The few-token kernel's LDS: a step's inputs of every wave, then the joined sums.
+// The few-token kernel's LDS: a step's inputs and codes of every wave, then the joined sums.
 template <int MT, int NT, int WAVES, int DEPTH>
 struct RowsShape {
-    static constexpr int STEP = MT * 4096;               // 16 MT tokens x 256 bytes
+    static constexpr int CODES = MT * 4096;              // 16 MT tokens x 256 bytes, then 16 NT features x 64 bytes of codes
+    static constexpr int STEP = CODES + NT * 1024;
     static constexpr int JOIN = WAVES < 4 ? WAVES : 4;   // waves whose sums are in LDS at once
     static constexpr int LDS = WAVES * DEPTH * STEP > JOIN * MT * NT * 1024 ? WAVES * DEPTH * STEP : JOIN * MT * NT * 1024;
     static_assert(LDS <= 160 * 1024, "more LDS than a CU has");
@@ -137,10 +131,11 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
     int64_t srow[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int64_t o = min(o0 + nt * 16 + n, a.O - 1);
-        wrow[nt] = a.codes + o * (a.K / 2) + g * 16;
-        srow[nt] = o * groups;
+        wrow[nt] = a.codes + (int64_t)min(o0 + nt * 16 + (lane >> 2), a.O - 1) * (a.K / 2);
+        srow[nt] = (int64_t)min(o0 + nt * 16 + n, a.O - 1) * groups;
     }
+    // (codes: 16 features x 64 contiguous bytes an instruction, feature r's chunk c at place c ^ (r / 4))
+    const int wchunk = ((lane & 3) ^ (lane >> 4)) * 16, wat = n * 64 + (g ^ (n >> 2)) * 16;
     // Inputs go straight to LDS, 4 tokens x 256 contiguous bytes an instruction (as fragments they would be 64 separate
     // 16-byte reads of the cache, which bound this kernel before: 8192 x 4096 NVFP4, 64 tokens, 22.7 us): token r's 16
     // chunks of 16 bytes, chunk c at place c ^ (r % 16), read back without bank conflicts.
@@ -152,7 +147,10 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    using Step = W4Step<NT>;
+    // NVFP4: the lane's two block scales; INT4: as fetched
+    struct Step {
+        GroupRaw scale[NT];
+    };
     const u32x4 zero4 = {0u, 0u, 0u, 0u};
     // Lanes past K take zeros: NVFP4 products vanish, INT4 steps stop at the last group (K is a multiple of it).
     auto load = [&](int k0, Step& s, int d) {
@@ -166,9 +164,14 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
                                              (__attribute__((address_space(3))) void*)(xlds + d * Sh::STEP + i * 1024), 16, 0, 0);
         }
         const bool in = k0 + g * 32 < a.K;
+        const int at = k0 / 2 + wchunk < a.K / 2 ? k0 / 2 + wchunk : 0;  // (past K: anything, against zero inputs)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(wrow[nt] + at),
+                                             (__attribute__((address_space(3))) void*)(xlds + d * Sh::STEP + Sh::CODES + nt * 1024),
+                                             16, 0, 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            s.w[nt] = in ? *(const u32x4*)(wrow[nt] + k0 / 2) : zero4;
             if constexpr (kNv) {
                 s.scale[nt].scale = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
             } else {
@@ -177,6 +180,9 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
         }
     };
     auto use = [&](int k0, Step& s, int d) {
+        u32x4 w[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) w[nt] = *(const u32x4*)(xlds + d * Sh::STEP + Sh::CODES + nt * 1024 + wat);
         u32x4 x[MT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -193,7 +199,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     BFrag f;
-                    nvfp4_frag(s.w[nt][j], sc[j >> 1], f);
+                    nvfp4_frag(w[nt][j], sc[j >> 1], f);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
                         acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[mt][j]), f.v,
@@ -203,7 +209,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
         } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                transpose4(s.w[nt]);  // word j: inputs k0 + 32 j + 8 g ..
+                transpose4(w[nt]);  // word j: inputs k0 + 32 j + 8 g ..
                 uint32_t all[kGroups];
                 groups_of<G>(group_word(s.scale[nt], (k0 + 32 * g) / G, groups), all);
 #pragma unroll
@@ -215,7 +221,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
 #pragma unroll
                     for (int j = i * (G / 32); j < (i + 1) * (G / 32); ++j) {
                         BFrag f;
-                        int4_frag(s.w[nt][j], z, f);
+                        int4_frag(w[nt][j], z, f);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt)
                             part[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[mt][j]),

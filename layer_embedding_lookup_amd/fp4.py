@@ -239,6 +239,8 @@ def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table,
     if workspace is None:
         if need > 0:
             workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+            if stream is not None:  # it is given up here, before the work on that stream has ended
+                workspace.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
     else:
         _req_bytes("workspace", workspace, need)
         _same_device(cache.tensors[0], workspace)

@@ -400,6 +400,30 @@ def test_attention_strided_queries_streams_and_graph():
         assert torch.equal(y, ple.ple_w4_linear(eager.view(3, 1024), w))
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_attention_keeps_its_workspace_for_another_stream(handle):
+    """A call on a stream of the caller's that is still busy: its own workspace must not go to the next allocation."""
+    g = gen(21)
+    cache = U.Cache(g, [2500], H=1, D=128, page=16)
+    qsl, seq, _ = batch([1], [2500], cache)
+    q = torch.randn((1, 8, 128), generator=g).to(BF)
+    c = ple.KV4Cache(*cache.tensors(DEV))
+    args = (q.to(DEV), c, qsl.to(DEV), seq.to(DEV), cache.table.to(DEV))
+    kw = dict(max_request_tokens=1, max_seq_len=2500, want_lse=True)
+    need = ple.ple_kv4_attention_workspace_bytes(c, 8, 1, 1, cache.width, max_request_tokens=1, max_seq_len=2500)
+    assert need > 0
+    want, want_lse = ple.ple_kv4_attention(*args, **kw)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    out, lse = ple.ple_kv4_attention(*args, stream=side.cuda_stream if handle else side, **kw)
+    taken = [torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV) for _ in range(8)]
+    torch.cuda.current_stream().synchronize()
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse) and len(taken) == 8
+
+
 def test_attention_is_the_same_every_time():
     g = gen(18)
     lens = [2000, 700]
