@@ -55,9 +55,11 @@ __device__ __forceinline__ void transpose4(u32x4& w) {
     w = u32x4{p[0], p[1], q[0], q[1]};
 }
 
-// The INT4 group scales of a step of 128 inputs.  Lane group g fetches only the one of inputs 32 g .. (the last one past
-// the end), since a fetch touches 16 rows whatever its width.  Nothing waits in the fetch: `group_word` puts scale and
-// zero point together later (scale | zero point << 16; zero past the end), and `groups_of` gives every lane all of them.
+// The group scales of a step of 128 inputs.  Lane 4 r + c fetches those of row r's inputs 32 c .. (four neighbouring lanes
+// in one access) and hands them to lane r + 16 c, which holds these codes (the few-token NVFP4 kernel fetches its scales
+// where they are used: there the exchange costs 3% more than it saves, elsewhere it saves 2..12%).  INT4: the last group's past the end; nothing
+// waits in the fetch, `group_word` puts scale and zero point together later (scale | zero point << 16; zero past the
+// end), and `groups_of` gives every lane of a row all of them.
 struct GroupRaw {
     uint32_t scale, zero;
 };
@@ -132,7 +134,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         wrow[nt] = a.codes + (int64_t)min(o0 + nt * 16 + (lane >> 2), a.O - 1) * (a.K / 2);
-        srow[nt] = (int64_t)min(o0 + nt * 16 + n, a.O - 1) * groups;
+        srow[nt] = (int64_t)min(o0 + nt * 16 + (kNv ? n : lane >> 2), a.O - 1) * groups;
     }
     // (codes: 16 features x 64 contiguous bytes an instruction, feature r's chunk c at place c ^ (r / 4))
     const int wchunk = ((lane & 3) ^ (lane >> 4)) * 16, wat = n * 64 + (g ^ (n >> 2)) * 16;
@@ -175,7 +177,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
             if constexpr (kNv) {
                 s.scale[nt].scale = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
             } else {
-                s.scale[nt] = group_fetch(a.scales, a.zeros, srow[nt], (k0 + 32 * g) / G, groups);
+                s.scale[nt] = group_fetch(a.scales, a.zeros, srow[nt], (k0 + 32 * (lane & 3)) / G, groups);
             }
         }
     };
@@ -211,7 +213,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
             for (int nt = 0; nt < NT; ++nt) {
                 transpose4(w[nt]);  // word j: inputs k0 + 32 j + 8 g ..
                 uint32_t all[kGroups];
-                groups_of<G>(group_word(s.scale[nt], (k0 + 32 * g) / G, groups), all);
+                groups_of<G>(__shfl(group_word(s.scale[nt], (k0 + 32 * (lane & 3)) / G, groups), 4 * n + g, kWave), all);
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
                     const float z = (float)(all[i] >> 16), sc = bf16_lo(all[i]);
@@ -344,7 +346,7 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         wrow[nt] = a.codes + (int64_t)min(o0 + nt * 16 + (lane >> 2), a.O - 1) * (a.K / 2);
-        srow[nt] = (int64_t)min(o0 + nt * 16 + n, a.O - 1) * groups;
+        srow[nt] = (int64_t)min(o0 + nt * 16 + (lane >> 2), a.O - 1) * groups;
     }
     char* const wlds = lds + Sh::CODES_AT + wave * (2 * Sh::CODES);
     const int wat = n * 64 + (g ^ (n >> 2)) * 16;
@@ -361,7 +363,7 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
     u32x4 xs[MT];
     GroupRaw scale[NT];
     auto load = [&](int k0) {
-        const bool in = k0 + g * 32 < a.K;
+        const bool in = k0 + (lane & 3) * 32 < a.K;
         const int at = k0 / 2 + wchunk < a.K / 2 ? k0 / 2 + wchunk : 0;  // (past K: anything, against zero inputs)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -371,9 +373,9 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if constexpr (kNv) {
-                scale[nt].scale = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + g * 2) : 0u;
+                scale[nt].scale = in ? *(const uint16_t*)((const uint8_t*)a.scales + srow[nt] + k0 / 16 + (lane & 3) * 2) : 0u;
             } else {
-                scale[nt] = group_fetch(a.scales, a.zeros, srow[nt], (k0 + 32 * g) / G, groups);
+                scale[nt] = group_fetch(a.scales, a.zeros, srow[nt], (k0 + 32 * (lane & 3)) / G, groups);
             }
         }
         const bool xin = k0 + (tid & 15) * 8 < a.K;
@@ -405,14 +407,14 @@ __device__ __forceinline__ void w4_gemm_body(const W4Args& a) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if constexpr (kNv) {
-                const f32x2 s2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)scale[nt].scale, false);
+                const f32x2 s2 = __builtin_amdgcn_cvt_pk_f32_fp8(__shfl((int)scale[nt].scale, 4 * n + g, kWave), false);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) nvfp4_frag(w[nt][j], s2[j >> 1], f[nt][j]);
             } else {
                 u32x4 t = w[nt];
                 transpose4(t);
                 uint32_t all[kGroups];
-                groups_of<G>(group_word(scale[nt], (st * 128 + 32 * g) / G, groups), all);
+                groups_of<G>(__shfl(group_word(scale[nt], (st * 128 + 32 * (lane & 3)) / G, groups), 4 * n + g, kWave), all);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) int4_frag(t[j], (float)(all[j / (G / 32)] >> 16), f[nt][j]);
 #pragma unroll
