@@ -27,6 +27,15 @@
 //    its operands of four MFMAs; the queries are laid out to match.
 //  - value codes lie along the elements but enter along the tokens: they are
 //    staged in LDS and come back through the transposing 4-bit read.
+//
+// Few rows: the waves of a block take the tiles of a cache range in turn and
+// join through LDS; four waves a block, eight where there is a block per CU
+// at most.  The next tile is loaded while this one's weights and value
+// product are formed, its page-table entry a tile before that.  Bound by
+// reading the cache where there is much of it (256 requests of up to 6000
+// tokens, 914 MB: 191 us, 4.8 TB/s; one of 131k tokens, 151 MB: 29 us and 5
+// for the join, 38.7 with the launches), else by the chain of dependent loads
+// (one of 777 tokens: 10 us; 64 windows of 1..4 drafts over 1024 tokens: 17).
 #include "ple_fp4_launch.h"
 
 namespace ple {
@@ -574,7 +583,12 @@ PLE_ATTN_SHAPES(PLE_ATTN_KERNEL)
 // finished MFMA fragments, one 16-byte read per lane each; so a tile is
 // dequantised once for 128 rows.  Two tiles in LDS: the next one is filled
 // while this one is used, with one barrier a tile.  Two blocks per CU cover
-// each other's softmax (D = 256: one).
+// each other's softmax (D = 256: one).  1289 + 1455 tokens at 5403 and 2004,
+// 32 heads of 128: 230 us, 0.57 PFLOP/s, 25 of them the join of cut tiles.  A
+// wave takes 6300..7000 cycles for a tile of which its products are 1024,
+// softmax about 900, dequantising about 400; without waiting for memory, or
+// with these hand-interleaved, it takes as long, so what is left is the two
+// waves of a SIMD in the same phase.
 // ---------------------------------------------------------------------------
 constexpr int kChunkRows = 128;
 constexpr int kFlatLeast = 8;        // places of a share at least

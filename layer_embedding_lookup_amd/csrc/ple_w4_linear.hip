@@ -1,13 +1,17 @@
 // Products with 4-bit weights: out = x W^T, W dequantised on the way to the
 // matrix cores and never written out.
 //
-// Few tokens (decode): bound by reading W once.  A wave takes 16 output
-// features and a share of K.  One 16-byte load per lane brings 32 codes of
-// one feature, a wave 16 features x 128 inputs, which feed four 16x16x32 bf16
-// MFMAs with the tokens as the first operand and the features as the second;
-// so every lane's scales belong to its own feature lane % 16.  The waves of a
-// block share the features, split K between them in steps of 128 and join
-// their sums through LDS.
+// Few tokens (decode): bound by reading W once, then by a launch's own time
+// (about 5 us; one token, 4096 -> 8192 NVFP4, 18.9 MB: 6.5 us, 2.9 TB/s; 64
+// tokens 13.4).  A wave takes NT x 16 output features and a share of K in
+// steps of 128.  Inputs and codes come in whole rows straight into LDS, 1 KiB
+// an instruction: read as MFMA operands from memory (lane n its own row) each
+// lane's 16 bytes are a cache access of their own, and those accesses, 64 an
+// instruction, bound the kernel (64 tokens: 22.6 us).  Four 16x16x32 bf16
+// MFMAs a step have the tokens as the first operand and the features as the
+// second, so every lane's scales belong to its own feature lane % 16.  The
+// waves of a block share the features, split K between them and join their
+// sums through LDS, which needs no second launch and no atomics.
 //  NVFP4: code * block scale is exact in bf16 (6 significant bits); the
 //         tensor's scale multiplies the sum.
 //  INT4:  code - zero is exact in bf16.  The four lanes of a feature swap
@@ -57,9 +61,9 @@ __device__ __forceinline__ void transpose4(u32x4& w) {
 
 // The group scales of a step of 128 inputs.  Lane 4 r + c fetches those of row r's inputs 32 c .. (four neighbouring lanes
 // in one access) and hands them to lane r + 16 c, which holds these codes (the few-token NVFP4 kernel fetches its scales
-// where they are used: there the exchange costs 3% more than it saves, elsewhere it saves 2..12%).  INT4: the last group's past the end; nothing
-// waits in the fetch, `group_word` puts scale and zero point together later (scale | zero point << 16; zero past the
-// end), and `groups_of` gives every lane of a row all of them.
+// where they are used: there the exchange costs 3% more than it saves, elsewhere it saves 2..12%).  INT4: the last
+// group's past the end; nothing waits in the fetch, `group_word` puts scale and zero point together later (scale | zero
+// point << 16; zero past the end), and `groups_of` gives every lane of a row all of them.
 struct GroupRaw {
     uint32_t scale, zero;
 };
@@ -104,22 +108,21 @@ struct W4Args {
 };
 
 // The few-token kernel's LDS: a step's inputs and codes of every wave, then the joined sums.
-template <int MT, int NT, int WAVES, int DEPTH>
+template <int MT, int NT, int WAVES>
 struct RowsShape {
     static constexpr int CODES = MT * 4096;              // 16 MT tokens x 256 bytes, then 16 NT features x 64 bytes of codes
     static constexpr int STEP = CODES + NT * 1024;
     static constexpr int JOIN = WAVES < 4 ? WAVES : 4;   // waves whose sums are in LDS at once
-    static constexpr int LDS = WAVES * DEPTH * STEP > JOIN * MT * NT * 1024 ? WAVES * DEPTH * STEP : JOIN * MT * NT * 1024;
+    static constexpr int LDS = WAVES * STEP > JOIN * MT * NT * 1024 ? WAVES * STEP : JOIN * MT * NT * 1024;
     static_assert(LDS <= 160 * 1024, "more LDS than a CU has");
 };
 
-// MT tiles of 16 tokens, NT tiles of 16 features; G: 16 for NVFP4, else the INT4 group; DEPTH steps are loaded
-// before the first of them is used.
-template <int MT, int NT, int G, int WAVES, int DEPTH>
+// MT tiles of 16 tokens, NT tiles of 16 features; G: 16 for NVFP4, else the INT4 group.
+template <int MT, int NT, int G, int WAVES>
 __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
     constexpr bool kNv = G == 16;
     constexpr int kGroups = kNv ? 1 : 128 / G;  // groups of a step
-    using Sh = RowsShape<MT, NT, WAVES, DEPTH>;
+    using Sh = RowsShape<MT, NT, WAVES>;
     constexpr int kJoin = Sh::JOIN;
     extern __shared__ __align__(16) char lds[];
     float(*const join)[MT * NT][64][4] = (float(*)[MT * NT][64][4])lds;
@@ -141,7 +144,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
     // Inputs go straight to LDS, 4 tokens x 256 contiguous bytes an instruction (as fragments they would be 64 separate
     // 16-byte reads of the cache, which bound this kernel before: 8192 x 4096 NVFP4, 64 tokens, 22.7 us): token r's 16
     // chunks of 16 bytes, chunk c at place c ^ (r % 16), read back without bank conflicts.
-    char* const xlds = lds + wave * (DEPTH * Sh::STEP);
+    char* const xlds = lds + wave * Sh::STEP;
     const int live = (int)(a.T - t0 < 16 * MT ? a.T - t0 : 16 * MT);
     f32x4 acc[MT][NT];
 #pragma unroll
@@ -155,7 +158,7 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
     };
     const u32x4 zero4 = {0u, 0u, 0u, 0u};
     // Lanes past K take zeros: NVFP4 products vanish, INT4 steps stop at the last group (K is a multiple of it).
-    auto load = [&](int k0, Step& s, int d) {
+    auto load = [&](int k0, Step& s) {
 #pragma unroll
         for (int i = 0; i < 4 * MT; ++i) {
             if (4 * i >= live) break;
@@ -163,14 +166,14 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
             const int64_t t = t0 + (r < live ? r : live - 1);
             const uint16_t* src = a.x + t * a.x_stride + (k0 + c * 8 < a.K ? k0 + c * 8 : 0);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                             (__attribute__((address_space(3))) void*)(xlds + d * Sh::STEP + i * 1024), 16, 0, 0);
+                                             (__attribute__((address_space(3))) void*)(xlds + i * 1024), 16, 0, 0);
         }
         const bool in = k0 + g * 32 < a.K;
         const int at = k0 / 2 + wchunk < a.K / 2 ? k0 / 2 + wchunk : 0;  // (past K: anything, against zero inputs)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(wrow[nt] + at),
-                                             (__attribute__((address_space(3))) void*)(xlds + d * Sh::STEP + Sh::CODES + nt * 1024),
+                                             (__attribute__((address_space(3))) void*)(xlds + Sh::CODES + nt * 1024),
                                              16, 0, 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -181,17 +184,17 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
             }
         }
     };
-    auto use = [&](int k0, Step& s, int d) {
+    auto use = [&](int k0, Step& s) {
         u32x4 w[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) w[nt] = *(const u32x4*)(xlds + d * Sh::STEP + Sh::CODES + nt * 1024 + wat);
+        for (int nt = 0; nt < NT; ++nt) w[nt] = *(const u32x4*)(xlds + Sh::CODES + nt * 1024 + wat);
         u32x4 x[MT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = kNv ? 4 * g + j : 4 * j + g;
-                x[mt][j] = *(const u32x4*)(xlds + d * Sh::STEP + mt * 4096 + n * 256 + (c ^ n) * 16);
+                x[mt][j] = *(const u32x4*)(xlds + mt * 4096 + n * 256 + (c ^ n) * 16);
                 if (k0 + 128 > a.K && k0 + c * 8 >= a.K) x[mt][j] = zero4;
             }
         if constexpr (kNv) {
@@ -238,15 +241,11 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
             }
         }
     };
-    Step st[DEPTH];
-    for (int k0 = wave * 128; k0 < a.K; k0 += DEPTH * WAVES * 128) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            if (k0 + d * WAVES * 128 < a.K) load(k0 + d * WAVES * 128, st[d], d);
+    for (int k0 = wave * 128; k0 < a.K; k0 += WAVES * 128) {
+        Step st;
+        load(k0, st);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            if (k0 + d * WAVES * 128 < a.K) use(k0 + d * WAVES * 128, st[d], d);
+        use(k0, st);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the inputs are read before the next ones come in
     }
     __syncthreads();  // the sums take the inputs' place
@@ -283,26 +282,29 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
     }
 }
 
-// Shapes of the few-token kernel: token tiles, feature tiles, waves, steps in flight, waves per SIMD that registers are
-// kept to (two blocks per CU for up to 32 tokens: 8192 x 4096 INT4, one token, 10.5 us, with four steps in flight and one block 14.1).
-#define PLE_W4_SHAPES(X) X(1, 1, 8, 1, 4) X(2, 1, 8, 1, 4) X(4, 1, 8, 1, 2) X(4, 2, 8, 1, 2) X(4, 4, 8, 1, 2)
-#define PLE_W4_KERNEL(MT, NT, G, WAVES, DEPTH, OCC)                                                                   \
-    __global__ __launch_bounds__(WAVES * 64, OCC) void w4_rows_##MT##x##NT##_##G##_kernel(W4Args a) {                 \
-        w4_rows_body<MT, NT, G, WAVES, DEPTH>(a);                                                                     \
+// Shapes of the few-token kernel: token tiles, feature tiles, waves, waves per SIMD that registers are kept to (up to 32
+// tokens two blocks per CU and more: 8192 x 4096 INT4, one token, 14.1 us with one).
+#define PLE_W4_SHAPES(X) X(1, 1, 8, 4) X(2, 1, 8, 4) X(4, 1, 8, 2) X(4, 2, 8, 2) X(4, 4, 8, 2)
+#define PLE_W4_KERNEL(MT, NT, G, WAVES, OCC)                                                          \
+    __global__ __launch_bounds__(WAVES * 64, OCC) void w4_rows_##MT##x##NT##_##G##_kernel(W4Args a) { \
+        w4_rows_body<MT, NT, G, WAVES>(a);                                                            \
     }
-#define PLE_W4_KERNELS(MT, NT, WAVES, DEPTH, OCC)                                                   \
-    PLE_W4_KERNEL(MT, NT, 16, WAVES, DEPTH, OCC) PLE_W4_KERNEL(MT, NT, 32, WAVES, DEPTH, OCC)       \
-    PLE_W4_KERNEL(MT, NT, 64, WAVES, DEPTH, OCC) PLE_W4_KERNEL(MT, NT, 128, WAVES, DEPTH, OCC)
+#define PLE_W4_KERNELS(MT, NT, WAVES, OCC)                                              \
+    PLE_W4_KERNEL(MT, NT, 16, WAVES, OCC) PLE_W4_KERNEL(MT, NT, 32, WAVES, OCC)         \
+    PLE_W4_KERNEL(MT, NT, 64, WAVES, OCC) PLE_W4_KERNEL(MT, NT, 128, WAVES, OCC)
 PLE_W4_SHAPES(PLE_W4_KERNELS)
 
 // ---------------------------------------------------------------------------
-// Many tokens: bound by the products and by dequantising between them.  A
+// Many tokens: bound by the products and by dequantising between them (1024
+// tokens 4096 -> 8192 NVFP4: 72..75 us, 0.92..0.95 PFLOP/s; INT4 in groups of
+// 128 94 us, of 32, with four times the scaling of partial sums, 171).  A
 // block of four waves holds MT x 16 tokens x NT x 64 features, a wave all of
-// the tokens and NT x 16 features.  The inputs go through LDS in slices of
-// 128 (two slots), shared by the waves; the codes do not: each wave
-// dequantises its own features in registers, once for the block's tokens.
-// 64 tokens leave room for two blocks per CU, which cover each other's waits
-// and let one dequantise while the other multiplies.
+// the tokens and NT x 16 features.  Inputs and codes go through LDS in slices
+// of 128 (two slots), the inputs shared by the waves; each wave dequantises
+// its own features in registers, once for the block's tokens.  128 features a
+// block, not 256, leave room for two blocks per CU, which cover each other's
+// waits (T = 1024 in 128 x 256 tiles, one block per CU: 88 us; INT4 in groups
+// of 32 spilled, 1183).
 //
 // LDS layout of a slice: a token's 256 bytes are 16 chunks of 16 bytes, chunk
 // c at place c ^ (token % 16), so the 16 lanes of a fragment read (16 tokens,
@@ -542,12 +544,12 @@ hipError_t launch_w4_linear(const uint16_t* x, int64_t x_stride, const ple_w4_we
     const int64_t rows = (T + 63) / 64;
     const int nt = mt < 4 || rows * ((w.out_dim + 15) / 16) <= 256 ? 1 : (rows * ((w.out_dim + 31) / 32) <= 256 ? 2 : 4);
     const unsigned blocks = (unsigned)((w.out_dim + 16 * nt - 1) / (16 * nt) * ((T + 16 * mt - 1) / (16 * mt)));
-#define PLE_W4_LAUNCH(MT, NT, G, WAVES, DEPTH) \
-    if (mt == MT && nt == NT && w.group == G)  \
-        return launch_blocks<w4_rows_##MT##x##NT##_##G##_kernel, RowsShape<MT, NT, WAVES, DEPTH>::LDS>(a, blocks, WAVES * 64, s);
-#define PLE_W4_LAUNCHES(MT, NT, WAVES, DEPTH, OCC)                                            \
-    PLE_W4_LAUNCH(MT, NT, 16, WAVES, DEPTH) PLE_W4_LAUNCH(MT, NT, 32, WAVES, DEPTH)           \
-    PLE_W4_LAUNCH(MT, NT, 64, WAVES, DEPTH) PLE_W4_LAUNCH(MT, NT, 128, WAVES, DEPTH)
+#define PLE_W4_LAUNCH(MT, NT, G, WAVES)       \
+    if (mt == MT && nt == NT && w.group == G) \
+        return launch_blocks<w4_rows_##MT##x##NT##_##G##_kernel, RowsShape<MT, NT, WAVES>::LDS>(a, blocks, WAVES * 64, s);
+#define PLE_W4_LAUNCHES(MT, NT, WAVES, OCC)                               \
+    PLE_W4_LAUNCH(MT, NT, 16, WAVES) PLE_W4_LAUNCH(MT, NT, 32, WAVES)     \
+    PLE_W4_LAUNCH(MT, NT, 64, WAVES) PLE_W4_LAUNCH(MT, NT, 128, WAVES)
     PLE_W4_SHAPES(PLE_W4_LAUNCHES)
     return hipErrorInvalidValue;
 }
