@@ -8,8 +8,8 @@
 // bytes in, 4 bytes of codes out), and the two lanes of a 16-element block
 // join their maxima with one exchange.  The rotation itself is 64-bit too and
 // rounded once to fp32, so that a key next to a code's border falls on the
-// side that the definition says.  8190 tokens of 32 + 8 + 8 heads of 128: 41 us
-// (187 MB, 4.5 TB/s) and 12.5 us to read them back (43 MB); 256 tokens: 7.4 and
+// side that the definition says.  7984 tokens of 32 + 8 + 8 heads of 128: 35 us
+// (173 MB, 4.9 TB/s; with the codes found by comparisons 41.6) and 12.5 us to read them back (43 MB); 256 tokens: 7.4 and
 // 3.7 us, where finding the request and its angles is the time.
 #include "ple_fp4_launch.h"
 
@@ -31,18 +31,28 @@ __device__ __forceinline__ uint32_t e4m3_code(float v) {
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v, 0.0f, 0, false) & 0xFFu;
 }
 
-// e2m1 code of t: nearest of 0 .5 1 1.5 2 3 4 6, ties to the even code (zero for NaN).
-__device__ __forceinline__ uint32_t e2m1_code(float t) {
-    const float a = fabsf(t);
-    const uint32_t c = (uint32_t)(a > 0.25f) + (uint32_t)(a >= 0.75f) + (uint32_t)(a > 1.25f) +
-                       (uint32_t)(a >= 1.75f) + (uint32_t)(a > 2.5f) + (uint32_t)(a >= 3.5f) + (uint32_t)(a > 5.0f);
-    return c | (__float_as_uint(t) >> 31 << 3);
+// e2m1 codes of 8 quotients: nearest of 0 .5 1 1.5 2 3 4 6, ties to the even code, 6 beyond it.
+__device__ __forceinline__ uint32_t e2m1_codes(const float (&t)[8]) {
+    uint32_t c = 0;
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = __builtin_amdgcn_fmed3f(t[i], -6.f, 6.f);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, u[0], u[1], 1.0f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, u[2], u[3], 1.0f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, u[4], u[5], 1.0f, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, u[6], u[7], 1.0f, 3);
+}
+
+// The token's 16-token group of head 0, or -1; one head on it is per_page groups on.
+__device__ __forceinline__ int64_t first_group(const ple_kv4_cache& c, const int32_t* row, int pos) {
+    return pos < 0 ? -1 : (int64_t)kv4_group(c, row, 0, pos >> 4);
 }
 
 __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArgs a) {
     __shared__ double2 turn[128];  // cos, sin of the token's angles
     const int64_t t = blockIdx.x;
-    const int D = a.cache.head_dim, per_head = D / 8, half = a.rot_dim / 2;
+    const int D = a.cache.head_dim, half = a.rot_dim / 2;
+    const int per_head = D / 8, shift = D == 64 ? 3 : (D == 128 ? 4 : 5);  // chunks of a head
     int r;
     const int pos = kv4_position(a.cache, a.batch, t, r);
     for (int i = threadIdx.x; i < half; i += kAppendThreads) {
@@ -53,12 +63,13 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArg
         turn[i] = make_double2(cs, sn);
     }
     __syncthreads();
-    const int32_t* row = a.batch.page_table + (int64_t)r * a.batch.table_width;
+    const int64_t group0 = first_group(a.cache, a.batch.page_table + (int64_t)r * a.batch.table_width, pos);
+    const int per_page = a.cache.page_size >> 4, place = pos & 15;
     const int nq = a.num_q_heads * per_head, nk = a.cache.num_kv_heads * per_head;
     for (int c = threadIdx.x; c < nq + 2 * nk; c += kAppendThreads) {
         const int which = c < nq ? 0 : (c < nq + nk ? 1 : 2);
         const int at = which == 0 ? c : (which == 1 ? c - nq : c - nq - nk);
-        const int head = at / per_head, d0 = (at - head * per_head) * 8;
+        const int head = at >> shift, d0 = (at & (per_head - 1)) * 8;
         const uint16_t* src = a.src[which] + t * a.stride[which] + head * D;
         float v[8];
         load8(src + d0, v);
@@ -107,17 +118,16 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArg
         const uint32_t sc = e4m3_code(s);
         float step = __builtin_amdgcn_cvt_pk_f32_fp8((int)sc, false)[0] * g;
         step = step > 0.f ? step : __builtin_inff();
-        uint32_t codes = 0;
+        float quotient[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) codes |= e2m1_code(v[i] / step) << (4 * i);
-        if (pos < 0) continue;
-        const int grp = kv4_group(a.cache, row, head, pos >> 4);
-        if (grp < 0) continue;
-        const int place = pos & 15;
-        uint8_t* cd = (which == 1 ? a.cache.k_codes : a.cache.v_codes) + (int64_t)grp * (8 * D) + place * (D / 2) + d0 / 2;
+        for (int i = 0; i < 8; ++i) quotient[i] = v[i] / step;
+        const uint32_t codes = e2m1_codes(quotient);
+        if (group0 < 0) continue;
+        const int64_t grp = group0 + (int64_t)head * per_page;
+        uint8_t* cd = (which == 1 ? a.cache.k_codes : a.cache.v_codes) + grp * (8 * D) + place * (D / 2) + d0 / 2;
         *(uint32_t*)cd = codes;
         if ((d0 & 8) == 0)
-            ((which == 1 ? a.cache.k_scales : a.cache.v_scales) + (int64_t)grp * D)[d0 + place] = (uint8_t)sc;
+            ((which == 1 ? a.cache.k_scales : a.cache.v_scales) + grp * D)[d0 + place] = (uint8_t)sc;
     }
 }
 
@@ -131,22 +141,22 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_read_kernel(ple_kv4_cache 
                                                                   uint16_t* __restrict__ k_out,
                                                                   uint16_t* __restrict__ v_out) {
     const int64_t t = blockIdx.x;
-    const int D = cache.head_dim, per_head = D / 8;
+    const int D = cache.head_dim, per_head = D / 8, shift = D == 64 ? 3 : (D == 128 ? 4 : 5);
     int r;
     const int pos = kv4_position(cache, batch, t, r);
-    const int32_t* row = batch.page_table + (int64_t)r * batch.table_width;
+    const int64_t group0 = first_group(cache, batch.page_table + (int64_t)r * batch.table_width, pos);
+    const int per_page = cache.page_size >> 4, place = pos & 15;
     const int nk = cache.num_kv_heads * per_head;
     for (int c = threadIdx.x; c < 2 * nk; c += kAppendThreads) {
         const bool val = c >= nk;
         const int at = val ? c - nk : c;
-        const int head = at / per_head, d0 = (at - head * per_head) * 8;
-        const int grp = pos < 0 ? -1 : kv4_group(cache, row, head, pos >> 4);
+        const int head = at >> shift, d0 = (at & (per_head - 1)) * 8;
         u32x4 o = {0u, 0u, 0u, 0u};
-        if (grp >= 0) {
-            const int place = pos & 15;
+        if (group0 >= 0) {
+            const int64_t grp = group0 + (int64_t)head * per_page;
             const uint32_t w =
-                *(const uint32_t*)((val ? cache.v_codes : cache.k_codes) + (int64_t)grp * (8 * D) + place * (D / 2) + d0 / 2);
-            const uint8_t sc = ((val ? cache.v_scales : cache.k_scales) + (int64_t)grp * D)[(d0 & ~15) + place];
+                *(const uint32_t*)((val ? cache.v_codes : cache.k_codes) + grp * (8 * D) + place * (D / 2) + d0 / 2);
+            const uint8_t sc = ((val ? cache.v_scales : cache.k_scales) + grp * D)[(d0 & ~15) + place];
             const float s = __builtin_amdgcn_cvt_pk_f32_fp8((int)sc, false)[0];
             const float g = (val ? cache.v_scale : cache.k_scale)[head];
             const f32x2 e0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);

@@ -162,6 +162,29 @@ def test_append_and_read(D, Hq, H, page, news, lens, rot, interleaved):
         assert torch.equal(back[i].cpu(), held.float().to(BF)), name
 
 
+def test_append_ties_go_to_the_even_code():
+    """Quotients on every border, next to it and beyond the largest code, of both signs: scales that are powers of two
+    make them exact."""
+    border = torch.tensor([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0]).to(BF)
+    above, below = ((border.view(torch.int16) + i).view(BF) for i in (1, -1))
+    t = torch.cat((border, above, below, torch.tensor([0., .5, 1., 1.5, 2., 3., 4., 6., 5.75]).to(BF))).float()
+    t = torch.cat((t, -t, torch.tensor([0., -0., 6., -6.])))           # 64 quotients
+    blocks = torch.cat((t.view(-1, 8), torch.full((len(t) // 8, 1), 6.0), torch.zeros(len(t) // 8, 7)), 1)
+    k = blocks.reshape(1, 1, 128).to(BF)                                # each block's largest is 6, so its step is 1
+    assert torch.equal(k.float().view(-1), blocks.view(-1))
+    cache = U.Cache(gen(22), [1], H=1, D=128, page=16, poison=False)
+    cache.scale = {n: torch.tensor([2.0 ** -4]) for n in "kv"}
+    dev = [x.to(DEV) for x in cache.tensors("cpu")]
+    args = (torch.tensor([0, 1], dtype=torch.int32, device=DEV), torch.tensor([1], dtype=torch.int32, device=DEV),
+            cache.table.to(DEV))
+    ple.ple_kv4_append(ple.KV4Cache(*dev), k.to(DEV), k.to(DEV), *args)
+    codes, scales = U.quantise(k.float(), cache.scale["k"][:, None])
+    assert (scales == torch.tensor(16.0).to(torch.float8_e4m3fn).view(torch.uint8)).all()
+    page = int(cache.table[0, 0])
+    for i in (0, 2):
+        assert torch.equal(U.nibbles(dev[i].cpu()[page, 0, 0]), U.nibbles(codes[0, 0]))
+
+
 def test_append_bad_pages_and_places_write_nothing():
     """Table entries outside the cache, and tokens before position 0: dropped, read back as zeros."""
     g = gen(5)
