@@ -8,7 +8,8 @@ a paged 4-bit key/value cache and attention over it.
     out, lse = ple_kv4_attention(q, cache, query_start_loc, seq_lens, page_table, want_lse=True)
 
 Like the rest of the binding these only marshal tensors; the header states
-formats, layouts and limits.
+formats, layouts and limits.  Outputs and workspaces that a call makes itself
+belong to the stream it runs on (`stream`, or the current one).
 """
 from __future__ import annotations
 
@@ -29,10 +30,24 @@ def _raw_stream(device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _new(shape, dtype, device):
-    """torch.empty for two or three dimensions, in 1.3 us where that takes 2.0."""
+def _on(stream, device):
+    """The context for memory that work on `stream` writes.  The allocator hands out what was freed in the current
+    stream's order, so a block from its pool may still be in use by work queued there, which `stream` does not wait
+    for; memory taken on `stream` itself follows that stream's order, when it is taken and when it is given back."""
+    if isinstance(stream, int):  # a handle; 0 is the default stream, which ExternalStream would not take it for
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _new(shape, dtype, device, stream=None):
+    """torch.empty for two or three dimensions, in 1.3 us where that takes 2.0, for a call on `stream`."""
     strides = (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1)
-    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    with _on(stream, device):
+        t = torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))  # where the caller most likely reads it before giving it up
+    return t
 
 
 def _fits(t, dtype, shape, device: int) -> bool:
@@ -85,7 +100,7 @@ def ple_w4_linear(x, w: W4Weight, *, out=None, stream=None):
     if out is None:
         if x.get_device() != w.device:
             _same_device(x, w.codes)
-        out = _new((T, w.out_dim), _BF, x.device)
+        out = _new((T, w.out_dim), _BF, x.device, stream)
     else:
         _req("out", out, (T, w.out_dim), _BF16)
         _same_device(x, w.codes, out)
@@ -146,10 +161,10 @@ def _kv4_batch(cache, query_start_loc, seq_lens, page_table, T, max_request_toke
                               page_table.shape[1], max_request_tokens, max_seq_len)
 
 
-def _out(name, t, shape, dtypes, cache):
-    """An output: the caller's, checked, or a new one."""
+def _out(name, t, shape, dtypes, cache, stream):
+    """An output of a call on `stream`: the caller's, checked, or a new one."""
     if t is None:
-        return _new(shape, dtypes[0], cache.tensors[0].device)
+        return _new(shape, dtypes[0], cache.tensors[0].device, stream)
     _req(name, t, shape, dtypes)
     _same_device(cache.tensors[0], t)
     return t
@@ -165,7 +180,7 @@ def ple_kv4_append(cache: KV4Cache, k, v, query_start_loc, seq_lens, page_table,
     q_at = out_at = freq_at = None
     if q is not None:
         qs, hq = _heads("q", q, T, None, cache), q.shape[1]
-        q_out = _out("q_out", q_out, (T, hq, D), _BF16, cache)
+        q_out = _out("q_out", q_out, (T, hq, D), _BF16, cache, stream)
         q_at, out_at = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out given without q")
@@ -191,8 +206,8 @@ def ple_kv4_read(cache: KV4Cache, query_start_loc, seq_lens, page_table, num_tok
     """The new tokens' keys and values as the cache holds them: two bf16 [T][heads][D]."""
     T = int(num_tokens)
     shape = (T, cache.num_kv_heads, cache.head_dim)
-    k_out = _out("k_out", k_out, shape, _BF16, cache)
-    v_out = _out("v_out", v_out, shape, _BF16, cache)
+    k_out = _out("k_out", k_out, shape, _BF16, cache, stream)
+    v_out = _out("v_out", v_out, shape, _BF16, cache, stream)
     b = _kv4_batch(cache, query_start_loc, seq_lens, page_table, T)
     rc = capi.load().ple_kv4_read(ctypes.byref(cache.desc), ctypes.byref(b), k_out.data_ptr(), v_out.data_ptr(),
                                   _raw_stream(cache.device) if stream is None else _stream(stream))
@@ -221,9 +236,9 @@ def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table,
     [T][q heads] or None)."""
     D, T = cache.head_dim, q.shape[0]
     qs, hq = _heads("q", q, T, None, cache), q.shape[1]
-    out = _out("out", out, (T, hq, D), _BF16, cache)
+    out = _out("out", out, (T, hq, D), _BF16, cache, stream)
     if lse is not None or want_lse:
-        lse = _out("lse", lse, (T, hq), _F32, cache)
+        lse = _out("lse", lse, (T, hq), _F32, cache, stream)
     b = _kv4_batch(cache, query_start_loc, seq_lens, page_table, T, max_request_tokens, max_seq_len)
     if q.get_device() != cache.device:
         _same_device(cache.tensors[0], q)
@@ -237,10 +252,12 @@ def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table,
         need = int(lib.ple_kv4_attention_workspace_bytes(hq, ctypes.byref(cache.desc), ctypes.byref(b), window))
         cache._workspaces[sizes] = need
     if workspace is None:
-        if need > 0:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-            if stream is not None:  # it is given up here, before the work on that stream has ended
-                workspace.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        if need > 0:  # (given up on return, before the work has ended: taken in the order of the stream it runs on)
+            if stream is None:
+                workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+            else:
+                with _on(stream, q.device):
+                    workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
     else:
         _req_bytes("workspace", workspace, need)
         _same_device(cache.tensors[0], workspace)
