@@ -85,7 +85,11 @@ typedef struct ple_kv4_cache {
  * What the device reads of these is clamped: a sequence to what its row of
  * the page table covers, a token window to [0, T].  A table entry outside
  * [0, num_pages) names no page: append drops what would go there, read gives
- * zeros and attention leaves its tokens out.
+ * zeros and attention leaves its tokens out.  query_start_loc has to be
+ * non-decreasing; tokens before query_start_loc[0] or from query_start_loc[R]
+ * on (a batch padded to a captured graph's T) belong to no request: append
+ * drops their keys and values and leaves their queries unrotated, read gives
+ * zeros.
  */
 typedef struct ple_kv4_batch {
     const int32_t* query_start_loc; /* device [R+1] */

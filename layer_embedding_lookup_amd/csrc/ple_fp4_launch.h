@@ -63,11 +63,13 @@ __host__ __device__ __forceinline__ int kv4_group(const ple_kv4_cache& c, const 
     return (page * c.num_kv_heads + head) * per_page + (g - p * per_page);
 }
 
-// Request of token t and its position; -1 if the token stands nowhere (before position 0 or past the table).
+// Request of token t and its position; -1 if the token stands nowhere: in no request's tokens (a padded batch; the last
+// request's places past its length may be another's), before position 0 or past the table.
 __device__ __forceinline__ int kv4_position(const ple_kv4_cache& c, const ple_kv4_batch& b, int64_t t, int& r) {
     r = find_request(b.query_start_loc, b.num_reqs, t);
-    const int64_t p = (int64_t)b.seq_lens[r] - ((int64_t)b.query_start_loc[r + 1] - t);
-    return p < 0 || p >= (int64_t)b.table_width * c.page_size ? -1 : (int)p;
+    const int64_t from = b.query_start_loc[r], to = b.query_start_loc[r + 1];
+    const int64_t p = (int64_t)b.seq_lens[r] - (to - t);
+    return t < from || t >= to || p < 0 || p >= (int64_t)b.table_width * c.page_size ? -1 : (int)p;
 }
 
 }  // namespace ple
