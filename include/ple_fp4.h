@@ -89,7 +89,7 @@ typedef struct ple_kv4_cache {
  * non-decreasing; tokens before query_start_loc[0] or from query_start_loc[R]
  * on (a batch padded to a captured graph's T) belong to no request: append
  * drops their keys and values and leaves their queries unrotated, read gives
- * zeros.
+ * zeros and attention rows that see nothing.
  */
 typedef struct ple_kv4_batch {
     const int32_t* query_start_loc; /* device [R+1] */

@@ -67,6 +67,24 @@ __device__ __forceinline__ void attn_request(const Kv4AttentionArgs& a, int r, A
     w.len = min(a.batch.seq_lens[r], a.batch.table_width * a.cache.page_size);
 }
 
+// Tokens of no request (a batch padded to a graph's size): their rows of `out` are zeros and of `lse` -inf.  The blocks
+// share them token by token; mostly there are none, and the two entries come with those of the block's own request.
+__device__ __forceinline__ void attn_idle_tokens(const Kv4AttentionArgs& a) {
+    const int64_t T = a.batch.num_tokens;
+    int64_t first = a.batch.query_start_loc[0], last = a.batch.query_start_loc[a.batch.num_reqs];
+    first = first < 0 ? 0 : (first > T ? T : first);
+    last = last < first ? first : (last > T ? T : last);
+    const int64_t idle = first + (T - last);
+    if (idle == 0) return;
+    const int row = a.num_q_heads * a.cache.head_dim;
+    for (int64_t i = (int64_t)blockIdx.y * gridDim.x + blockIdx.x; i < idle; i += (int64_t)gridDim.x * gridDim.y) {
+        const int64_t t = i < first ? i : last + (i - first);
+        for (int e = threadIdx.x * 8; e < row; e += blockDim.x * 8) *(u32x4*)(a.out + t * row + e) = u32x4{0u, 0u, 0u, 0u};
+        if (a.lse != nullptr)
+            for (int h = threadIdx.x; h < a.num_q_heads; h += blockDim.x) a.lse[t * a.num_q_heads + h] = -__builtin_inff();
+    }
+}
+
 // Its query tile; false if it has no such tile.
 __device__ __forceinline__ bool attn_tile(const Kv4AttentionArgs& a, int tile, AttnTile& w) {
     w.row0 = tile * a.rows;
@@ -286,6 +304,7 @@ __device__ __forceinline__ void attn_body(const Kv4AttentionArgs& a) {
     attn_block(a, r, head, tile);
     AttnTile w;
     attn_request(a, r, w);
+    attn_idle_tokens(a);
     if (!attn_tile(a, tile, w)) return;
     const int splits = attn_splits(a, w);
     if (split >= splits) return;
@@ -949,6 +968,7 @@ __device__ __forceinline__ void attn_chunk_body(const Kv4AttentionArgs& a) {
     // blocks of an XCD (block number mod 8) take neighbouring shares, which read the same heads
     const int share = (a.flat & 7) == 0 ? (int)(blockIdx.x & 7) * (a.flat >> 3) + (int)(blockIdx.x >> 3) : (int)blockIdx.x;
     AttnFlat f;
+    attn_idle_tokens(a);
     if (a.flat == 0) {
         attn_block(a, r, head, tile);
         attn_request(a, r, w);

@@ -45,3 +45,27 @@ def test_tokens_of_no_request(qsl, T):
     assert torch.equal(out_q[a:b], own_q) and torch.equal(out_q[idle], q[idle])
     for x, y in zip(ple.ple_kv4_read(c, *args, T), ple.ple_kv4_read(oc, *own, b - a)):
         assert (x[idle] == 0).all() and torch.equal(x[a:b], y)
+
+
+@pytest.mark.parametrize("D,Hq,H,qsl,lens,T,hint", [
+    (128, 4, 2, [0, 1, 2], [300, 40], 9, 1), (64, 4, 1, [2, 3], [5000], 70, 1), (256, 2, 1, [1, 3, 3, 5], [90, 8, 33], 600, 2),
+    (128, 8, 2, [5, 60, 200], [500, 140], 333, 140), (64, 2, 2, [7, 80], [73], 100, 73), (256, 4, 1, [0, 90], [300], 91, 90),
+    (128, 2, 1, [3] + [3 + 20 * (i + 1) for i in range(65)], [20] * 65, 1310, 128), (128, 4, 4, [0, 0], [9], 33, 0)])
+def test_attention_of_tokens_of_no_request(D, Hq, H, qsl, lens, T, hint):
+    print(f"idle tokens D={D} Hq={Hq} H={H} T={T}", flush=True)
+    g = torch.Generator().manual_seed(T + D)
+    cache = U.Cache(g, lens, H=H, D=D, page=16)
+    q = torch.randn((T, Hq, D), generator=g).to(BF).to(DEV)
+    _, c, args = tensors(cache, qsl, lens, cache.table)
+    out = torch.full((T, Hq, D), math.nan, dtype=BF, device=DEV)
+    lse = torch.full((T, Hq), math.nan, device=DEV)
+    ple.ple_kv4_attention(q, c, *args, max_request_tokens=hint, max_seq_len=max(lens), out=out, lse=lse)
+    idle = [t for t in range(T) if t < qsl[0] or t >= qsl[-1]]
+    assert (out[idle] == 0).all() and (lse[idle] == -math.inf).all()
+    want, want_lse, tol, tol_lse = U.attention(cache, q.cpu(), qsl, torch.tensor(lens))
+    a, b = qsl[0], qsl[-1]
+    assert ((out.cpu().to(F64) - want).abs() <= tol)[a:b].all()
+    assert ((lse.cpu().to(F64) - want_lse).abs() <= tol_lse)[a:b].all()
+    out.fill_(math.nan)
+    ple.ple_kv4_attention(q, c, *args, max_request_tokens=hint, max_seq_len=max(lens), out=out)
+    assert (out[idle] == 0).all()
