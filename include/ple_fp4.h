@@ -82,10 +82,11 @@ typedef struct ple_kv4_cache {
  * One ragged batch: request r has the new tokens [query_start_loc[r],
  * query_start_loc[r+1]) of the call's T and, with them, seq_lens[r] tokens in
  * all, so new token t stands at position seq_lens[r] - (query_start_loc[r+1] - t).
- * What the device reads of these is clamped: a sequence to what its row of
- * the page table covers, a token window to [0, T].  A table entry outside
- * [0, num_pages) names no page: append drops what would go there, read gives
- * zeros and attention leaves its tokens out.  query_start_loc has to be
+ * That holds for a request that runs past T too, whose first tokens the call
+ * has, and for a sequence longer than its row of the page table covers.
+ * Positions past what the row covers, and those whose table entry lies outside
+ * [0, num_pages), are on no page: append drops what would go there, read gives
+ * zeros and attention leaves those tokens out.  query_start_loc has to be
  * non-decreasing; tokens before query_start_loc[0] or from query_start_loc[R]
  * on (a batch padded to a captured graph's T) belong to no request: append
  * drops their keys and values and leaves their queries unrotated, read gives

@@ -52,7 +52,8 @@ constexpr float kWeightShift = 8.0f, kSlack = 7.0f;
 // What a block's query tile sees: rows [row0, row1) of request r, cache tokens [lo, hi).
 struct AttnTile {
     int64_t first;  // first new token of the request
-    int n, len;     // its new tokens, its length
+    int n, len;     // its new tokens, its length as far as the page table covers it
+    int before;     // position of its first new token
     int row0, row1;
     int first_seen;  // the first token that any row sees
     int lo, hi;      // lo: first_seen rounded down to a group of 16
@@ -60,11 +61,14 @@ struct AttnTile {
 
 // Request r of the batch, its query tiles not yet looked at.
 __device__ __forceinline__ void attn_request(const Kv4AttentionArgs& a, int r, AttnTile& w) {
-    int64_t q0, q1;
-    carried_window(a.batch.query_start_loc, a.batch.num_tokens, r, nullptr, q0, q1);
+    const int T = (int)a.batch.num_tokens, seq = max(a.batch.seq_lens[r], 0);
+    const int q0 = min(max(a.batch.query_start_loc[r], 0), T), to = a.batch.query_start_loc[r + 1];
     w.first = q0;
-    w.n = (int)(q1 - q0);
-    w.len = min(a.batch.seq_lens[r], a.batch.table_width * a.cache.page_size);
+    w.n = max(min(to, T), q0) - q0;
+    w.len = min(seq, a.batch.table_width * a.cache.page_size);
+    // As for append, by the whole length and all of the request's tokens.  Where it has new tokens, `to - q0` lies in
+    // 1 .. 2^31 - 1; further before position 0 than there are new tokens is the same as that far.
+    w.before = max((int)((uint32_t)seq - ((uint32_t)to - (uint32_t)q0)), -w.n);
 }
 
 // Tokens of no request (a batch padded to a graph's size): their rows of `out` are zeros and of `lse` -inf.  The blocks
@@ -90,9 +94,8 @@ __device__ __forceinline__ bool attn_tile(const Kv4AttentionArgs& a, int tile, A
     w.row0 = tile * a.rows;
     w.row1 = min(w.row0 + a.rows, w.n * a.group);
     if (w.row0 >= w.row1) return false;
-    const int before = w.len - w.n;  // position of new token 0
-    w.hi = max(0, min(w.len, before + (w.row1 - 1) / a.group + 1));
-    w.first_seen = a.window > 0 ? max(0, before + w.row0 / a.group - a.window + 1) : 0;
+    w.hi = max(0, min(w.len, w.before + (w.row1 - 1) / a.group + 1));
+    w.first_seen = a.window > 0 ? max(0, w.before + w.row0 / a.group - a.window + 1) : 0;
     w.lo = min(w.first_seen & ~15, w.hi & ~15);
     return true;
 }
@@ -185,7 +188,6 @@ __device__ __forceinline__ void attn_queries(const Kv4AttentionArgs& a, const At
                                              int end, f16x8 (&q)[MT][D / 32], float (&qs)[MT], int (&see_lo)[MT],
                                              int (&see_hi)[MT]) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    const int before = w.len - w.n;
     const float base = a.scale * 1.44269504088896341f * a.cache.k_scale[head];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -222,7 +224,7 @@ __device__ __forceinline__ void attn_queries(const Kv4AttentionArgs& a, const At
                 q[mt][ks][2 * j] = (_Float16)(bf16_lo(raw[ks][j]) * up);
                 q[mt][ks][2 * j + 1] = (_Float16)(bf16_hi(raw[ks][j]) * up);
             }
-        const int p = before + i;
+        const int p = w.before + i;
         // (rows past the tile's end, all zeros and never stored, see everything, which keeps the masks out of whole tiles)
         see_hi[mt] = live ? min(end, p + 1) : end;
         see_lo[mt] = live ? max(begin, a.window > 0 ? p - a.window + 1 : 0) : begin;
@@ -633,15 +635,16 @@ struct ChunkShape {
 // A chunk of 1289 + 1455 tokens at 5403 and 2004: 308 us with a block a query tile (CUs busy for 53% of it).
 struct AttnFlat {
     // of lane r:
-    int first, n, len;  // request r's first new token, new tokens, length
-    int tiles_of;       // the places of one of its heads
-    int before;         // and those of all heads of the requests before it
+    int first, n, len, pos;  // request r's first new token, new tokens, length, position of the first new token
+    int tiles_of;            // the places of one of its heads
+    int before;              // and those of all heads of the requests before it
     int total, quota;
 
     __device__ __forceinline__ void request(int r, AttnTile& w) const {
         w.first = __builtin_amdgcn_readlane(first, r);
         w.n = __builtin_amdgcn_readlane(n, r);
         w.len = __builtin_amdgcn_readlane(len, r);
+        w.before = __builtin_amdgcn_readlane(pos, r);
     }
 
     static __device__ __forceinline__ int count(const AttnTile& w) { return max(1, (w.hi - w.lo + kTile - 1) / kTile); }
@@ -657,6 +660,7 @@ struct AttnFlat {
         first = (int)w.first;
         n = w.n;
         len = w.len;
+        pos = w.before;
         tiles_of = 0;
         if (a.tiles < 4 * a.batch.num_reqs) {  // a lane a request, or the wave for one after the other: what is shorter
             for (int t = 0, c; (c = places(a, t, w)) > 0; ++t) tiles_of += c;
@@ -737,10 +741,9 @@ __device__ __forceinline__ void attn_chunk_piece(const Kv4AttentionArgs& a, cons
     extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    const int before = w.len - w.n;
     // what every row of the block sees
-    const int common_lo = a.window > 0 ? max(0, before + (w.row1 - 1) / a.group - a.window + 1) : 0;
-    const int common_hi = min(end, before + w.row0 / a.group + 1);
+    const int common_lo = a.window > 0 ? max(0, w.before + (w.row1 - 1) / a.group - a.window + 1) : 0;
+    const int common_hi = min(end, w.before + w.row0 / a.group + 1);
 
     const int32_t* table_row = a.batch.page_table + (int64_t)r * a.batch.table_width;
     const uint32_t pick = (uint32_t)((n & 3) | ((4 + (n & 3)) << 8));

@@ -69,3 +69,78 @@ def test_attention_of_tokens_of_no_request(D, Hq, H, qsl, lens, T, hint):
     out.fill_(math.nan)
     ple.ple_kv4_attention(q, c, *args, max_request_tokens=hint, max_seq_len=max(lens), out=out)
     assert (out[idle] == 0).all()
+
+
+@pytest.mark.parametrize("D,Hq,n,extra,window", [(128, 4, 10, 6, 0), (64, 2, 3, 2, 0), (128, 2, 10, 6, 8), (128, 8, 40, 30, 0),
+                                                 (256, 4, 40, 30, 16), (128, 4, 10, 40, 8), (64, 8, 60, 70, 32)])
+def test_sequences_longer_than_the_table(D, Hq, n, extra, window):
+    """A sequence of `extra` tokens more than the 64 that its table row covers: the tokens past it stand on no page, the
+    others keep their positions."""
+    g = torch.Generator().manual_seed(n + extra)
+    lens = [64 + extra, 64]
+    cache = U.Cache(g, lens, H=1, D=D, page=16, poison=False)
+    cache.table[:, 4:] = -7                                    # (the definition's table: these pages do not exist)
+    qsl, seq = torch.tensor([0, n, n + 1], dtype=I32), torch.tensor(lens, dtype=I32)
+    q, k = (torch.randn((n + 1, h, D), generator=g).to(BF) for h in (Hq, 1))
+    dev, c, args = tensors(cache, qsl, seq, cache.table[:, :4].contiguous())
+    out, lse = ple.ple_kv4_attention(q.to(DEV), c, *args, window=window, want_lse=True)
+    want, want_lse, tol, tol_lse = U.attention(cache, q, qsl, seq, window)
+    empty = want_lse == -math.inf
+    assert torch.equal(lse.cpu() == -math.inf, empty) and (out.cpu()[empty] == 0).all()
+    assert ((out.cpu().to(F64) - want).abs() <= tol).all()
+    assert ((lse.cpu().to(F64) - want_lse).abs() <= tol_lse)[~empty].all()
+    ple.ple_kv4_append(c, k.to(DEV), k.to(DEV), *args)
+    got, _ = ple.ple_kv4_read(c, *args, n + 1)
+    stored = torch.cat((lens[0] - n + torch.arange(n) < 64, torch.tensor([True])))
+    assert (got.cpu()[~stored] == 0).all() and (got.cpu()[stored].flatten(1) != 0).any(1).all()
+    codes, _ = U.quantise(k.float(), cache.scale["k"][:, None])
+    for t in range(n):
+        p = lens[0] - n + t
+        if p < 64:
+            assert torch.equal(dev[0].cpu()[int(cache.table[0, p // 16]), :, p % 16], codes[t])
+
+
+@pytest.mark.parametrize("n,T", [(10, 6), (100, 70), (64, 1)])
+def test_requests_longer_than_the_call(n, T):
+    """query_start_loc that runs past T: the tokens that are there stand where they would in the whole request."""
+    g = torch.Generator().manual_seed(n)
+    cache = U.Cache(g, [200], H=2, D=128, page=16)
+    qsl, seq = torch.tensor([0, n], dtype=I32), torch.tensor([200], dtype=I32)
+    q = torch.randn((n, 4, 128), generator=g).to(BF)
+    _, c, args = tensors(cache, qsl, seq, cache.table)
+    out, lse = ple.ple_kv4_attention(q[:T].to(DEV), c, *args, want_lse=True)
+    want, want_lse, tol, tol_lse = U.attention(cache, q, qsl, seq)
+    assert ((out.cpu().to(F64) - want[:T]).abs() <= tol[:T]).all()
+    assert ((lse.cpu().to(F64) - want_lse[:T]).abs() <= tol_lse[:T]).all()
+
+
+def test_lengths_at_the_ends_of_their_type():
+    g = torch.Generator().manual_seed(3)
+    lens = [40, -2 ** 31, 2 ** 31 - 1, 2 ** 31 - 1]
+    cache = U.Cache(g, [40, 0, 0, 48], H=1, D=64, page=16)
+    qsl = [0, 1, 3, 4, 44]
+    q = torch.randn((44, 2, 64), generator=g).to(BF).to(DEV)
+    _, c, args = tensors(cache, qsl, lens, cache.table)
+    for window in (0, 7, 2 ** 30 - 1):
+        out, lse = ple.ple_kv4_attention(q, c, *args, window=window, want_lse=True)
+        assert (out[1:4] == 0).all() and (lse[1:4] == -math.inf).all()
+        # request 3 stands far past its 48 tokens: its rows see all of them without a window, none with one
+        assert torch.isfinite(out).all() and ((lse[4:] == -math.inf) == (window > 0)).all()
+        want, want_lse, tol, tol_lse = U.attention(cache, q[:1].cpu(), [0, 1], [40], window)
+        assert ((out[:1].cpu().to(F64) - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("qsl", [[-2 ** 31, 3, 5], [0, -2 ** 31, 5], [5, 2, 2 ** 31 - 1], [2 ** 31 - 1, 0, -2 ** 31]])
+def test_broken_offsets_stay_in_bounds(qsl):
+    """Offsets at the ends of their type and falling ones: results are unspecified, what surrounds the outputs and the
+    cache's other tensors stays."""
+    g = torch.Generator().manual_seed(8)
+    cache = U.Cache(g, [90, 30], H=1, D=64, page=16)
+    q = torch.randn((5, 2, 64), generator=g).to(BF).to(DEV)
+    for hint in (0, 1):
+        _, c, args = tensors(cache, qsl, [90, 30], cache.table)
+        out, lse = torch.full((15, 2, 64), 7, dtype=BF, device=DEV), torch.full((16, 2), 7.0, device=DEV)
+        ple.ple_kv4_attention(q, c, *args, max_request_tokens=hint, out=out[5:10], lse=lse[4:9])
+        assert (out[:5] == 7).all() and (out[10:] == 7).all() and (lse[:4] == 7).all() and (lse[9:] == 7).all()
+        ple.ple_kv4_read(c, *args, 5, k_out=(k := torch.full((15, 1, 64), 7, dtype=BF, device=DEV))[5:10], v_out=k.clone()[5:10])
+        assert (k[:5] == 7).all() and (k[10:] == 7).all()
