@@ -17,6 +17,12 @@ namespace ple {
 
 constexpr int kAppendThreads = 256;
 
+// A block per token: along x as many as a launch takes with room to spare, the rest along y.
+constexpr int64_t kAppendAcross = 1 << 20;
+static dim3 append_grid(int64_t T) {
+    return dim3((unsigned)(T < kAppendAcross ? T : kAppendAcross), (unsigned)((T + kAppendAcross - 1) / kAppendAcross));
+}
+
 __device__ __forceinline__ void load8(const uint16_t* __restrict__ p, float (&v)[8]) {
     const u32x4 w = *(const u32x4*)p;
 #pragma unroll
@@ -50,7 +56,8 @@ __device__ __forceinline__ int64_t first_group(const ple_kv4_cache& c, const int
 
 __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArgs a) {
     __shared__ double2 turn[128];  // cos, sin of the token's angles
-    const int64_t t = blockIdx.x;
+    const int64_t t = blockIdx.x + blockIdx.y * kAppendAcross;
+    if (t >= a.batch.num_tokens) return;
     const int D = a.cache.head_dim, half = a.rot_dim / 2;
     const int per_head = D / 8, shift = D == 64 ? 3 : (D == 128 ? 4 : 5);  // chunks of a head
     int r;
@@ -132,7 +139,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArg
 }
 
 hipError_t launch_kv4_append(const Kv4AppendArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(kv4_append_kernel, dim3((unsigned)a.batch.num_tokens), dim3(kAppendThreads), 0, s, a);
+    hipLaunchKernelGGL(kv4_append_kernel, append_grid(a.batch.num_tokens), dim3(kAppendThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -140,7 +147,8 @@ hipError_t launch_kv4_append(const Kv4AppendArgs& a, hipStream_t s) {
 __global__ __launch_bounds__(kAppendThreads) void kv4_read_kernel(ple_kv4_cache cache, ple_kv4_batch batch,
                                                                   uint16_t* __restrict__ k_out,
                                                                   uint16_t* __restrict__ v_out) {
-    const int64_t t = blockIdx.x;
+    const int64_t t = blockIdx.x + blockIdx.y * kAppendAcross;
+    if (t >= batch.num_tokens) return;
     const int D = cache.head_dim, per_head = D / 8, shift = D == 64 ? 3 : (D == 128 ? 4 : 5);
     int r;
     const int pos = kv4_position(cache, batch, t, r);
@@ -175,7 +183,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_read_kernel(ple_kv4_cache 
 
 hipError_t launch_kv4_read(const ple_kv4_cache& cache, const ple_kv4_batch& batch, uint16_t* k_out, uint16_t* v_out,
                            hipStream_t s) {
-    hipLaunchKernelGGL(kv4_read_kernel, dim3((unsigned)batch.num_tokens), dim3(kAppendThreads), 0, s, cache, batch,
+    hipLaunchKernelGGL(kv4_read_kernel, append_grid(batch.num_tokens), dim3(kAppendThreads), 0, s, cache, batch,
                        k_out, v_out);
     return hipGetLastError();
 }
