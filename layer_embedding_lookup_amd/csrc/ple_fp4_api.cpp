@@ -106,9 +106,9 @@ int plan_attention(int32_t num_q_heads, const ple_kv4_cache* cache, const ple_kv
     a->group = num_q_heads / cache->num_kv_heads;
     a->window = window < (1 << 30) ? window : 0;  // wider than any sequence: none
     plan_kv4_attention(*a);
-    if ((int64_t)batch->num_reqs * cache->num_kv_heads * a->tiles >= ((int64_t)1 << 31))
-        return fail(PLE_ERR_UNSUPPORTED, "%d requests of up to %d query tiles exceed the launch; pass max_request_tokens",
-                    batch->num_reqs, a->tiles);
+    if (kv4_attention_threads(*a) > kMostThreads)
+        return fail(PLE_ERR_UNSUPPORTED, "%d requests of up to %d query tiles need a launch of 2^32 threads or more; pass "
+                    "max_request_tokens", batch->num_reqs, a->tiles);
     return PLE_OK;
 }
 

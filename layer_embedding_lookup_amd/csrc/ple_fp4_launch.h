@@ -9,6 +9,9 @@ namespace ple {
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+// A launch holds below 2^32 threads along x.
+constexpr int64_t kMostThreads = ((int64_t)1 << 32) - 1;
+
 hipError_t launch_w4_linear(const uint16_t* x, int64_t x_stride, const ple_w4_weight& w, int64_t T, uint16_t* out,
                             hipStream_t s);
 
@@ -49,6 +52,8 @@ struct Kv4AttentionArgs {
 // The plan part of the arguments (rows, waves, tiles, flat, chunk, splits), from sizes and hints alone.
 void plan_kv4_attention(Kv4AttentionArgs& a);
 size_t kv4_attention_part_bytes(const Kv4AttentionArgs& a);
+// Most threads along x of the call's launches.
+int64_t kv4_attention_threads(const Kv4AttentionArgs& a);
 hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t s);
 
 // One 16-token group of the cache: its number ((page * heads + head) * page_size/16 + group in page), which

@@ -44,6 +44,7 @@ constexpr int kAttnWaves = 4;  // of a chunk block, and those whose sums a decod
 constexpr int kAttnThreads = kAttnWaves * kWave;
 constexpr int kTile = 64;  // cache tokens of a tile
 constexpr int kMostSplits = 1024;
+constexpr int kFewSplits = 8;  // up to which one wave joins a row
 // Weights are 2^(s - m + kWeightShift) with m a row's largest exponent but for kSlack: m only moves on, and the row's
 // sums are only rescaled, when the maximum has passed it by more than that.  Weights stay below 2^15 and fp16 keeps
 // them above 2^-24, so tokens down to 2^-32 of the heaviest one count.
@@ -1217,12 +1218,27 @@ size_t kv4_attention_part_bytes(const Kv4AttentionArgs& a) {
     return (size_t)a.batch.num_tokens * a.num_q_heads * a.splits * (a.cache.head_dim + 1) * sizeof(float);
 }
 
+// Query tiles of all requests and key heads, and blocks along x of the kernel that joins splits.
+static int64_t attention_units(const Kv4AttentionArgs& a) {
+    return (int64_t)a.batch.num_reqs * a.cache.num_kv_heads * a.tiles;
+}
+static int64_t join_blocks(const Kv4AttentionArgs& a) {
+    const int64_t rows = a.batch.num_tokens * a.num_q_heads;
+    return a.splits <= kFewSplits ? (rows + 3) / 4 : rows;
+}
+
+int64_t kv4_attention_threads(const Kv4AttentionArgs& a) {
+    // (the shares are at most 512 blocks, their join a block per unit)
+    const int64_t own = attention_units(a) * (a.flat > 0 ? 256 : a.waves * kWave);
+    const int64_t join = a.splits > 1 ? join_blocks(a) * 256 : 0;
+    return own > join ? own : join;
+}
+
 template <void (*FN)(Kv4AttentionArgs), int LDS>
 static hipError_t launch_attention(const Kv4AttentionArgs& a, int threads, hipStream_t s) {
     static const hipError_t attr = hipFuncSetAttribute((const void*)FN, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
     if (attr != hipSuccess) return attr;
-    const int64_t units = (int64_t)a.batch.num_reqs * a.cache.num_kv_heads * a.tiles;
-    const dim3 grid((unsigned)(a.flat > 0 ? a.flat : units), (unsigned)a.splits);
+    const dim3 grid((unsigned)(a.flat > 0 ? a.flat : attention_units(a)), (unsigned)a.splits);
     hipLaunchKernelGGL(FN, grid, dim3(threads), LDS, s, a);
     return hipGetLastError();
 }
@@ -1240,7 +1256,7 @@ hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t s) {
     PLE_ATTN_SHAPES(PLE_ATTN_LAUNCH)
 #undef PLE_ATTN_LAUNCH
     if (e == hipSuccess && a.flat > 0) {
-        const dim3 grid((unsigned)((int64_t)a.batch.num_reqs * a.cache.num_kv_heads * a.tiles), kChunkRows / kFlatJoinRows);
+        const dim3 grid((unsigned)attention_units(a), kChunkRows / kFlatJoinRows);
         if (D == 64)
             hipLaunchKernelGGL(kv4_attention_flat_join_64_kernel, grid, dim3(256), 0, s, a);
         else if (D == 128)
@@ -1250,9 +1266,8 @@ hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t s) {
         return hipGetLastError();
     }
     if (e != hipSuccess || a.splits <= 1) return e;
-    const int64_t rows = a.batch.num_tokens * a.num_q_heads;
-    const bool few = a.splits <= 8;
-    const dim3 grid((unsigned)(few ? (rows + 3) / 4 : rows));
+    const bool few = a.splits <= kFewSplits;
+    const dim3 grid((unsigned)join_blocks(a));
 #define PLE_ATTN_LAUNCH(DD)                                                                                          \
     if (D == DD) {                                                                                                   \
         if (few)                                                                                                     \

@@ -1,11 +1,30 @@
 """Calls at the limits that the header states and at those of a launch (below 2^32 threads along x)."""
+import ctypes
+
 import pytest
 import torch
 
 import fp4_util as U
 import layer_embedding_lookup_amd as ple
+from layer_embedding_lookup_amd import capi
 
+FAKE = 1 << 40
 DEV = "cuda:0"
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="made-up addresses stay off hosts with a GPU")
+@pytest.mark.parametrize("T,R,H,Hq,width,new,refused", [
+    (8192, 8192, 8, 32, 5, 0, True), (8192, 8192, 8, 32, 5, 1, False),   # 2^24 blocks of 256 threads, 2^16
+    (8191, 8191, 8, 32, 5, 0, False),                                    # 2^24 less 2048
+    (1 << 16, 1 << 16, 256, 256, 5, 1, True),                            # 2^24 blocks of four waves, a row each
+    (1 << 24, 1, 1, 64, 5000, 1, True)])                                # (a wrong hint: splits of one token, joined for 2^30 rows)
+def test_attention_launches(T, R, H, Hq, width, new, refused):
+    lib = capi.load()
+    cache = ctypes.byref(capi.ple_kv4_cache(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 10, H, 16, 128, 0))
+    batch = ctypes.byref(capi.ple_kv4_batch(FAKE, FAKE, FAKE, T, R, width, new, 0))
+    rc = lib.ple_kv4_attention(FAKE, Hq * 128, Hq, cache, batch, 0, 0.1, FAKE, None, FAKE, 1 << 62, None)
+    assert (rc == capi.PLE_ERR_UNSUPPORTED and "max_request_tokens" in ple.ple_error_message()) == refused
+    assert rc != capi.PLE_ERR_INVALID_ARGUMENT
 
 
 @pytest.mark.gpu
