@@ -12,6 +12,12 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 // A launch holds below 2^32 threads along x.
 constexpr int64_t kMostThreads = ((int64_t)1 << 32) - 1;
 
+// The linear kernel of a call: the many-token or the few-token one, in token and feature tiles of a block.
+struct W4Shape {
+    bool many;
+    int mt, nt;
+};
+W4Shape w4_linear_shape(int64_t T, int32_t out_dim, int32_t group);
 hipError_t launch_w4_linear(const uint16_t* x, int64_t x_stride, const ple_w4_weight& w, int64_t T, uint16_t* out,
                             hipStream_t s);
 

@@ -520,29 +520,36 @@ static hipError_t launch_gemm(const W4Args& a, hipStream_t s) {
     return launch_blocks<FN, Sh::LDS>(a, (unsigned)((a.T + Sh::T - 1) / Sh::T * ((a.O + Sh::O - 1) / Sh::O)), kGemmThreads, s);
 }
 
-hipError_t launch_w4_linear(const uint16_t* x, int64_t x_stride, const ple_w4_weight& w, int64_t T, uint16_t* out,
-                            hipStream_t s) {
-    const W4Args a = {x, x_stride, w.codes, w.scales, w.zeros, w.tensor_scale, T, w.out_dim, w.k_dim, out};
+W4Shape w4_linear_shape(int64_t T, int32_t out_dim, int32_t group) {
     // Tiles of the many-token kernel where there are enough of them for the CUs, below that blocks that split K between
     // their waves (K = 4096: 320 tiles NVFP4 43 us against 47, INT4 in groups of 32 90 against 81; 512 tiles 50 against 67
     // and 91 against 109).
-    const int64_t features = (w.out_dim + 127) / 128;
-    if (T > 64 && (T + 63) / 64 * features > (w.group == 16 ? 256 : 384)) {
+    const int64_t features = (out_dim + 127) / 128;
+    if (T > 64 && (T + 63) / 64 * features > (group == 16 ? 256 : 384)) {
         // 128 tokens a block where that leaves two blocks per CU (8192 x 4096 NVFP4: T = 1024 70 us against 92, T = 500,
         // 256 blocks, 57 against 48)
-        const bool tall = (T + 127) / 128 * features >= 512;
-        switch (w.group) {
-            case 16: return tall ? launch_gemm<w4_gemm_8x2_16_kernel, 8, 2>(a, s) : launch_gemm<w4_gemm_4x2_16_kernel, 4, 2>(a, s);
-            case 32: return launch_gemm<w4_gemm_4x2_32_kernel, 4, 2>(a, s);
-            case 64: return launch_gemm<w4_gemm_4x2_64_kernel, 4, 2>(a, s);
-            default: return tall ? launch_gemm<w4_gemm_8x2_128_kernel, 8, 2>(a, s) : launch_gemm<w4_gemm_4x2_128_kernel, 4, 2>(a, s);
-        }
+        const bool tall = (group == 16 || group == 128) && (T + 127) / 128 * features >= 512;
+        return {true, tall ? 8 : 4, 2};
     }
     const int mt = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
     // Feature tiles of a block of 64 tokens: as few as keep one block per CU (its inputs fill the LDS; 100 tokens
     // 4096 -> 5003 NVFP4: 22 us in 314 blocks of two, 17 in 158 of four).
     const int64_t rows = (T + 63) / 64;
-    const int nt = mt < 4 || rows * ((w.out_dim + 15) / 16) <= 256 ? 1 : (rows * ((w.out_dim + 31) / 32) <= 256 ? 2 : 4);
+    const int nt = mt < 4 || rows * ((out_dim + 15) / 16) <= 256 ? 1 : (rows * ((out_dim + 31) / 32) <= 256 ? 2 : 4);
+    return {false, mt, nt};
+}
+
+hipError_t launch_w4_linear(const uint16_t* x, int64_t x_stride, const ple_w4_weight& w, int64_t T, uint16_t* out,
+                            hipStream_t s) {
+    const W4Args a = {x, x_stride, w.codes, w.scales, w.zeros, w.tensor_scale, T, w.out_dim, w.k_dim, out};
+    const W4Shape shape = w4_linear_shape(T, w.out_dim, w.group);
+    const int mt = shape.mt, nt = shape.nt;
+    if (shape.many) switch (w.group) {
+            case 16: return mt == 8 ? launch_gemm<w4_gemm_8x2_16_kernel, 8, 2>(a, s) : launch_gemm<w4_gemm_4x2_16_kernel, 4, 2>(a, s);
+            case 32: return launch_gemm<w4_gemm_4x2_32_kernel, 4, 2>(a, s);
+            case 64: return launch_gemm<w4_gemm_4x2_64_kernel, 4, 2>(a, s);
+            default: return mt == 8 ? launch_gemm<w4_gemm_8x2_128_kernel, 8, 2>(a, s) : launch_gemm<w4_gemm_4x2_128_kernel, 4, 2>(a, s);
+        }
     const unsigned blocks = (unsigned)((w.out_dim + 16 * nt - 1) / (16 * nt) * ((T + 16 * mt - 1) / (16 * mt)));
 #define PLE_W4_LAUNCH(MT, NT, G, WAVES)       \
     if (mt == MT && nt == NT && w.group == G) \
