@@ -53,7 +53,8 @@ def _new(shape, dtype, device, stream=None):
 def _fits(t, dtype, shape, device: int) -> bool:
     """A contiguous tensor of this type, shape and device: what most calls pass.  Anything else goes through the
     checks that name the fault."""
-    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous())
 
 
 class W4Weight:
@@ -105,7 +106,7 @@ def ple_w4_linear(x, w: W4Weight, *, out=None, stream=None):
         _req("out", out, (T, w.out_dim), _BF16)
         _same_device(x, w.codes, out)
     rc = capi.load().ple_w4_linear(x.data_ptr(), x.stride(0) if T > 1 else w.k_dim, ctypes.byref(w.desc), T,
-                                   out.data_ptr(), _raw_stream(w.device) if stream is None else _stream(stream))
+                                   _ptr(out), _raw_stream(w.device) if stream is None else _stream(stream))
     if rc:
         capi.check(rc, "ple_w4_linear")
     return out
@@ -157,7 +158,7 @@ def _kv4_batch(cache, query_start_loc, seq_lens, page_table, T, max_request_toke
         _req("seq_lens", seq_lens, (R,), _I32)
         _req("page_table", page_table, (R, None), _I32)
         _same_device(cache.tensors[0], query_start_loc, seq_lens, page_table)
-    return capi.ple_kv4_batch(query_start_loc.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), T, R,
+    return capi.ple_kv4_batch(query_start_loc.data_ptr(), _ptr(seq_lens), page_table.data_ptr(), T, R,
                               page_table.shape[1], max_request_tokens, max_seq_len)
 
 
@@ -181,7 +182,7 @@ def ple_kv4_append(cache: KV4Cache, k, v, query_start_loc, seq_lens, page_table,
     if q is not None:
         qs, hq = _heads("q", q, T, None, cache), q.shape[1]
         q_out = _out("q_out", q_out, (T, hq, D), _BF16, cache, stream)
-        q_at, out_at = q.data_ptr(), q_out.data_ptr()
+        q_at, out_at = q.data_ptr(), _ptr(q_out)
     elif q_out is not None:
         raise ValueError("q_out given without q")
     if inv_freq is not None:
@@ -209,7 +210,7 @@ def ple_kv4_read(cache: KV4Cache, query_start_loc, seq_lens, page_table, num_tok
     k_out = _out("k_out", k_out, shape, _BF16, cache, stream)
     v_out = _out("v_out", v_out, shape, _BF16, cache, stream)
     b = _kv4_batch(cache, query_start_loc, seq_lens, page_table, T)
-    rc = capi.load().ple_kv4_read(ctypes.byref(cache.desc), ctypes.byref(b), k_out.data_ptr(), v_out.data_ptr(),
+    rc = capi.load().ple_kv4_read(ctypes.byref(cache.desc), ctypes.byref(b), _ptr(k_out), _ptr(v_out),
                                   _raw_stream(cache.device) if stream is None else _stream(stream))
     if rc:
         capi.check(rc, "ple_kv4_read")
@@ -263,7 +264,7 @@ def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table,
         _same_device(cache.tensors[0], workspace)
     rc = lib.ple_kv4_attention(
         q.data_ptr(), qs, hq, ctypes.byref(cache.desc), ctypes.byref(b), window,
-        D ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse),
         None if workspace is None else _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
         _raw_stream(cache.device) if stream is None else _stream(stream))
     if rc:
