@@ -21,6 +21,7 @@ from . import capi
 from . import _BF16, _BYTES, _F32, _I32, _nbytes, _ptr, _req, _req_bytes, _same_device, _stream
 
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
+_MOST = 2 ** 31 - 1  # ctypes would pass the low 32 bits of a larger window or hint; all of them mean "no limit"
 _BF, _INT = torch.bfloat16, torch.int32
 
 
@@ -159,7 +160,7 @@ def _kv4_batch(cache, query_start_loc, seq_lens, page_table, T, max_request_toke
         _req("page_table", page_table, (R, None), _I32)
         _same_device(cache.tensors[0], query_start_loc, seq_lens, page_table)
     return capi.ple_kv4_batch(query_start_loc.data_ptr(), _ptr(seq_lens), page_table.data_ptr(), T, R,
-                              page_table.shape[1], max_request_tokens, max_seq_len)
+                              page_table.shape[1], min(max_request_tokens, _MOST), min(max_seq_len, _MOST))
 
 
 def _out(name, t, shape, dtypes, cache, stream):
@@ -223,9 +224,9 @@ def ple_kv4_attention_workspace_bytes(cache: KV4Cache, num_q_heads: int, num_tok
     """Workspace of a call with these sizes and hints (0: none is needed)."""
     any_ptr = cache.desc.k_codes  # sizes alone matter here
     b = capi.ple_kv4_batch(any_ptr, any_ptr, any_ptr, int(num_tokens), int(num_reqs), int(table_width),
-                           int(max_request_tokens), int(max_seq_len))
+                           min(int(max_request_tokens), _MOST), min(int(max_seq_len), _MOST))
     return int(capi.load().ple_kv4_attention_workspace_bytes(int(num_q_heads), ctypes.byref(cache.desc),
-                                                             ctypes.byref(b), int(window)))
+                                                             ctypes.byref(b), min(int(window), _MOST)))
 
 
 def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table, *, window: int = 0, scale=None,
@@ -235,7 +236,7 @@ def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table,
     scale: 1/sqrt(D) if None.  window: tokens seen, the own one included (0: all).  max_request_tokens and
     max_seq_len (0: unknown) let the call size its launch; pass them.  Returns (out bf16 [T][q heads][D], lse fp32
     [T][q heads] or None)."""
-    D, T = cache.head_dim, q.shape[0]
+    D, T, window = cache.head_dim, q.shape[0], min(window, _MOST)
     qs, hq = _heads("q", q, T, None, cache), q.shape[1]
     out = _out("out", out, (T, hq, D), _BF16, cache, stream)
     if lse is not None or want_lse:

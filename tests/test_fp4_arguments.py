@@ -1,4 +1,5 @@
-"""What the binding of the 4-bit operators hands to the library: raw addresses as the other calls take them.  On the CPU, with a library that notes its arguments."""
+"""What the binding of the 4-bit operators hands to the library: raw addresses as the other calls take them, and numbers
+beyond 32 bits.  On the CPU, with a library that notes its arguments."""
 import pytest
 import torch
 
@@ -6,6 +7,7 @@ import layer_embedding_lookup_amd as ple
 from layer_embedding_lookup_amd import capi, fp4
 
 BF, I32 = torch.bfloat16, torch.int32
+MOST = 2 ** 31 - 1
 
 
 class Weight:
@@ -51,3 +53,17 @@ def test_raw_addresses(calls, cache):
     assert ple.ple_kv4_attention(Q, cache, *lens, out=4096, lse=8192, workspace=64, stream=9) == (4096, 8192)
     args = calls["ple_kv4_attention"]
     assert args[7:10] == [4096, 8192, 64] and args[4].seq_lens == 777 * 16
+
+
+def test_numbers_beyond_32_bits(calls, cache):
+    """A window, or a hint, wider than an int32 is the widest one, not what its low 32 bits say."""
+    for big in (MOST, MOST + 1, 2 ** 32 + 5, 2 ** 63 - 1):
+        ple.ple_kv4_attention(Q, cache, *ARGS, window=big, max_request_tokens=big, max_seq_len=big, out=Q, stream=9)
+        args = calls["ple_kv4_attention"]
+        assert args[5] == MOST and args[4].max_request_tokens == MOST and args[4].max_seq_len == MOST
+        cache.desc.k_codes = 16
+        ple.ple_kv4_attention_workspace_bytes(cache, 4, 3, 1, 2, window=big, max_request_tokens=big, max_seq_len=big)
+        args = calls["ple_kv4_attention_workspace_bytes"]
+        assert args[3] == MOST and args[2].max_request_tokens == MOST and args[2].max_seq_len == MOST
+    ple.ple_kv4_attention(Q, cache, *ARGS, window=-1, out=Q, stream=9)
+    assert calls["ple_kv4_attention"][5] == -1  # (refused by the library)
