@@ -129,7 +129,7 @@ class KV4Cache:
         _req("v_scale", v_scale, (heads,), _F32)
         _same_device(k_codes, k_scales, v_codes, v_scales, k_scale, v_scale)
         self.tensors = (k_codes, k_scales, v_codes, v_scales, k_scale, v_scale)
-        self.device, self._workspaces = k_codes.get_device(), {}
+        self.device = k_codes.get_device()
         self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = pages, heads, size, 2 * half
         self.desc = capi.ple_kv4_cache(*(t.data_ptr() for t in self.tensors), pages, heads, size, 2 * half, 0)
 
@@ -245,14 +245,7 @@ def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table,
     if q.get_device() != cache.device:
         _same_device(cache.tensors[0], q)
     lib = capi.load()
-    # the workspace's size follows from these numbers alone
-    sizes = (T, b.num_reqs, b.table_width, hq, window, max_request_tokens, max_seq_len)
-    need = cache._workspaces.get(sizes)
-    if need is None:
-        if len(cache._workspaces) >= 4096:
-            cache._workspaces.clear()
-        need = int(lib.ple_kv4_attention_workspace_bytes(hq, ctypes.byref(cache.desc), ctypes.byref(b), window))
-        cache._workspaces[sizes] = need
+    need = int(lib.ple_kv4_attention_workspace_bytes(hq, ctypes.byref(cache.desc), ctypes.byref(b), window))
     if workspace is None:
         if need > 0:  # (given up on return, before the work has ended: taken in the order of the stream it runs on)
             if stream is None:

@@ -67,3 +67,13 @@ def test_numbers_beyond_32_bits(calls, cache):
         assert args[3] == MOST and args[2].max_request_tokens == MOST and args[2].max_seq_len == MOST
     ple.ple_kv4_attention(Q, cache, *ARGS, window=-1, out=Q, stream=9)
     assert calls["ple_kv4_attention"][5] == -1  # (refused by the library)
+
+
+def test_a_growing_sequence_leaves_nothing_behind(calls, cache):
+    """A decode loop that passes its longest length as it grows: the cache object holds no more after it than before."""
+    def held():
+        return {name: len(v) for name, v in vars(cache).items() if hasattr(v, "__len__")}
+    before = held()
+    for n in range(1, 100):
+        ple.ple_kv4_attention(Q, cache, *ARGS, max_request_tokens=3, max_seq_len=n, stream=9, out=Q)
+    assert held() == before
