@@ -9,8 +9,9 @@
 // join their maxima with one exchange.  The rotation itself is 64-bit too and
 // rounded once to fp32, so that a key next to a code's border falls on the
 // side that the definition says.  7984 tokens of 32 + 8 + 8 heads of 128: 35 us
-// (173 MB, 4.9 TB/s; with the codes found by comparisons 41.6) and 12.5 us to read them back (43 MB); 256 tokens: 7.4 and
-// 3.7 us, where finding the request and its angles is the time.
+// (173 MB, 4.9 TB/s; with the codes found by comparisons 41.6) and 13 us to read them back (43 MB); 256 tokens: 7.3 and
+// 3.8 us, of which a launch is about 3 and the rest the chain of loads that finds the request (a binary search, then its
+// length and its table entry) and, for append, the angles.
 #include "ple_fp4_launch.h"
 
 namespace ple {
@@ -63,7 +64,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArg
     int r;
     const int pos = kv4_position(a.cache, a.batch, t, r);
     for (int i = threadIdx.x; i < half; i += kAppendThreads) {
-        // a position below 2^30 times a 24-bit frequency is exact in 64 bits
+        // (a position of 30 bits times a 24-bit frequency: rounded at most in its 54th bit, 2^-53 of the angle)
         const double angle = (double)(pos < 0 ? 0 : pos) * (double)a.inv_freq[i];
         double sn, cs;
         sincos(angle, &sn, &cs);

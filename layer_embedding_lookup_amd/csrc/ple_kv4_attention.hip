@@ -33,9 +33,9 @@
 // at most.  The next tile is loaded while this one's weights and value
 // product are formed, its page-table entry a tile before that.  Bound by
 // reading the cache where there is much of it (256 requests of up to 6000
-// tokens, 914 MB: 191 us, 4.8 TB/s; one of 131k tokens, 151 MB: 29 us and 5
-// for the join, 38.7 with the launches), else by the chain of dependent loads
-// (one of 777 tokens: 10 us; 64 windows of 1..4 drafts over 1024 tokens: 17).
+// tokens, 914 MB: 194 us, 4.7 TB/s; one of 131k tokens, 151 MB: 29 us and 5
+// for the join, 38.8 with the launches), else by the chain of dependent loads
+// (one of 777 tokens: 10.5 us; 64 windows of 1..4 drafts over 1024 tokens: 17).
 #include "ple_fp4_launch.h"
 
 namespace ple {
@@ -47,7 +47,10 @@ constexpr int kMostSplits = 1024;
 constexpr int kFewSplits = 8;  // up to which one wave joins a row
 // Weights are 2^(s - m + kWeightShift) with m a row's largest exponent but for kSlack: m only moves on, and the row's
 // sums are only rescaled, when the maximum has passed it by more than that.  Weights stay below 2^15 and fp16 keeps
-// them above 2^-24, so tokens down to 2^-32 of the heaviest one count.
+// them above 2^-24, so tokens down to 2^-32 of the heaviest one count.  The products take them in fp16 so that they run
+// on the matrix cores beside values that fp16 holds exactly; the sums take them unrounded, which keeps the log-sum-exp
+// at fp32.  That costs 1.6e-4 of an output (rms over 777 random keys; summing the rounded weights instead: the same),
+// a tenth of the 1.65e-3 of its rounding to bf16: 0.00166 against 64 bits with it and 0.00165 without.
 constexpr float kWeightShift = 8.0f, kSlack = 7.0f;
 
 // What a block's query tile sees: rows [row0, row1) of request r, cache tokens [lo, hi).
@@ -606,13 +609,20 @@ PLE_ATTN_SHAPES(PLE_ATTN_KERNEL)
 // dequantised once for 128 rows.  Two tiles in LDS: the next one is filled
 // while this one is used, with one barrier a tile.  Two blocks per CU cover
 // each other's softmax (D = 256: one).  1289 + 1455 tokens at 5403 and 2004,
-// 32 heads of 128: 230 us, 0.57 PFLOP/s, 25 of them the join of cut tiles.  A
-// wave takes 6300..7000 cycles for a tile of which its products are 1024,
-// softmax about 900, dequantising about 400; without waiting for memory, or
-// with these hand-interleaved, it takes as long, so what is left is the two
-// waves of a SIMD in the same phase.
+// 32 heads of 128: 231 us, 0.57 PFLOP/s, 25 of them the join of cut tiles.  A
+// CU's eight waves take about 7300 cycles for a tile each.  In those a SIMD's
+// products are 2048 and its other vector instructions (softmax, dequantising)
+// about 3300; LDS is busy for 1750, almost without bank conflicts.  Without
+// waiting for memory, or with these hand-interleaved, it takes as long, so
+// what is left is the two waves of a SIMD in the same phase.
 // ---------------------------------------------------------------------------
 constexpr int kChunkRows = 128;
+// Measured with 32 heads of 128 over 8 where nothing else is said, and where a value other than these does better too:
+//  kFlatLeast: 1289 + 1455 tokens at 5403 and 2004 232 us with 4, 8 and 16, 237 with 2; 100 behind 2000 43 (with 4 44, 2 54,
+//              16 58); 1000 behind nothing 54 (4 53, 16 70); but 100 behind nothing 30 (4 21), 50 behind 500 38 (4 30).
+//  kFlatStart: the first 232 us (with 0 278, 2 252, 8 242), the second 44.5 (51, 46, 43.7), the third 54 (86, 60, 56).
+//  kFlatUnits: 736 query tiles 233 us in shares, 401 a block each; 4864 of 32 requests 330 and 275, which the rule keeps
+//              apart; between them it takes the slower one (1920 tiles of 16 requests 165 and 155, 2560 of 32 162 and 146).
 constexpr int kFlatLeast = 8;        // places of a share at least
 constexpr int kFlatStart = 4;        // places that beginning a query tile counts for (queries in, results out)
 constexpr int kFlatUnits = 4096;     // query tiles (of all heads and requests) up to which the work is cut into shares
@@ -1030,8 +1040,9 @@ __device__ __forceinline__ void attn_join_store(const Kv4AttentionArgs& a, int64
 }
 
 // Joins the splits of a row: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top).  Few splits: a wave a row
-// (WAVES = 1), four rows a block; many: four waves a row, each with a quarter of the splits, joined through LDS (29
-// splits: 1 us less than a wave a row).
+// (WAVES = 1), four rows a block; many: four waves a row, each with a quarter of the splits, joined through LDS (30
+// splits 18.0 us as a whole against 18.8, 29 of a longer cache 1 us less; 4 splits 16.0 against 15.5, between 7 and 16
+// splits no difference beyond the spread).
 template <int D, int WAVES>
 __device__ __forceinline__ void attn_join_body(const Kv4AttentionArgs& a) {
     constexpr int E = D / 64;  // elements of a lane
@@ -1184,8 +1195,12 @@ void plan_kv4_attention(Kv4AttentionArgs& a) {
         len = len < span ? len : span;
     }
     // Splits where the query tiles alone leave CUs idle, each of at least 1024 tokens, below which a block's fixed cost
-    // and the joining kernel outweigh what a shorter loop saves.  Up to one block per CU: blocks of eight waves (verify
-    // windows 64 x 4 17.2 us, of four in twice the splits 23.8; one of 131k tokens 34.6 against 38.5).
+    // and the joining kernel outweigh what a shorter loop saves (8 requests of up to 2500 tokens 15.6 us, with 512 16.2,
+    // 256 20.1, 2048 17.5; 4 of 20000 18.2, 18.3, 21.9 and 20.2).  Up to one block per CU: blocks of eight waves (verify
+    // windows 64 x 4 17.2 us, of four in twice the splits 23.8; one of 131k tokens 34.6 against 38.5; 256 blocks over 2000
+    // tokens 17.5 against 21.8; 264 blocks 21.2 against 21.1, 768 over 500 23.7 against 14.7, but 264 over 8000 44 against
+    // 54).  Blocks of four waves in as many splits as two or three of them per CU (384 blocks over 4000 tokens 37.8 us
+    // with 768 slots, 41.1 with 512, 39.5 with 1024; over 8000 1024 would be better, 320 blocks 49.9 against 57.6).
     const int64_t blocks = R * a.cache.num_kv_heads * a.tiles;
     // (the line's length has to fit 32 bits whatever the hints say)
     if (a.rows == kChunkRows && R <= kWave && blocks > 0 && blocks <= kFlatUnits &&

@@ -1,10 +1,13 @@
 // Products with 4-bit weights: out = x W^T, W dequantised on the way to the
 // matrix cores and never written out.
 //
-// Few tokens (decode): bound by reading W once, then by a launch's own time
-// (about 5 us; one token, 4096 -> 8192 NVFP4, 18.9 MB: 6.5 us, 2.9 TB/s; 64
-// tokens 13.4).  A wave takes NT x 16 output features and a share of K in
-// steps of 128.  Inputs and codes come in whole rows straight into LDS, 1 KiB
+// Few tokens (decode): bound by the latency of its rounds of loads.  A round
+// is a step of 128 inputs of each of the block's eight waves, loaded, waited
+// for and used; launch and join take about 3 us, a round 0.7..0.9 (one token,
+// 8192 features NVFP4, kernel alone: K = 512 3.5 us, 1024 4.0, 2048 4.8, 4096
+// 6.5 (18.9 MB, 2.9 TB/s), 8192 12.1; back to back no call takes less than
+// the host's 5.9; 64 tokens, K = 4096 12.4).  A wave takes NT x 16 output
+// features and a share of K in steps of 128.  Inputs and codes come in whole rows straight into LDS, 1 KiB
 // an instruction: read as MFMA operands from memory (lane n its own row) each
 // lane's 16 bytes are a cache access of their own, and those accesses, 64 an
 // instruction, bound the kernel (64 tokens: 22.6 us).  Four 16x16x32 bf16
@@ -295,9 +298,10 @@ __device__ __forceinline__ void w4_rows_body(const W4Args& a) {
 PLE_W4_SHAPES(PLE_W4_KERNELS)
 
 // ---------------------------------------------------------------------------
-// Many tokens: bound by the products and by dequantising between them (1024
-// tokens 4096 -> 8192 NVFP4: 72..75 us, 0.92..0.95 PFLOP/s; INT4 in groups of
-// 128 94 us, of 32, with four times the scaling of partial sums, 171).  A
+// Many tokens: bound by the products and by dequantising between them (4096
+// -> 8192, 1024 tokens: NVFP4 72..75 us, 0.92..0.95 PFLOP/s; INT4 in groups of
+// 128 92 us, of 32, with four times the scaling of partial sums and tiles of
+// 64 tokens, 164; 8192 tokens: NVFP4 618 us, INT4 in groups of 128 775).  A
 // block of four waves holds MT x 16 tokens x NT x 64 features, a wave all of
 // the tokens and NT x 16 features.  Inputs and codes go through LDS in slices
 // of 128 (two slots), the inputs shared by the waves; each wave dequantises
@@ -522,18 +526,23 @@ static hipError_t launch_gemm(const W4Args& a, hipStream_t s) {
 
 W4Shape w4_linear_shape(int64_t T, int32_t out_dim, int32_t group) {
     // Tiles of the many-token kernel where there are enough of them for the CUs, below that blocks that split K between
-    // their waves (K = 4096: 320 tiles NVFP4 43 us against 47, INT4 in groups of 32 90 against 81; 512 tiles 50 against 67
-    // and 91 against 109).
+    // their waves.  Measured at K = 4096, many-token against few-token kernel: NVFP4 256 tiles 34.1 us against 32.3, 320
+    // 41.0 against 45.8; INT4 320 tiles in groups of 32 81 against 68, of 64 61 against 63, of 128 62 against 59, 384 tiles
+    // 83 against 71, 67 against 64 and 67 against 62; 512 tiles in groups of 32 91 against 109.  K is not looked at: with
+    // K = 8192 the border lies higher (INT4 384 tiles 131..159 against 111..126), with K = 512 lower, where the few-token
+    // blocks need a second round of the CUs (160 tiles NVFP4 7.4 against 12.0, INT4 9 against 12..14).
     const int64_t features = (out_dim + 127) / 128;
     if (T > 64 && (T + 63) / 64 * features > (group == 16 ? 256 : 384)) {
-        // 128 tokens a block where that leaves two blocks per CU (8192 x 4096 NVFP4: T = 1024 70 us against 92, T = 500,
-        // 256 blocks, 57 against 48)
+        // 128 tokens a block where that leaves two blocks per CU (K = 4096: 512 blocks NVFP4 75 us against 93, INT4 in
+        // groups of 128 93 against 124; 256 blocks 55 against 48 and 84 against 66; 1024 blocks 144 against 180 and 181
+        // against 229; just past 512 the last blocks run alone, 576 blocks 119 against 103 and 169 against 145)
         const bool tall = (group == 16 || group == 128) && (T + 127) / 128 * features >= 512;
         return {true, tall ? 8 : 4, 2};
     }
     const int mt = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
-    // Feature tiles of a block of 64 tokens: as few as keep one block per CU (its inputs fill the LDS; 100 tokens
-    // 4096 -> 5003 NVFP4: 22 us in 314 blocks of two, 17 in 158 of four).
+    // Feature tiles of a block of 64 tokens: as few as keep one block per CU (its inputs fill the LDS; K = 4096, NVFP4: 64
+    // tokens -> 4096 11.1 us in 256 blocks of one tile, 11.6 in 128 of two; -> 5120 18.0 in 320 of one, 11.5 in 160 of two;
+    // 100 tokens -> 5003 24 in 626 of one, 20 in 314 of two, 16.3 in 158 of four; at K = 512 the same order).
     const int64_t rows = (T + 63) / 64;
     const int nt = mt < 4 || rows * ((out_dim + 15) / 16) <= 256 ? 1 : (rows * ((out_dim + 31) / 32) <= 256 ? 2 : 4);
     return {false, mt, nt};
