@@ -117,3 +117,36 @@ def test_leaves_alone_what_the_current_stream_still_reads(what, handle):
     torch.cuda.synchronize()
     assert all((x == 7).all() for x in copies)
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_a_call_on_a_forked_stream_in_a_graph():
+    """Captured on a stream that forks off the capturing one, workspace and outputs made by the calls; every replay
+    against the eager result, with eager work of the same size between them."""
+    g = torch.Generator().manual_seed(32)
+    cache = U.Cache(g, [2500, 900], H=1, D=128, page=16)
+    c = ple.KV4Cache(*cache.tensors(DEV))
+    args = (torch.tensor([0, 1, 2], dtype=I32, device=DEV), torch.tensor([2500, 900], dtype=I32, device=DEV), cache.table.to(DEV))
+    kw = dict(max_request_tokens=1, max_seq_len=2500, want_lse=True)
+    q = torch.randn((2, 8, 128), generator=g).to(BF).to(DEV)
+    w = ple.W4Weight.nvfp4(torch.randint(0, 256, (192, 512), generator=g).to(torch.uint8).to(DEV),
+                           torch.randint(0, 0x60, (192, 64), generator=g).to(torch.uint8).to(DEV), torch.ones(1, device=DEV))
+
+    def calls(stream):
+        out, lse = ple.ple_kv4_attention(q, c, *args, stream=stream, **kw)
+        return out, lse, ple.ple_w4_linear(out.view(2, 1024), w, stream=stream)
+
+    calls(None)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = calls(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for i in range(4):
+        q.normal_(generator=torch.Generator(device=DEV).manual_seed(i))
+        want = calls(None)
+        graph.replay()
+        calls(None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
