@@ -10,9 +10,10 @@ include/ple_8bit.h:
 
   inputs   codes int8 [T][K], one fp32 scale per token
   weights  codes int8 [O][K], one fp32 scale per output channel
-  cache    e4m3fn codes uint8, keys [pages][heads][page_size][D], values
-           [pages][heads][page_size/16][D][16 tokens], and for each one fp32
-           scale per block of 16 tokens and head [pages][heads][page_size/16]
+  cache    e4m3fn codes uint8, keys [pages][heads][page_size/16][D/16]
+           [16 tokens][16], values [pages][heads][page_size/16][D][16 tokens],
+           and for each one fp32 scale per block of 16 tokens and head
+           [pages][heads][page_size/16]
 """
 import math
 import random
@@ -44,7 +45,7 @@ def listed():
         # a prefill of 8k tokens through the key/value projection: bound by the products
         dict(name="linear_8k", kind="linear", T=8192, K=4096, O=8192),
         # a decode step's new keys and values, one token of each of 256 requests, far positions, query rotated too
-        dict(name="append_decode_256", kind="append", R=256, new=1, past=120000, Hq=32, Hkv=8, D=128, page=16, rot=128,
+        dict(name="append_decode_256", kind="append", R=256, new=1, past=60000, Hq=32, Hkv=8, D=128, page=16, rot=128,
              interleaved=False),
         # a prefill's keys and values, ragged prompts behind cached ones, half of each head rotated, neighbouring pairs
         dict(name="append_prefill_8k", kind="append", R=5, new=1638, past=300, Hq=32, Hkv=8, D=128, page=64, rot=64,
@@ -106,6 +107,22 @@ def _e4m3(x):
 
 def _value(codes, dtype=torch.float32):
     return codes.view(torch.float8_e4m3fn).to(torch.float32).to(dtype)
+
+
+def _laid_out(codes, name):
+    """Blocks of codes [...][16 tokens][D] as the cache holds them."""
+    return codes.unflatten(-1, (-1, 16)).transpose(-3, -2) if name == "k" else codes.transpose(-1, -2)
+
+
+def _in_order(held, name):
+    """And back."""
+    return held.transpose(-3, -2).flatten(-2) if name == "k" else held.transpose(-1, -2)
+
+
+def _tokens(s, name, page, place):
+    """The codes of tokens at these places of these pages, [...][heads][D]."""
+    codes = s[name + "_codes"][page, :, place // BLOCK, :, place % BLOCK]
+    return codes.flatten(-2) if name == "k" else codes
 
 
 # ---- states ----
@@ -171,8 +188,8 @@ def _prepare_cache(c, g):
     s = dict(case=c, T=T, most_new=int(new.max()), most_seq=int(seq.max()), qsl=qsl.to(DEV), seq=seq.to(DEV), table=table,
              unused=where[-1].long())
     for name in ("k", "v"):
-        s[name + "_codes"] = torch.empty((pages, Hkv, page, D) if name == "k" else (pages, Hkv, page // BLOCK, D, BLOCK),
-                                         dtype=torch.uint8, device=DEV)
+        shape = (D // 16, BLOCK, 16) if name == "k" else (D, BLOCK)
+        s[name + "_codes"] = torch.empty((pages, Hkv, page // BLOCK, *shape), dtype=torch.uint8, device=DEV)
         s[name + "_scales"] = torch.empty((pages, Hkv, page // BLOCK), device=DEV)
         step = max(1, (1 << 26) // (Hkv * page * D))
         for p in range(0, pages, step):
@@ -181,15 +198,15 @@ def _prepare_cache(c, g):
             x = _randn((n, Hkv, page // BLOCK, BLOCK, D), g) * torch.exp(0.5 * _randn((n, Hkv, page // BLOCK, BLOCK, 1), g))
             scale = _block_scale(x.abs().amax((-2, -1)))
             codes = _e4m3(x / scale[..., None, None])
-            s[name + "_codes"][p:p + n] = codes.flatten(2, 3) if name == "k" else codes.transpose(-1, -2)
+            s[name + "_codes"][p:p + n] = _laid_out(codes, name)
             s[name + "_scales"][p:p + n] = scale
     # what no token has been written to yet holds anything, codes that are no number and such scales among it
     filled = s["seq"] - (new.to(DEV) if c["kind"] == "append" else 0)
     t = torch.arange(width * page, device=DEV)
     r, j = torch.nonzero((t[None, :] >= filled[:, None]) & (t[None, :] < need.to(DEV)[:, None] * page), as_tuple=True)
     at, i = table[r, j // page].long(), j % page
-    s["k_codes"][at, :, i] = 0x7F
-    s["v_codes"][at, :, i // BLOCK, :, i % BLOCK] = 0x7F
+    for name in ("k", "v"):
+        s[name + "_codes"][at, :, i // BLOCK, :, i % BLOCK] = 0x7F
     first = i % BLOCK == 0
     for name in ("k", "v"):
         s[name + "_scales"][at[first], :, i[first] // BLOCK] = torch.nan
@@ -315,38 +332,27 @@ def _plain_append(s):
     keep = (torch.arange(BLOCK, device=DEV) < kept[:, None])[:, None, :, None]
     mine = r * most + pos // BLOCK - begin[r] // BLOCK
     page_of, place = s["table"][r, pos // page].long(), pos % page
-    rows = group[:, None] * BLOCK + torch.arange(BLOCK, device=DEV)
     for name, x in (("k", k), ("v", v.float())):
         codes, scales = s[name + "_codes"], s[name + "_scales"]
         top = torch.zeros((R * most, H), device=DEV).scatter_reduce_(0, mine[:, None].expand(-1, H), x.abs().amax(-1), "amax")
         old = torch.where(kept[:, None] > 0, scales[at, :, group], 0.0)
         scale = torch.maximum(_block_scale(top), old)
         by = (old / scale)[:, :, None, None]
-        if name == "k":
-            held = codes[at[:, None], :, rows].transpose(1, 2)                # [blocks][H][16][D]
-            codes[at[:, None], :, rows] = torch.where(keep, _e4m3(_value(held) * by), held).transpose(1, 2)
-        else:
-            held = codes[at, :, group].transpose(-1, -2)
-            codes[at, :, group] = torch.where(keep, _e4m3(_value(held) * by), held).transpose(-1, -2)
+        held = _in_order(codes[at, :, group], name)                           # [blocks][H][16][D]
+        codes[at, :, group] = _laid_out(torch.where(keep, _e4m3(_value(held) * by), held), name)
         scales[at, :, group] = scale
         new = _e4m3(x / scale[mine][..., None])
-        if name == "k":
-            codes[page_of, :, place] = new
-        else:
-            codes[page_of, :, place // BLOCK, :, place % BLOCK] = new
+        codes[page_of, :, place // BLOCK, :, place % BLOCK] = new.unflatten(-1, (-1, 16)) if name == "k" else new
     r, pos = _places(s, s["back_qsl"], s["back_T"])
     page_of, place = s["table"][r, pos // page].long(), pos % page
-    k = _value(s["k_codes"][page_of, :, place]) * s["k_scales"][page_of, :, place // BLOCK][..., None]
-    v = _value(s["v_codes"][page_of, :, place // BLOCK, :, place % BLOCK]) * s["v_scales"][page_of, :, place // BLOCK][..., None]
+    k, v = (_value(_tokens(s, n, page_of, place)) * s[n + "_scales"][page_of, :, place // BLOCK][..., None] for n in ("k", "v"))
     return q, k.bfloat16(), v.bfloat16()
 
 
 def _rows(s, name):
     """Keys or values of every request in order, [R][Hkv][width * page][D], and whether a token stands there, [R][width * page]."""
     table = s["table"].long()
-    x = _value(s[name + "_codes"][table])
-    if name == "v":
-        x = x.transpose(-1, -2).flatten(3, 4)                                    # [R][width][Hkv][page][D]
+    x = _value(_in_order(s[name + "_codes"][table], name)).flatten(3, 4)          # [R][width][Hkv][page][D]
     x = x * s[name + "_scales"][table].repeat_interleave(BLOCK, -1)[..., None]
     x = x.transpose(1, 2).flatten(2, 3)
     live = torch.arange(x.shape[2], device=DEV)[None, :] < s["seq"][:, None]
@@ -455,7 +461,7 @@ def _exact_append(s):
             if kept:
                 p, g = int(s["table"][i, lo // page]), lo % page // BLOCK
                 old = s[name + "_scales"][p, :, g].double()
-                codes = s["k_codes"][p, :, g * BLOCK:g * BLOCK + kept] if name == "k" else \
+                codes = s["k_codes"][p, :, g, :, :kept].transpose(1, 2).flatten(2) if name == "k" else \
                     s["v_codes"][p, :, g, :, :kept].transpose(1, 2)
                 scale[0] = torch.maximum(scale[0], old)
                 rows[:kept] = (_code_value(codes) * old[:, None, None]).transpose(0, 1)
@@ -473,7 +479,7 @@ def _exact_attention(s):
         a, b, n = int(s["qsl"][r]), int(s["qsl"][r + 1]), int(s["seq"][r])
         at = s["table"][r, torch.arange(n, device=DEV) // page].long()
         i = torch.arange(n, device=DEV) % page
-        k = _code_value(s["k_codes"][at, :, i]) * s["k_scales"][at, :, i // BLOCK].double()[..., None]
+        k = _code_value(s["k_codes"][at, :, i // BLOCK, :, i % BLOCK].flatten(2)) * s["k_scales"][at, :, i // BLOCK].double()[..., None]
         v = _code_value(s["v_codes"][at, :, i // BLOCK, :, i % BLOCK]) * s["v_scales"][at, :, i // BLOCK].double()[..., None]
         k, v = (x.transpose(0, 1).contiguous() for x in (k, v))
         q = s["q"][a:b].double().view(b - a, Hkv, G, D).permute(1, 2, 0, 3).reshape(Hkv, G * (b - a), D)
