@@ -36,7 +36,9 @@ __all__ = ["HashParams", "Table", "Layer", "ple_ngram_ids", "ple_gather", "ple_l
            "ple_host_alloc", "ple_host_free", "HostBuffer", "ple_stream_create_cu_masked", "ple_stream_destroy",
            "ple_error_message", "ple_version", "library",
            "W4Weight", "KV4Cache", "ple_w4_linear", "ple_kv4_append", "ple_kv4_read", "ple_kv4_attention",
-           "ple_kv4_attention_workspace_bytes"]
+           "ple_kv4_attention_workspace_bytes",
+           "W8Weight", "KV8Cache", "ple_rms_norm8", "ple_w8_linear", "ple_kv8_append", "ple_kv8_read", "ple_kv8_attention",
+           "ple_kv8_attention_workspace_bytes"]
 
 
 def library() -> ctypes.CDLL:
@@ -625,3 +627,5 @@ def ple_version() -> str:
 
 from .fp4 import (KV4Cache, W4Weight, ple_kv4_append, ple_kv4_attention, ple_kv4_attention_workspace_bytes,  # noqa: E402
                   ple_kv4_read, ple_w4_linear)
+from .bits8 import (KV8Cache, W8Weight, ple_kv8_append, ple_kv8_attention, ple_kv8_attention_workspace_bytes,  # noqa: E402
+                    ple_kv8_read, ple_rms_norm8, ple_w8_linear)

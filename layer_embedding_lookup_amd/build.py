@@ -22,7 +22,8 @@ BENCH_LIB = os.path.join(HERE, "libple_bench.so")
 BENCH_SOURCE = "ple_bench.hip"
 SOURCES = ["ple_api.cpp", "ple_lookup.hip", "ple_kv_proj.hip", "ple_gate_conv.hip", "ple_dedup.hip", "ple_dp.hip",
            "ple_spec.hip", "ple_static.hip", "ple_fp4_api.cpp", "ple_kv4_append.hip", "ple_kv4_attention.hip",
-           "ple_w4_linear.hip"]
+           "ple_w4_linear.hip", "ple_8bit_api.cpp", "ple_rms_norm8.hip", "ple_w8_linear.hip", "ple_kv8_append.hip",
+           "ple_kv8_attention.hip"]
 ARCH = "gfx950"
 
 
@@ -44,7 +45,7 @@ def common_flags() -> list[str]:
 def build(force: bool = True, verbose: bool = False, jobs: int = 4) -> str:
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     deps = srcs + [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith(".h")] + \
-        [os.path.join(INCLUDE, "ple.h"), os.path.join(INCLUDE, "ple_fp4.h")]
+        [os.path.join(INCLUDE, h) for h in ("ple.h", "ple_fp4.h", "ple_8bit.h")]
     deps.append(os.path.join(CSRC, BENCH_SOURCE))
     if not force and all(os.path.exists(lb) and os.path.getmtime(lb) >= max(os.path.getmtime(d) for d in deps)
                          for lb in (LIB, BENCH_LIB)):

@@ -1,4 +1,4 @@
-"""ctypes view of libple's C ABI (include/ple.h, include/ple_fp4.h): structures, prototypes, loader.
+"""ctypes view of libple's C ABI (include/ple.h, include/ple_fp4.h, include/ple_8bit.h): structures, prototypes, loader.
 
 Argument marshalling only; every step of the path runs in libple's kernels.
 Loading fails loudly when libple.so has not been built.
@@ -15,6 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libple.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "ple.h")
 FP4_HEADER = os.path.join(os.path.dirname(HERE), "include", "ple_fp4.h")
+BITS8_HEADER = os.path.join(os.path.dirname(HERE), "include", "ple_8bit.h")
 
 PLE_OK = 0
 PLE_ERR_INVALID_ARGUMENT = 1
@@ -73,6 +74,15 @@ class ple_kv4_batch(ctypes.Structure):
                 ("table_width", I32), ("max_request_tokens", I32), ("max_seq_len", I32)]
 
 
+class ple_w8_weight(ctypes.Structure):
+    _fields_ = [("codes", P), ("scales", P), ("out_dim", I32), ("k_dim", I32)]
+
+
+class ple_kv8_cache(ctypes.Structure):
+    _fields_ = [("k_codes", P), ("k_scales", P), ("v_codes", P), ("v_scales", P), ("num_pages", I64),
+                ("num_kv_heads", I32), ("page_size", I32), ("head_dim", I32), ("reserved", I32)]
+
+
 _PROTOS = {
     "ple_ngram_ids": (ctypes.c_int, [ctypes.POINTER(ple_hash_desc), ctypes.POINTER(ple_batch_desc), P, P]),
     "ple_gather": (ctypes.c_int, [ctypes.POINTER(ple_table_desc), P, I64, I32, P, P]),
@@ -116,6 +126,17 @@ _FP4_PROTOS = {
     "ple_kv4_attention_workspace_bytes": (ctypes.c_size_t, [I32, _CACHE, _BATCH, I32]),
 }
 
+_CACHE8 = ctypes.POINTER(ple_kv8_cache)
+_BITS8_PROTOS = {
+    "ple_rms_norm8": (ctypes.c_int, [P, I64, P, P, I64, I32, ctypes.c_float, P, P, P, P]),
+    "ple_w8_linear": (ctypes.c_int, [P, I64, P, ctypes.POINTER(ple_w8_weight), I64, P, P]),
+    "ple_kv8_append": (ctypes.c_int, [_CACHE8, _BATCH, P, I64, P, I64, P, I64, I32, P, P, I32, I32, P]),
+    "ple_kv8_read": (ctypes.c_int, [_CACHE8, _BATCH, P, P, P]),
+    "ple_kv8_attention": (ctypes.c_int, [P, I64, I32, _CACHE8, _BATCH, I32, ctypes.c_float, P, P, P, ctypes.c_size_t,
+                                         P]),
+    "ple_kv8_attention_workspace_bytes": (ctypes.c_size_t, [I32, _CACHE8, _BATCH, I32]),
+}
+
 _lib = None
 
 
@@ -127,7 +148,7 @@ def load() -> ctypes.CDLL:
             raise RuntimeError(f"libple.so is not built ({LIB_PATH}); run "
                                "`python -m layer_embedding_lookup_amd.build` (needs hipcc)")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in (*_PROTOS.items(), *_FP4_PROTOS.items()):
+        for name, (res, args) in (*_PROTOS.items(), *_FP4_PROTOS.items(), *_BITS8_PROTOS.items()):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args

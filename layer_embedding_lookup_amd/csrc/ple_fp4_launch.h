@@ -36,8 +36,10 @@ hipError_t launch_kv4_append(const Kv4AppendArgs& a, hipStream_t s);
 hipError_t launch_kv4_read(const ple_kv4_cache& cache, const ple_kv4_batch& batch, uint16_t* k_out, uint16_t* v_out,
                            hipStream_t s);
 
-struct Kv4AttentionArgs {
-    ple_kv4_cache cache;
+// The arguments of attention over a paged cache (ple_kv4_cache, or another with the same sizes in it).
+template <class Cache>
+struct PagedAttentionArgs {
+    Cache cache;
     ple_kv4_batch batch;
     const uint16_t* q;
     int64_t q_stride;
@@ -55,6 +57,8 @@ struct Kv4AttentionArgs {
     int32_t chunk;    // tokens of the cache per split
     int32_t splits;   // most splits of any query tile (grid)
 };
+typedef PagedAttentionArgs<ple_kv4_cache> Kv4AttentionArgs;
+__device__ __forceinline__ float value_scale(const Kv4AttentionArgs& a, int head) { return a.cache.v_scale[head]; }
 // The plan part of the arguments (rows, waves, tiles, flat, chunk, splits), from sizes and hints alone.
 void plan_kv4_attention(Kv4AttentionArgs& a);
 size_t kv4_attention_part_bytes(const Kv4AttentionArgs& a);
@@ -65,7 +69,8 @@ hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, hipStream_t s);
 // One 16-token group of the cache: its number ((page * heads + head) * page_size/16 + group in page), which
 // times 8 D is its byte offset in codes and times D in scales, or -1 where the table names no page.
 // `g` is the token's position / 16 and lies inside the table.
-__host__ __device__ __forceinline__ int kv4_group(const ple_kv4_cache& c, const int32_t* __restrict__ table_row, int head,
+template <class Cache>
+__host__ __device__ __forceinline__ int kv4_group(const Cache& c, const int32_t* __restrict__ table_row, int head,
                                          int g) {
     const int per_page = c.page_size >> 4;
     const int p = g / per_page;
@@ -76,7 +81,8 @@ __host__ __device__ __forceinline__ int kv4_group(const ple_kv4_cache& c, const 
 
 // Request of token t and its position; -1 if the token stands nowhere: in no request's tokens (a padded batch; the last
 // request's places past its length may be another's), before position 0 or past the table.
-__device__ __forceinline__ int kv4_position(const ple_kv4_cache& c, const ple_kv4_batch& b, int64_t t, int& r) {
+template <class Cache>
+__device__ __forceinline__ int kv4_position(const Cache& c, const ple_kv4_batch& b, int64_t t, int& r) {
     r = find_request(b.query_start_loc, b.num_reqs, t);
     const int64_t from = b.query_start_loc[r], to = b.query_start_loc[r + 1];
     const int64_t p = (int64_t)b.seq_lens[r] - (to - t);

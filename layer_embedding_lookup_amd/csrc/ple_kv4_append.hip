@@ -12,7 +12,7 @@
 // (173 MB, 4.9 TB/s; with the codes found by comparisons 41.6) and 13 us to read them back (43 MB); 256 tokens: 7.3 and
 // 3.8 us, of which a launch is about 3 and the rest the chain of loads that finds the request (a binary search, then its
 // length and its table entry) and, for append, the angles.
-#include "ple_fp4_launch.h"
+#include "ple_rotate.h"
 
 namespace ple {
 
@@ -22,15 +22,6 @@ constexpr int kAppendThreads = 256;
 constexpr int64_t kAppendAcross = 1 << 20;
 static dim3 append_grid(int64_t T) {
     return dim3((unsigned)(T < kAppendAcross ? T : kAppendAcross), (unsigned)((T + kAppendAcross - 1) / kAppendAcross));
-}
-
-__device__ __forceinline__ void load8(const uint16_t* __restrict__ p, float (&v)[8]) {
-    const u32x4 w = *(const u32x4*)p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(w[i]);
-        v[2 * i + 1] = bf16_hi(w[i]);
-    }
 }
 
 // e4m3 code of a finite or NaN value already clamped to 448, round to nearest even.
@@ -80,28 +71,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArg
         const int head = at >> shift, d0 = (at & (per_head - 1)) * 8;
         const uint16_t* src = a.src[which] + t * a.stride[which] + head * D;
         float v[8];
-        load8(src + d0, v);
-        if (which != 2 && d0 < a.rot_dim) {
-            if (a.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const double2 w = turn[d0 / 2 + i];
-                    const double x = v[2 * i], y = v[2 * i + 1];
-                    v[2 * i] = (float)(x * w.x - y * w.y);
-                    v[2 * i + 1] = (float)(y * w.x + x * w.y);
-                }
-            } else {
-                const bool upper = d0 >= half;  // half is a multiple of 8
-                float o[8];
-                load8(src + (upper ? d0 - half : d0 + half), o);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const double2 w = turn[(upper ? d0 - half : d0) + i];
-                    const double x = v[i], y = o[i];
-                    v[i] = (float)(upper ? x * w.x + y * w.y : x * w.x - y * w.y);
-                }
-            }
-        }
+        load_rotated(src, d0, which != 2 ? a.rot_dim : 0, a.interleaved, turn, v);
         if (which == 0) {
             u32x4 o;
 #pragma unroll

@@ -1,0 +1,420 @@
+// New keys and values, rotated by position, into the paged 8-bit cache, and
+// back out of it.
+//
+// A block of 16 tokens and a head share one scale, so a wave takes a whole
+// block of one head's keys or values: the largest magnitude of its new tokens
+// gives the scale, a power of two, by which they are coded; where tokens of
+// the request stand in the block before them and its scale grows, their codes
+// are read, taken to the new scale and written back.  Both layouts of the
+// cache are written in 16-byte pieces where a block is filled as a whole.
+// Queries go through blocks of their own, one per token.
+//
+// Requests' blocks are numbered one after the other without a count of them:
+// request r has those from floor(start of r / 16) + 2 r on, which is enough
+// for any position it begins at.
+//
+// Angles are formed in 64 bits (positions of 10^5 and more lose them in 32):
+// two sines and cosines a thread, of its four tokens' first angle and of the
+// angle from one token to the next, then by products (2^-51 of the angle's
+// sine and cosine after three).
+#include "ple_8bit_launch.h"
+#include "ple_rotate.h"
+
+namespace ple {
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendWaves = kAppendThreads / kWave;
+
+// What a unit of the launch writes or reads: new tokens of request r at places [from, to) of a block.
+struct Kv8Unit {
+    int r, group;     // group of head 0 (one head on: page_size / 16 groups on); -1: the table names no page
+    int64_t first;    // the new token at place `from`
+    int block;        // position / 16
+    int from, to;     // (from > 0: earlier tokens of the request stand before it)
+    bool any;
+};
+
+// Blocks that the launch has for requests: with a hint as many as a request can reach, times the requests; or by their
+// starts as above.
+__host__ __device__ __forceinline__ int64_t kv8_units_each(const ple_kv8_batch& b) {
+    return b.max_request_tokens > 0 ? ((int64_t)b.max_request_tokens + 14) / 16 + 1 : 0;
+}
+__host__ __device__ __forceinline__ int64_t kv8_units(const ple_kv8_batch& b, bool hint) {
+    const int64_t by_start = b.num_tokens / 16 + 2 * (int64_t)b.num_reqs;
+    const int64_t each = hint ? kv8_units_each(b) : 0;
+    return each > 0 && each * b.num_reqs < by_start ? each * b.num_reqs : by_start;
+}
+
+__device__ __forceinline__ Kv8Unit kv8_unit(const ple_kv8_cache& c, const ple_kv8_batch& b, int64_t u, bool hint) {
+    Kv8Unit w;
+    const int64_t T = b.num_tokens, each = hint ? kv8_units_each(b) : 0;
+    const auto start = [&](int r) { return min(max((int64_t)b.query_start_loc[r], (int64_t)0), T); };
+    int64_t i;  // of the request's blocks
+    if (each > 0 && each * b.num_reqs == kv8_units(b, hint)) {
+        w.r = (int)(u / each);
+        i = u - w.r * each;
+    } else {
+        int lo = 0, hi = b.num_reqs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (start(mid) / 16 + 2 * (int64_t)mid <= u)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        w.r = lo;
+        i = u - (start(lo) / 16 + 2 * (int64_t)lo);
+    }
+    // (by the whole length and all of the request's tokens, as kv4_position)
+    const int64_t q0 = start(w.r), to = b.query_start_loc[w.r + 1], n = max(min(to, T) - q0, (int64_t)0);
+    const int64_t before = (int64_t)b.seq_lens[w.r] - (to - q0);
+    const int64_t lo = max(before, (int64_t)0), hi = min(before + n, (int64_t)b.table_width * c.page_size);
+    const int64_t block = lo / 16 + i;
+    const int64_t p0 = max(lo, block * 16), p1 = min(hi, block * 16 + 16);
+    w.any = i >= 0 && p0 < p1;
+    w.block = (int)block;
+    w.from = (int)(p0 - block * 16);
+    w.to = (int)(p1 - block * 16);
+    w.first = q0 + (p0 - before);
+    w.group = w.any ? kv4_group(c, b.page_table + (int64_t)w.r * b.table_width, 0, w.block) : -1;
+    return w;
+}
+
+// The least power of two s with top <= 448 s, within the cache's range; top >= 0 and finite.
+__device__ __forceinline__ float block_scale(float top) {
+    const uint32_t u = __float_as_uint(top);
+    int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);  // 448 = 1.75 * 2^8
+    e = min(max(e, -32), 32);
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ float finite_size(float x) { return x - x == 0.f ? fabsf(x) : 0.f; }
+
+// x / s as the cache holds it, before its rounding: at most 448, NaN for what is not finite.
+__device__ __forceinline__ float coded(float x, float inv) {
+    return x - x == 0.f ? __builtin_amdgcn_fmed3f(x * inv, -448.f, 448.f) : __builtin_nanf("");
+}
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+// Four codes at a larger scale (by: old over new).
+__device__ __forceinline__ uint32_t rescaled4(uint32_t w, float by) {
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    return codes4(lo[0] * by, lo[1] * by, hi[0] * by, hi[1] * by);
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, kWave));
+    return x;
+}
+
+// The scale of a block: the one its new tokens need, or the one it has; `by`: what the earlier tokens' codes change by.
+__device__ __forceinline__ float joined_scale(const float* at, bool earlier, float top, float& by) {
+    const float need = block_scale(top), old = earlier ? *at : 0.f;
+    const float s = fmaxf(need, old);
+    by = earlier ? old / s : 1.f;
+    return s;
+}
+
+template <int D>
+__device__ __forceinline__ void append_keys(const Kv8AppendArgs& a, const Kv8Unit& w, int head, const double2 (*turn)[D / 2]) {
+    constexpr int N = D / 64;  // pieces of 16 elements of a token that a lane has
+    const int lane = threadIdx.x & 63, j = lane & 15;
+    const int64_t grp = w.group + (int64_t)head * (a.cache.page_size >> 4);
+    const bool mine = j >= w.from && j < w.to;
+    const uint16_t* src = a.src[1] + (w.first + (j - w.from)) * a.stride[1] + head * D;
+    float x[N][2][8], top = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[i][h][e] = 0.f;
+            if (mine) load_rotated(src, (4 * i + (lane >> 4)) * 16 + h * 8, a.rot_dim, a.interleaved, turn[j], x[i][h]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_size(x[i][h][e]));
+        }
+    float by;
+    float* const scale = a.cache.k_scales + grp;
+    const float s = joined_scale(scale, w.from > 0, wave_max(top), by), inv = 1.f / s;
+    uint8_t* const codes = a.cache.k_codes + grp * (16 * D) + lane * 16;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        u32x4* const at = (u32x4*)(codes + i * 1024);
+        if (mine) {
+            u32x4 c;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    c[2 * h + e] = codes4(coded(x[i][h][4 * e], inv), coded(x[i][h][4 * e + 1], inv),
+                                          coded(x[i][h][4 * e + 2], inv), coded(x[i][h][4 * e + 3], inv));
+            *at = c;
+        } else if (by != 1.f && j < w.from) {
+            u32x4 c = *at;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e] = rescaled4(c[e], by);
+            *at = c;
+        }
+    }
+    if (lane == 0) *scale = s;
+}
+
+template <int D>
+__device__ __forceinline__ void append_values(const Kv8AppendArgs& a, const Kv8Unit& w, int head) {
+    constexpr int E = D == 256 ? 4 : 2;  // elements of a lane, of all 16 tokens
+    const int lane = threadIdx.x & 63, d0 = lane * E;
+    const bool live = d0 < D;
+    const int64_t grp = w.group + (int64_t)head * (a.cache.page_size >> 4);
+    const uint16_t* src = a.src[2] + (w.first - w.from) * a.stride[2] + head * D + d0;
+    uint32_t raw[16][E / 2];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) raw[j][e] = 0u;
+        if (live && j >= w.from && j < w.to)
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) raw[j][e] = ((const uint32_t*)(src + j * a.stride[2]))[e];
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e)
+            top = fmaxf(top, fmaxf(finite_size(bf16_lo(raw[j][e])), finite_size(bf16_hi(raw[j][e]))));
+    float by;
+    float* const scale = a.cache.v_scales + grp;
+    const float s = joined_scale(scale, w.from > 0, wave_max(top), by), inv = 1.f / s;
+    const bool whole = w.from == 0 && w.to == 16;
+    if (live) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            uint8_t* const at = a.cache.v_codes + grp * (16 * D) + (d0 + e) * 16;
+            const auto value = [&](int j) { return (e & 1) ? bf16_hi(raw[j][e / 2]) : bf16_lo(raw[j][e / 2]); };
+            u32x4 c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                c[i] = codes4(coded(value(4 * i), inv), coded(value(4 * i + 1), inv), coded(value(4 * i + 2), inv),
+                              coded(value(4 * i + 3), inv));
+            if (whole) {
+                *(u32x4*)at = c;
+                continue;
+            }
+            if (by != 1.f) {  // the earlier tokens' codes at the new scale (what stands behind the new tokens stays)
+                const u32x4 held = *(const u32x4*)at;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t r = rescaled4(held[i], by);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        if (4 * i + b < w.from) at[4 * i + b] = (uint8_t)(r >> (8 * b));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (4 * i + b >= w.from && 4 * i + b < w.to) at[4 * i + b] = (uint8_t)(c[i] >> (8 * b));
+        }
+    }
+    if (lane == 0) *scale = s;
+}
+
+// Blocks [0, units * parts): a block of 16 tokens, part by part of its heads' keys and then values, a wave each; then a
+// block per token for its queries.
+template <int D>
+__device__ __forceinline__ void append_body(const Kv8AppendArgs& a, int64_t units, int parts) {
+    __shared__ double2 turn[16][D / 2];  // cos, sin of the tokens' angles
+    const int half = a.rot_dim / 2, heads = a.cache.num_kv_heads;
+    const int64_t id = grid_block();
+    const int wave = threadIdx.x >> 6;
+    if (id < units * parts) {
+        const int64_t u = id / parts;
+        const int part = (int)(id - u * parts);
+        const Kv8Unit w = kv8_unit(a.cache, a.batch, u, true);
+        if (w.group < 0) return;
+        if (part * kAppendWaves < heads && half > 0) {  // some wave has keys
+            constexpr int kRuns = 4, kLong = 16 / kRuns;
+            for (int i = threadIdx.x; i < kRuns * half; i += kAppendThreads) {
+                const int run = i / half, f = i - run * half;
+                const double by = (double)a.inv_freq[f];
+                double sn, cs, s1, c1;
+                sincos((double)(w.block * 16 + run * kLong) * by, &sn, &cs);
+                sincos(by, &s1, &c1);
+#pragma unroll
+                for (int j = 0; j < kLong; ++j) {
+                    turn[run * kLong + j][f] = make_double2(cs, sn);
+                    const double c = cs * c1 - sn * s1;
+                    sn = sn * c1 + cs * s1;
+                    cs = c;
+                }
+            }
+            __syncthreads();
+        }
+        const int unit = part * kAppendWaves + wave;
+        if (unit < heads)
+            append_keys<D>(a, w, unit, turn);
+        else if (unit < 2 * heads)
+            append_values<D>(a, w, unit - heads);
+        return;
+    }
+    const int64_t t = id - units * parts;
+    if (t >= a.batch.num_tokens || a.num_q_heads == 0) return;
+    int r;
+    const int pos = kv4_position(a.cache, a.batch, t, r);
+    for (int i = threadIdx.x; i < half; i += kAppendThreads) {
+        double sn, cs;
+        sincos((double)(pos < 0 ? 0 : pos) * (double)a.inv_freq[i], &sn, &cs);
+        turn[0][i] = make_double2(cs, sn);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.num_q_heads * (D / 8); c += kAppendThreads) {
+        const int head = c / (D / 8), d0 = c % (D / 8) * 8;
+        float v[8];
+        load_rotated(a.src[0] + t * a.stride[0] + head * D, d0, a.rot_dim, a.interleaved, turn[0], v);
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        *(u32x4*)(a.q_out + (t * a.num_q_heads + head) * D + d0) = o;
+    }
+}
+
+#define PLE_KV8_KERNEL(D)                                                                                              \
+    __global__ __launch_bounds__(kAppendThreads) void kv8_append_##D##_kernel(Kv8AppendArgs a, int64_t units, int parts) { \
+        append_body<D>(a, units, parts);                                                                               \
+    }
+PLE_KV8_KERNEL(64)
+PLE_KV8_KERNEL(128)
+PLE_KV8_KERNEL(256)
+#undef PLE_KV8_KERNEL
+
+// Blocks of four waves for a block of 16 tokens: a wave a head's keys or values.
+static int kv8_parts(const ple_kv8_cache& c) { return (2 * c.num_kv_heads + kAppendWaves - 1) / kAppendWaves; }
+
+int64_t kv8_append_blocks(const ple_kv8_cache& cache, const ple_kv8_batch& batch, int32_t num_q_heads) {
+    return kv8_units(batch, true) * kv8_parts(cache) + (num_q_heads > 0 ? batch.num_tokens : 0);
+}
+int64_t kv8_read_blocks(const ple_kv8_cache& cache, const ple_kv8_batch& batch) {
+    return kv8_units(batch, false) * kv8_parts(cache) + batch.num_tokens;
+}
+
+hipError_t launch_kv8_append(const Kv8AppendArgs& a, hipStream_t s) {
+    const int64_t units = kv8_units(a.batch, true);
+    const int parts = kv8_parts(a.cache);
+    const dim3 grid = block_grid(kv8_append_blocks(a.cache, a.batch, a.num_q_heads));
+    if (a.cache.head_dim == 64)
+        hipLaunchKernelGGL(kv8_append_64_kernel, grid, dim3(kAppendThreads), 0, s, a, units, parts);
+    else if (a.cache.head_dim == 128)
+        hipLaunchKernelGGL(kv8_append_128_kernel, grid, dim3(kAppendThreads), 0, s, a, units, parts);
+    else
+        hipLaunchKernelGGL(kv8_append_256_kernel, grid, dim3(kAppendThreads), 0, s, a, units, parts);
+    return hipGetLastError();
+}
+
+struct Kv8ReadArgs {
+    ple_kv8_cache cache;
+    ple_kv8_batch batch;
+    uint16_t *k_out, *v_out;
+    int64_t units;
+    int32_t parts;
+};
+
+__device__ __forceinline__ void unpack4(uint32_t w, float s, float (&v)[4]) {
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    v[0] = lo[0] * s;
+    v[1] = lo[1] * s;
+    v[2] = hi[0] * s;
+    v[3] = hi[1] * s;
+}
+
+// A block of 16 tokens, a wave a head's keys or values, as append; tokens that stand on no page are zeros.
+template <int D>
+__device__ __forceinline__ void read_body(const Kv8ReadArgs& a) {
+    const int64_t id = grid_block(), T = a.batch.num_tokens;
+    if (id >= a.units * a.parts) {  // a block per token: those of no request and of no place in the table
+        const int64_t t = id - a.units * a.parts;
+        if (t >= T) return;
+        int r;
+        if (kv4_position(a.cache, a.batch, t, r) >= 0) return;
+        const int row = a.cache.num_kv_heads * D;
+        for (int e = threadIdx.x * 8; e < row; e += kAppendThreads * 8)
+            *(u32x4*)(a.k_out + t * row + e) = *(u32x4*)(a.v_out + t * row + e) = u32x4{0u, 0u, 0u, 0u};
+        return;
+    }
+    const int64_t u = id / a.parts;
+    const int lane = threadIdx.x & 63, heads = a.cache.num_kv_heads;
+    const int unit = (int)(id - u * a.parts) * kAppendWaves + (threadIdx.x >> 6);
+    const Kv8Unit w = kv8_unit(a.cache, a.batch, u, false);
+    if (!w.any || unit >= 2 * heads) return;
+    const int head = unit < heads ? unit : unit - heads;
+    const int64_t grp = w.group + (int64_t)head * (a.cache.page_size >> 4), tokens = (int64_t)heads * D;
+    if (unit < heads) {
+        const int j = lane & 15;
+        if (j < w.from || j >= w.to) return;
+        uint16_t* const out = a.k_out + (w.first + (j - w.from)) * tokens + head * D + (lane >> 4) * 16;
+        const float s = w.group < 0 ? 0.f : a.cache.k_scales[grp];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            u32x4 o[2] = {u32x4{0u, 0u, 0u, 0u}, u32x4{0u, 0u, 0u, 0u}};
+            if (w.group >= 0) {
+                const u32x4 c = *(const u32x4*)(a.cache.k_codes + grp * (16 * D) + i * 1024 + lane * 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v[4];
+                    unpack4(c[e], s, v);
+                    o[e / 2][(e & 1) * 2] = pack_bf16x2(v[0], v[1]);
+                    o[e / 2][(e & 1) * 2 + 1] = pack_bf16x2(v[2], v[3]);
+                }
+            }
+            *(u32x4*)(out + i * 64) = o[0];
+            *(u32x4*)(out + i * 64 + 8) = o[1];
+        }
+        return;
+    }
+    constexpr int E = D == 256 ? 4 : 2;
+    const int d0 = lane * E;
+    if (d0 >= D) return;
+    const float s = w.group < 0 ? 0.f : a.cache.v_scales[grp];
+    u32x4 c[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        c[e] = w.group < 0 ? u32x4{0u, 0u, 0u, 0u} : *(const u32x4*)(a.cache.v_codes + grp * (16 * D) + (d0 + e) * 16);
+    uint16_t* const out = a.v_out + (w.first - w.from) * tokens + head * D + d0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v[E][4];
+#pragma unroll
+        for (int e = 0; e < E; ++e) unpack4(c[e][i], s, v[e]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int j = 4 * i + b;
+            if (j < w.from || j >= w.to) continue;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) ((uint32_t*)(out + j * tokens))[e / 2] = pack_bf16x2(v[e][b], v[e + 1][b]);
+        }
+    }
+}
+
+#define PLE_KV8_KERNEL(D) \
+    __global__ __launch_bounds__(kAppendThreads) void kv8_read_##D##_kernel(Kv8ReadArgs a) { read_body<D>(a); }
+PLE_KV8_KERNEL(64)
+PLE_KV8_KERNEL(128)
+PLE_KV8_KERNEL(256)
+#undef PLE_KV8_KERNEL
+
+hipError_t launch_kv8_read(const ple_kv8_cache& cache, const ple_kv8_batch& batch, uint16_t* k_out, uint16_t* v_out,
+                           hipStream_t s) {
+    const Kv8ReadArgs a = {cache, batch, k_out, v_out, kv8_units(batch, false), kv8_parts(cache)};
+    const dim3 grid = block_grid(kv8_read_blocks(cache, batch));
+    if (cache.head_dim == 64)
+        hipLaunchKernelGGL(kv8_read_64_kernel, grid, dim3(kAppendThreads), 0, s, a);
+    else if (cache.head_dim == 128)
+        hipLaunchKernelGGL(kv8_read_128_kernel, grid, dim3(kAppendThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL(kv8_read_256_kernel, grid, dim3(kAppendThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace ple

@@ -1,0 +1,676 @@
+// Causal attention over the paged 8-bit cache.
+//
+// Per query head with its rows q_i:  s_ij = scale <q_i, k_j>,  out_i = sum_j
+// exp(s_ij) v_j / sum_j exp(s_ij), in one pass over the cache with a running
+// maximum in fp32.  Rows, tiles of 64 tokens, page walks, splits and joins are
+// those of ple_paged_attention.h; the products run on 16x16x32 MFMAs with the
+// tokens (then the value elements) as the first operand, the queries as the
+// second:  S^T [token][row] = K Q^T,  O^T [element][row] += V^T P^T.
+//
+// An e4m3 code is exact in bf16 and in fp16, so keys enter beside the bf16
+// queries as codes and their block's scale multiplies the product.  The
+// values' scale s_v of a block joins the exponent:
+//   z_ij = s_ij log2 e + log2 s_v(j),  p_ij = 2^(z_ij - m_i),  m_i = max_j z_ij
+//   out_i = sum_j p_ij code_j / sum_j p_ij / s_v(j)
+// so that the weights of the value product (fp16) carry it without a product
+// per element, whatever the scales' range, and codes enter as they are.
+//
+// Layouts, chosen so that nothing crosses lanes:
+//  - MFMA i of a tile takes its token rows in the order row ρ <-> token
+//    16 (ρ/4) + 4 i + ρ%4.  Lane (row n = lane%16, g = lane/16) of the result
+//    holds rows ρ = 4g .. 4g+3, so after four MFMAs it holds tokens 16 g ..
+//    16 g + 15 of its query row: one block of the cache, with one scale for
+//    keys and one for values, and just what it supplies to the second product.
+//  - a lane's 16 bytes of key codes are 16 elements of one token, four
+//    neighbouring lanes' 64 contiguous bytes; its 16 bytes of value codes are
+//    one element of 16 tokens, 16 lanes' 256 contiguous bytes.
+#include "ple_8bit_launch.h"
+#include "ple_paged_attention.h"
+
+namespace ple {
+
+union BFrag {
+    bf16x8 v;
+    uint32_t u[4];
+};
+
+// 8 codes (two words) as bf16 and as fp16.
+__device__ __forceinline__ void fp8_to_bf16(uint32_t lo, uint32_t hi, BFrag& f) {
+    f.u[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
+    f.u[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
+    f.u[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
+    f.u[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+}
+__device__ __forceinline__ void fp8_to_f16(uint32_t lo, uint32_t hi, Frag& f) {
+    f.p[0] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
+    f.p[1] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
+    f.p[2] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
+    f.p[3] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
+}
+// The queries of MT x 16 rows from row0 on: lane (n, g) holds, of row 16 mt + n, the elements that its key codes meet, and
+// the tokens it sees.
+template <int D, int MT>
+__device__ __forceinline__ void kv8_queries(const Kv8AttentionArgs& a, const AttnTile& w, int row0, int head, int begin,
+                                            int end, BFrag (&q)[MT][D / 32], int (&see_lo)[MT], int (&see_hi)[MT]) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int row = row0 + mt * 16 + n;
+        const bool live = row < w.row1;
+        const int i = row / a.group, hq = head * a.group + (row - i * a.group);
+        const uint16_t* src = a.q + (w.first + i) * a.q_stride + hq * D + g * (D / 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 32; ++ks) {
+            const u32x4 x = live ? *(const u32x4*)(src + ks * 8) : u32x4{0u, 0u, 0u, 0u};
+            q[mt][ks].v = __builtin_bit_cast(bf16x8, x);
+        }
+        const int p = w.before + i;
+        // (rows past the tile's end, all zeros and never stored, see everything, which keeps the masks out of whole tiles)
+        see_hi[mt] = live ? min(end, p + 1) : end;
+        see_lo[mt] = live ? max(begin, a.window > 0 ? p - a.window + 1 : 0) : begin;
+    }
+}
+
+// The scales of a lane's block in a tile: what turns its products into base-2 exponents, log2 of the values' scale, and
+// one over it.
+struct BlockScales {
+    float key, log_value, per_value;
+    __device__ __forceinline__ void set(float base, float k, float v) {
+        key = base * k;
+        log_value = __builtin_amdgcn_logf(v);
+        per_value = __builtin_amdgcn_rcpf(v);
+    }
+};
+
+// Exponents from which on a product's rounding, as the maximum was rounded, is more than a weight's own: there the maximum
+// is taken from the rounded products, not in one step with them.  `wide`: the wave has such rows.
+constexpr float kWide = 4194304.0f;  // 2^22
+
+// The weights of one tile: s (products, lane (n, g) holding tokens tg .. tg + 15 of MT rows) becomes the fp16 weights p;
+// m, l and o (the rows' running maxima, sums and outputs) move on.  `some`: not every row sees the whole tile.
+template <int NB, int MT>
+__device__ __forceinline__ void kv8_softmax(f32x4 (&s)[MT][4], const BlockScales& c, bool some, bool bad, int tg,
+                                            const int (&see_lo)[MT], const int (&see_hi)[MT], float (&m)[MT], float (&l)[MT],
+                                            f32x4 (&o)[MT][NB], bool& wide, Frag (&p)[MT][2]) {
+    if (some) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int tok = tg + 4 * i + e;
+                    if (bad || tok < see_lo[mt] || tok >= see_hi[mt]) s[mt][i][e] = -__builtin_inff();
+                }
+    }
+    float mn[MT];
+    bool up = false;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, s[mt][i][e]);
+        mn[mt] = fmaxf(m[mt], quad_max(fmaf(top, c.key, c.log_value)));  // (the scales are positive)
+        up |= mn[mt] > m[mt] + kSlack;
+    }
+    if (__ballot(up) != 0) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            // (a row by itself, whatever the wave's others do: its result does not depend on them)
+            const float next = mn[mt] > m[mt] + kSlack ? mn[mt] : m[mt];
+            const float by = m[mt] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m[mt] - next);
+            l[mt] *= by;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) o[mt][b] *= by;
+            m[mt] = next;
+        }
+        bool far = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) far |= fabsf(m[mt]) >= kWide && m[mt] != -__builtin_inff();
+        wide |= __ballot(far) != 0;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        float key = c.key, sub = c.log_value + (m[mt] == -__builtin_inff() ? 0.f : kWeightShift - m[mt]);
+        if (wide) {
+            const bool far = fabsf(m[mt]) >= kWide && m[mt] != -__builtin_inff();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (far) s[mt][i][e] = fmaf(s[mt][i][e], key, c.log_value) - m[mt];
+            if (far) {
+                key = 1.f;
+                sub = kWeightShift;
+            }
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(s[mt][i][e], key, sub));
+                const float y = __builtin_amdgcn_exp2f(fmaf(s[mt][i][e + 1], key, sub));
+                sum += x + y;
+                p[mt][i >> 1].p[(i & 1) * 2 + e / 2] = f16x2{(_Float16)x, (_Float16)y};
+            }
+        l[mt] = fmaf(sum, c.per_value, l[mt]);
+    }
+}
+
+// NaN elements of values in a tile that some row does not see as a whole would reach that row too, as 0 * NaN.  There they
+// enter the product as zeros, LDS keeps which they were (a bit a token of each lane's codes, [element block][lane]), and
+// the rows that do see one are found by a product of ones for NaN elements and ones for seen tokens.
+
+// Value codes of a lane's block: those of tokens outside [lo, hi), which may be anything, are cleared.  Returns whether the
+// wave has NaN among the others; they are cleared too then, and noted.
+template <int NB>
+__device__ __forceinline__ bool kv8_clear(u32x4 (&v)[NB], bool bad, int tg, int lo, int hi, uint16_t* noted) {
+    uint32_t keep[4], found = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        keep[i] = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int tok = tg + 4 * i + e;
+            if (!bad && tok >= lo && tok < hi) keep[i] |= 0xFFu << (8 * e);
+        }
+    }
+    const auto nans = [](uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u; };
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[b][i] &= keep[i];
+            found |= nans(v[b][i]);
+        }
+    if (__ballot(found != 0u) == 0) return false;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        uint32_t bits = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t is = nans(v[b][i]);
+            bits |= (is * 0x10204080u >> 28) << (4 * i);  // bits 0, 8, 16 and 24 side by side
+            v[b][i] &= ~(is * 0xFFu);
+        }
+        noted[b * 64] = (uint16_t)bits;
+    }
+    return true;
+}
+
+// The elements (bit 4 b + e) of the lane's rows that a noted NaN reaches.
+template <int NB, int MT>
+__device__ __forceinline__ void kv8_see_nans(const uint16_t* noted, int tg, const int (&see_lo)[MT], const int (&see_hi)[MT],
+                                             uint64_t (&nan)[MT]) {
+#pragma unroll 1
+    for (int b = 0; b < NB; ++b) {
+        const uint32_t bits = noted[b * 64];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            f32x4 count = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                Frag is, sees;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int tok = tg + 8 * h + e;
+                    is.v[e] = (_Float16)(bits >> (8 * h + e) & 1u ? 1.f : 0.f);
+                    sees.v[e] = (_Float16)(tok >= see_lo[mt] && tok < see_hi[mt] ? 1.f : 0.f);
+                }
+                count = __builtin_amdgcn_mfma_f32_16x16x32_f16(is.v, sees.v, count, 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (count[e] > 0.f) nan[mt] |= (uint64_t)1 << (4 * b + e);
+        }
+    }
+}
+
+template <int NB, int MT>
+__device__ __forceinline__ void kv8_give_nans(const uint64_t (&nan)[MT], f32x4 (&o)[MT][NB]) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        if (__ballot(nan[mt] != 0) == 0) continue;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (nan[mt] >> (4 * b + e) & 1u) o[mt][b][e] = __builtin_nanf("");
+    }
+}
+
+template <int D, int WAVES>
+struct Kv8Shape {
+    static constexpr int KS = D / 32;  // k-steps of the first product
+    static constexpr int NB = D / 16;  // element blocks
+    static constexpr int LDS = kAttnWaves * 16 * kJoinRow<D> * 4;  // the join's, and before it the waves' notes
+    static_assert(WAVES * NB * 128 <= LDS, "a bit per code of a tile");
+};
+
+// Few rows: the waves of a block take the tiles of a cache range in turn and join through LDS.  The next tile is on its
+// way while this one is used, its page-table entry a tile before that.
+template <int D, int MT, int WAVES>
+__device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
+    using Sh = Kv8Shape<D, WAVES>;
+    extern __shared__ __align__(16) char lds[];
+    const int split = blockIdx.y;
+    int r, head, tile;
+    attn_block(a, r, head, tile);
+    AttnTile w;
+    attn_request(a, r, w);
+    attn_idle_tokens(a);
+    if (!attn_tile(a, tile, w)) return;
+    const int splits = attn_splits(a, w);
+    if (split >= splits) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = lane & 15, g = lane >> 4;
+    const int begin = w.lo + split * a.chunk;
+    const int end = split == splits - 1 ? w.hi : min(w.hi, begin + a.chunk);
+    const float base = a.scale * 1.44269504088896341f;
+
+    f32x4 o[MT][Sh::NB];
+    float m[MT], l[MT];
+    uint64_t nan[MT] = {};
+    bool wide = false;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        m[mt] = -__builtin_inff();
+        l[mt] = 0.f;
+#pragma unroll
+        for (int b = 0; b < Sh::NB; ++b) o[mt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int32_t* table_row = a.batch.page_table + (int64_t)r * a.batch.table_width;
+    uint16_t* const noted = (uint16_t*)lds + wave * (Sh::NB * 64) + lane;
+    bool bad_next = false;
+    u32x4 kraw[4][D / 64], vraw[Sh::NB];
+    float ks, vs;
+    const int first = begin + wave * kTile;
+    PageWalk walk(a, table_row, head, first + 16 * g, WAVES * kTile / 16, end);
+    auto load = [&](int t0) {
+        const int grp = walk.number(t0 + 16 * g, end);
+        walk.fetch();
+        bad_next = grp < 0;
+        const int64_t safe = grp < 0 ? 0 : grp;
+        // (a block that no token was written to may have any scale)
+        ks = grp < 0 ? 1.f : a.cache.k_scales[safe];
+        vs = grp < 0 ? 1.f : a.cache.v_scales[safe];
+        // keys: block n / 4, token 4 i + n % 4
+        const int64_t kg = __shfl((int)safe, (n >> 2) * 16, kWave);
+        const uint8_t* kc = a.cache.k_codes + kg * (16 * D) + g * (D / 64) * 256 + (n & 3) * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) kraw[i][c] = *(const u32x4*)(kc + c * 256 + i * 64);
+        const uint8_t* vc = a.cache.v_codes + safe * (16 * D) + n * 16;
+#pragma unroll
+        for (int b = 0; b < Sh::NB; ++b) vraw[b] = *(const u32x4*)(vc + b * 256);
+    };
+    if (first < end) {
+        walk.fetch();
+        load(first);
+    }
+    BFrag q[MT][Sh::KS];
+    int see_lo[MT], see_hi[MT];
+    kv8_queries<D, MT>(a, w, w.row0, head, begin, end, q, see_lo, see_hi);
+    for (int t0 = first; t0 < end; t0 += WAVES * kTile) {
+        const int tg = t0 + 16 * g;  // this lane's block g of the tile
+        const bool bad = bad_next;
+        BlockScales c;
+        c.set(base, ks, vs);
+
+        f32x4 s[MT][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            BFrag f[Sh::KS];
+#pragma unroll
+            for (int k = 0; k < Sh::KS; ++k) fp8_to_bf16(kraw[i][k / 2][2 * (k & 1)], kraw[i][k / 2][2 * (k & 1) + 1], f[k]);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                s[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < Sh::KS; ++k)
+                    s[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[k].v, q[mt][k].v, s[mt][i], 0, 0, 0);
+            }
+        }
+        u32x4 v[Sh::NB];
+#pragma unroll
+        for (int b = 0; b < Sh::NB; ++b) v[b] = vraw[b];
+        if (t0 + WAVES * kTile < end) load(t0 + WAVES * kTile);
+
+        // a tile that not every row sees as a whole
+        bool every = t0 >= w.first_seen && t0 + kTile <= end && __ballot(bad) == 0;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) every = every && t0 >= see_lo[mt] && t0 + kTile <= see_hi[mt];
+        const bool some = __ballot(!every) != 0;
+        Frag p[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)  // (one after the other: fewer registers than all of them together)
+            kv8_softmax<Sh::NB, 1>((f32x4(&)[1][4])s[mt], c, some, bad, tg, (int(&)[1])see_lo[mt], (int(&)[1])see_hi[mt],
+                                   (float(&)[1])m[mt], (float(&)[1])l[mt], (f32x4(&)[1][Sh::NB])o[mt], wide, (Frag(&)[1][2])p[mt]);
+        if (some && kv8_clear<Sh::NB>(v, bad, tg, w.first_seen, end, noted)) kv8_see_nans<Sh::NB>(noted, tg, see_lo, see_hi, nan);
+#pragma unroll
+        for (int b = 0; b < Sh::NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                Frag f;
+                fp8_to_f16(v[b][2 * h], v[b][2 * h + 1], f);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    o[mt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.v, p[mt][h].v, o[mt][b], 0, 0, 0);
+            }
+    }
+    kv8_give_nans<Sh::NB>(nan, o);
+    const uint32_t none[MT] = {};
+    attn_join_waves<D, MT, WAVES>(a, w, head, split, splits, lds, m, l, o, none);
+}
+
+// D, row tiles, waves, waves per SIMD that registers allow
+#define PLE_ATTN_SHAPES(X)                                                                                        \
+    X(64, 1, 4, 3) X(64, 1, 8, 2) X(64, 2, 4, 2) X(64, 2, 8, 2) X(128, 1, 4, 2) X(128, 1, 8, 2) X(128, 2, 4, 2) \
+    X(128, 2, 8, 2) X(256, 1, 4, 1) X(256, 1, 8, 2)
+#define PLE_ATTN_KERNEL(D, MT, WAVES, OCC)                                                                                  \
+    __global__ __launch_bounds__(WAVES * kWave, OCC) void kv8_attention_##D##_##MT##x##WAVES##_kernel(Kv8AttentionArgs a) { \
+        kv8_body<D, MT, WAVES>(a);                                                                                          \
+    }
+PLE_ATTN_SHAPES(PLE_ATTN_KERNEL)
+#undef PLE_ATTN_KERNEL
+
+// ---------------------------------------------------------------------------
+// Many rows (a chunk of a prefill): a block's four waves hold 32 rows each and
+// go through the cache tiles together; each wave dequantises a quarter of a
+// tile (16 tokens of the keys, a quarter of the value elements) and leaves it
+// in LDS as finished MFMA fragments, one 16-byte read per lane each, so a tile
+// is dequantised once for 128 rows.  Two tiles in LDS: the next one is filled
+// while this one is used, with one barrier a tile.
+// ---------------------------------------------------------------------------
+template <int D>
+struct Kv8ChunkShape {
+    static constexpr int KS = D / 32, NB = D / 16, WB = D / 64;  // WB: element blocks that a wave dequantises
+    static constexpr int K_BYTES = 4 * KS * 1024, V_BYTES = NB * 2 * 1024;
+    static constexpr int BUF = K_BYTES + V_BYTES;
+    static constexpr int NOTES_AT = 2 * BUF, NOTES = NB * 128;         // NaN values of a tile, and whether there are any
+    static constexpr int ANY_AT = NOTES_AT + 2 * NOTES;
+    static constexpr int LDS = ANY_AT + 2 * kAttnWaves * 4;
+};
+
+// Rows [w.row0, w.row1) against the cache's tokens [begin, end).  Results go to the call's outputs (at < 0), or to the
+// partial results from row `at` on.
+template <int D>
+__device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const AttnTile& w, int r, int head, int begin,
+                                                int end, int at) {
+    using Sh = Kv8ChunkShape<D>;
+    constexpr int MT = 2;
+    extern __shared__ __align__(16) char lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const float base = a.scale * 1.44269504088896341f;
+    // what every row of the block sees
+    const int common_lo = a.window > 0 ? max(0, w.before + (w.row1 - 1) / a.group - a.window + 1) : 0;
+    const int common_hi = min(end, w.before + w.row0 / a.group + 1);
+    const int32_t* table_row = a.batch.page_table + (int64_t)r * a.batch.table_width;
+
+    // a tile's quarter, as loaded
+    u32x4 kraw[D / 64], vraw[Sh::WB];
+    float ks, vs;
+    bool bad_next = false;
+    PageWalk walk(a, table_row, head, begin + 16 * g, kTile / 16, end);
+    int grp = -1;
+    int64_t kg = 0;  // of the tile to load next: this lane's block, and block n / 4 of the tile
+    auto aim = [&](int t0) {
+        grp = walk.number(t0 + 16 * g, end);
+        walk.fetch();
+        kg = __shfl(max(grp, 0), (n >> 2) * 16, kWave);
+    };
+    auto load = [&]() {
+        bad_next = grp < 0;
+        const int64_t safe = max(grp, 0);
+        ks = grp < 0 ? 1.f : a.cache.k_scales[safe];
+        vs = grp < 0 ? 1.f : a.cache.v_scales[safe];
+        // keys: token 4 wave + n % 4 of block n / 4
+        const uint8_t* kc = a.cache.k_codes + kg * (16 * D) + g * (D / 64) * 256 + (4 * wave + (n & 3)) * 16;
+        // values: elements 16 (wave WB + b) + n of block g
+        const uint8_t* vc = a.cache.v_codes + safe * (16 * D) + (wave * Sh::WB * 16 + n) * 16;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            kraw[c] = *(const u32x4*)(kc + c * 256);
+            vraw[c] = *(const u32x4*)(vc + c * 256);
+        }
+    };
+    // the first tile is on its way before the queries are
+    if (begin < end) {
+        walk.fetch();
+        aim(begin);
+        load();
+        aim(begin + kTile);
+    }
+    BFrag q[MT][Sh::KS];
+    int see_lo[MT], see_hi[MT];
+    kv8_queries<D, MT>(a, w, w.row0 + wave * (16 * MT), head, begin, end, q, see_lo, see_hi);
+    f32x4 o[MT][Sh::NB];
+    float m[MT], l[MT];
+    uint64_t nan[MT] = {};
+    bool wide = false;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        m[mt] = -__builtin_inff();
+        l[mt] = 0.f;
+#pragma unroll
+        for (int b = 0; b < Sh::NB; ++b) o[mt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // whether some row does not see the whole tile (the same for the block: `bad` is the tile's four blocks)
+    auto partial = [&](int t0, bool bad) {
+        return t0 < common_lo || t0 < begin || t0 + kTile > common_hi || __ballot(bad) != 0;
+    };
+    auto fill = [&](int t0, int buf) {
+        char* kb = lds + buf * Sh::BUF + (wave * Sh::KS) * 1024 + lane * 16;
+        char* vb = lds + buf * Sh::BUF + Sh::K_BYTES + (wave * Sh::WB * 2) * 1024 + lane * 16;
+#pragma unroll
+        for (int k = 0; k < Sh::KS; ++k) {
+            BFrag f;
+            fp8_to_bf16(kraw[k / 2][2 * (k & 1)], kraw[k / 2][2 * (k & 1) + 1], f);
+            *(bf16x8*)(kb + k * 1024) = f.v;
+        }
+        if (partial(t0, bad_next)) {
+            uint16_t* const noted = (uint16_t*)(lds + Sh::NOTES_AT + buf * Sh::NOTES) + wave * (Sh::WB * 64) + lane;
+            const bool nans = kv8_clear<Sh::WB>(vraw, bad_next, t0 + 16 * g, w.first_seen, end, noted);
+            if (!nans)
+#pragma unroll
+                for (int b = 0; b < Sh::WB; ++b) noted[b * 64] = 0;  // (another wave's may be looked through)
+            if (lane == 0) *(int*)(lds + Sh::ANY_AT + (buf * kAttnWaves + wave) * 4) = nans;
+        }
+#pragma unroll
+        for (int b = 0; b < Sh::WB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                Frag f;
+                fp8_to_f16(vraw[b][2 * h], vraw[b][2 * h + 1], f);
+                *(u32x4*)(vb + (b * 2 + h) * 1024) = f.u;
+            }
+    };
+
+    bool bad = false;
+    BlockScales c = {};
+    if (begin < end) {
+        fill(begin, 0);
+        bad = bad_next;
+        c.set(base, ks, vs);
+    }
+    int buf = 0;
+    for (int t0 = begin; t0 < end; t0 += kTile, buf ^= 1) {
+        const bool more = t0 + kTile < end;
+        __syncthreads();  // this tile is whole; every read of the other buffer is done
+        if (more) load();
+        const char* kb = lds + buf * Sh::BUF + lane * 16;
+        const char* vb = kb + Sh::K_BYTES;
+        const bool some = partial(t0, bad);
+        f32x4 s[MT][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) s[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < Sh::KS; ++k) {
+                const bf16x8 f = *(const bf16x8*)(kb + (i * Sh::KS + k) * 1024);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    s[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[mt][k].v, s[mt][i], 0, 0, 0);
+            }
+        }
+        reads_ahead<4 * Sh::KS, MT>();
+        aim(t0 + 2 * kTile);
+        Frag p[MT][2];
+        kv8_softmax<Sh::NB, MT>(s, c, some, bad, t0 + 16 * g, see_lo, see_hi, m, l, o, wide, p);
+#pragma unroll
+        for (int b = 0; b < Sh::NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f16x8 f = *(const f16x8*)(vb + (b * 2 + h) * 1024);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    o[mt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[mt][h].v, o[mt][b], 0, 0, 0);
+            }
+        reads_ahead<2 * Sh::NB, MT>();
+        if (some) {
+            int any = 0;
+#pragma unroll
+            for (int k = 0; k < kAttnWaves; ++k) any |= *(const int*)(lds + Sh::ANY_AT + (buf * kAttnWaves + k) * 4);
+            if (any != 0)
+                kv8_see_nans<Sh::NB>((const uint16_t*)(lds + Sh::NOTES_AT + buf * Sh::NOTES) + lane, t0 + 16 * g, see_lo,
+                                     see_hi, nan);
+        }
+        if (more) {
+            fill(t0 + kTile, buf ^ 1);
+            bad = bad_next;
+            c.set(base, ks, vs);
+        }
+    }
+
+    kv8_give_nans<Sh::NB>(nan, o);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        float total = l[mt];
+        total += __shfl_xor(total, 16, kWave);
+        total += __shfl_xor(total, 32, kWave);
+        const int row = w.row0 + wave * (16 * MT) + mt * 16 + n;
+        if (row >= w.row1) continue;
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const float lse2 = total == 0.f ? -__builtin_inff() : (m[mt] - kWeightShift) + log2f(total);
+        const int i = row / a.group, hq = head * a.group + (row - i * a.group);
+        const int64_t orow = (w.first + i) * a.num_q_heads + hq;
+        const int64_t place = at + (row - w.row0);
+#pragma unroll
+        for (int b = 0; b < Sh::NB; ++b) {
+            const f32x4 x = o[mt][b] * inv;
+            if (at < 0)
+                *(u32x2*)(a.out + orow * D + b * 16 + g * 4) = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+            else
+                *(f32x4*)(a.part + place * D + b * 16 + g * 4) = x;
+        }
+        if (g == 0) {
+            if (at >= 0)
+                a.part[(int64_t)2 * a.flat * kChunkRows * D + place] = lse2;
+            else if (a.lse != nullptr)
+                a.lse[orow] = lse2 * 0.693147180559945309f;
+        }
+    }
+}
+
+#define PLE_ATTN_KERNEL(D, OCC)                                                                                         \
+    __global__ __launch_bounds__(kAttnThreads, OCC) void kv8_attention_chunk_##D##_kernel(Kv8AttentionArgs a) {         \
+        attn_chunk_body(a, [&](const AttnTile& w, int r, int head, int begin, int end, int at) {                        \
+            kv8_chunk_piece<D>(a, w, r, head, begin, end, at);                                                          \
+        });                                                                                                             \
+    }
+PLE_ATTN_KERNEL(64, 2)
+PLE_ATTN_KERNEL(128, 2)
+PLE_ATTN_KERNEL(256, 1)
+#undef PLE_ATTN_KERNEL
+
+#define PLE_ATTN_KERNEL(D)                                                                                  \
+    __global__ __launch_bounds__(256) void kv8_attention_join_##D##_1_kernel(Kv8AttentionArgs a) {          \
+        attn_join_body<D, 1>(a);                                                                            \
+    }                                                                                                       \
+    __global__ __launch_bounds__(256) void kv8_attention_join_##D##_4_kernel(Kv8AttentionArgs a) {          \
+        attn_join_body<D, 4>(a);                                                                            \
+    }                                                                                                       \
+    __global__ __launch_bounds__(256) void kv8_attention_flat_join_##D##_kernel(Kv8AttentionArgs a) {       \
+        attn_flat_join_body<D>(a);                                                                          \
+    }
+PLE_ATTN_KERNEL(64)
+PLE_ATTN_KERNEL(128)
+PLE_ATTN_KERNEL(256)
+#undef PLE_ATTN_KERNEL
+
+void plan_kv8_attention(Kv8AttentionArgs& a) {
+    const int64_t T = a.batch.num_tokens, R = a.batch.num_reqs;
+    const int64_t cover = (int64_t)a.batch.table_width * a.cache.page_size;
+    int64_t new_max = a.batch.max_request_tokens > 0 ? a.batch.max_request_tokens : T;
+    new_max = new_max < T ? new_max : T;
+    int64_t len = a.batch.max_seq_len > 0 && a.batch.max_seq_len < cover ? a.batch.max_seq_len : cover;
+    const int64_t rows = new_max * a.group;
+    a.rows = rows <= 16 || (rows <= 64 && a.cache.head_dim == 256) ? 16 : (rows <= 64 ? 32 : kChunkRows);
+    a.tiles = (int)((rows + a.rows - 1) / a.rows);
+    if (a.window > 0) {
+        const int64_t span = (int64_t)a.window + a.rows / a.group + 1 + 15;
+        len = len < span ? len : span;
+    }
+    const int64_t blocks = R * a.cache.num_kv_heads * a.tiles;
+    // (the line's length has to fit 32 bits whatever the hints say)
+    if (a.rows == kChunkRows && R <= kWave && blocks > 0 && blocks <= kFlatUnits &&
+        blocks * (cover / kTile + 2 + kFlatStart) < ((int64_t)1 << 30)) {
+        const int64_t most = blocks * ((len + kTile - 1) / kTile + 1 + kFlatStart), slots = a.cache.head_dim == 256 ? 256 : 512;
+        const int64_t shares = (most + kFlatLeast - 1) / kFlatLeast;
+        a.flat = (int)(shares < slots ? shares : slots);
+        a.waves = kAttnWaves;
+        a.splits = 1;
+        return;
+    }
+    a.waves = blocks <= 256 && a.rows < kChunkRows ? 8 : 4;
+    const int64_t slots = a.waves == 8 ? 256 : (a.rows == 16 && a.cache.head_dim == 64 ? 768 : 512);
+    int64_t splits = blocks <= 0 || a.rows == kChunkRows ? 1 : slots / blocks;
+    const int64_t most_splits = (len + 1023) / 1024;
+    splits = splits < most_splits ? splits : most_splits;
+    splits = splits < 1 ? 1 : (splits < kMostSplits - 1 ? splits : kMostSplits - 1);
+    int64_t chunk = (len + splits - 1) / splits;
+    const int64_t round = a.rows == kChunkRows ? kTile : kTile * a.waves;  // what a block goes through at a time
+    chunk = (chunk + round - 1) / round * round;
+    a.chunk = (int)chunk;
+    // (a range starts at a multiple of 16, up to 15 tokens before the first that is seen; the last split takes those)
+    a.splits = (int)((len + chunk - 1) / chunk);
+    if (a.splits < 1) a.splits = 1;
+}
+
+size_t kv8_attention_part_bytes(const Kv8AttentionArgs& a) { return attention_part_bytes(a); }
+int64_t kv8_attention_threads(const Kv8AttentionArgs& a) { return attention_threads(a); }
+
+hipError_t launch_kv8_attention(const Kv8AttentionArgs& a, hipStream_t s) {
+    const int D = a.cache.head_dim, mt = a.rows / 16;
+    hipError_t e = hipErrorInvalidValue;
+    if (a.rows == kChunkRows)
+        e = D == 64    ? launch_attention<Kv8AttentionArgs, kv8_attention_chunk_64_kernel, Kv8ChunkShape<64>::LDS>(a, kAttnThreads, s)
+            : D == 128 ? launch_attention<Kv8AttentionArgs, kv8_attention_chunk_128_kernel, Kv8ChunkShape<128>::LDS>(a, kAttnThreads, s)
+                       : launch_attention<Kv8AttentionArgs, kv8_attention_chunk_256_kernel, Kv8ChunkShape<256>::LDS>(a, kAttnThreads, s);
+#define PLE_ATTN_LAUNCH(DD, MT, WAVES, OCC)                                                                              \
+    if (D == DD && mt == MT && a.waves == WAVES)                                                                         \
+        e = launch_attention<Kv8AttentionArgs, kv8_attention_##DD##_##MT##x##WAVES##_kernel, Kv8Shape<DD, WAVES>::LDS>(  \
+            a, WAVES * kWave, s);
+    PLE_ATTN_SHAPES(PLE_ATTN_LAUNCH)
+#undef PLE_ATTN_LAUNCH
+    if (e != hipSuccess) return e;
+#define PLE_ATTN_LAUNCH(DD)                                                                                         \
+    if (D == DD)                                                                                                    \
+        return launch_attention_join(a, kv8_attention_join_##DD##_1_kernel, kv8_attention_join_##DD##_4_kernel,     \
+                                     kv8_attention_flat_join_##DD##_kernel, s);
+    PLE_ATTN_LAUNCH(64)
+    PLE_ATTN_LAUNCH(128)
+    PLE_ATTN_LAUNCH(256)
+#undef PLE_ATTN_LAUNCH
+    return hipErrorInvalidValue;
+}
+
+}  // namespace ple

@@ -1,0 +1,195 @@
+// The residual's addition, RMS norm and quantisation to 8 bits of a token's row, in one pass over it.
+//
+//   h = bf16(x + residual),  u = h w,  a = max|u|,  r = 1 / sqrt(mean h^2 + eps):
+//   code = round(127 u / a),  scale = a r / 127
+//
+// The norm's factor cancels in the quotient, so a code depends on u and a
+// alone, which fp32 holds exactly (8 x 8 significant bits), and 127 u too (23
+// bits): with one correction of u / a by its remainder the rounded quotient is
+// never on the wrong side of a border.  (u = U 2^i, a = A 2^j, U and A below
+// 2^16, d = i - j: a quotient that is not on a border is 2^d / 2A > 2^(d-17)
+// from it, half a step of the quotient, which lies below 2^(8+d); the
+// corrected quotient is off by 2^-22 of a step before its rounding.)
+//
+// Bound by bytes.  A row stays in its block's registers between the sums and
+// the codes; sum and maximum of a row are joined in one exchange.
+#include "ple_8bit_launch.h"
+
+namespace ple {
+
+__device__ __forceinline__ void unpack8(u32x4 w, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+
+// What turns the products of a row into codes, from its sum of squares and largest product.
+struct RowScale {
+    float top, inv, scale;
+    bool bad;
+    __device__ __forceinline__ RowScale(float sum, float largest, const RmsNorm8Args& a) {
+        top = largest;
+        bad = !(sum < __builtin_inff()) || !(127.f * largest < __builtin_inff());
+        inv = bad || top == 0.f ? 0.f : 1.0f / top;
+        scale = bad ? __builtin_nanf("") : top * (1.0f / sqrtf(sum / (float)a.n + a.eps)) / 127.0f;
+    }
+    // the codes of four products, in a word
+    __device__ __forceinline__ uint32_t codes(float u0, float u1, float u2, float u3) const {
+        const uint32_t c0 = code(u0), c1 = code(u1), c2 = code(u2), c3 = code(u3);
+        return (c0 & 0xFFu) | (c1 & 0xFFu) << 8 | (c2 & 0xFFu) << 16 | c3 << 24;
+    }
+
+private:
+    __device__ __forceinline__ uint32_t code(float u) const {
+        const float t = 127.f * u;
+        float q = t * inv;
+        q = fmaf(fmaf(-q, top, t), inv, q);
+        return bad ? 0u : __float_as_uint(q + 12582912.0f);  // 1.5 * 2^23: the sum's last bits are the rounded quotient
+    }
+};
+
+// The wave's, then the block's sum and maximum.  A NaN among the values makes the sum NaN.
+template <int WAVES>
+__device__ __forceinline__ void join_row(float& sum, float& top) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+        sum += __shfl_xor(sum, d, kWave);
+        top = fmaxf(top, __shfl_xor(top, d, kWave));
+    }
+    if constexpr (WAVES > 1) {
+        __shared__ float sums[WAVES], tops[WAVES];
+        if ((threadIdx.x & 63) == 0) {
+            sums[threadIdx.x >> 6] = sum;
+            tops[threadIdx.x >> 6] = top;
+        }
+        __syncthreads();
+        sum = 0.f;
+        top = 0.f;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+            sum += sums[i];
+            top = fmaxf(top, tops[i]);
+        }
+    }
+}
+
+// WAVES waves a row, CH chunks of 8 elements a lane; one wave a row: four rows a block.
+template <int WAVES, int CH>
+__device__ __forceinline__ void norm_body(const RmsNorm8Args& a) {
+    constexpr int kThreads = WAVES * kWave;
+    const int tid = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t block = grid_block();
+    const int64_t t = WAVES == 1 ? block * 4 + (threadIdx.x >> 6) : block;
+    if (t >= a.T) return;  // (the whole block, where more waves than one share a row)
+    const int chunks = a.n / 8;
+    u32x4 x[CH], y[CH], w[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = i * kThreads + tid;
+        x[i] = y[i] = w[i] = u32x4{0u, 0u, 0u, 0u};
+        if (c >= chunks) continue;
+        x[i] = *(const u32x4*)(a.x + t * a.x_stride + c * 8);
+        if (a.residual != nullptr) y[i] = *(const u32x4*)(a.residual + t * a.n + c * 8);
+        w[i] = *(const u32x4*)(a.weight + c * 8);
+    }
+    float u[CH][8], sum = 0.f, top = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = i * kThreads + tid;
+        float g[8];
+        if (a.residual != nullptr) {
+            float r[8];
+            unpack8(x[i], u[i]);
+            unpack8(y[i], r);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i][e] = pack_bf16x2(u[i][2 * e] + r[2 * e], u[i][2 * e + 1] + r[2 * e + 1]);
+            if (c < chunks) *(u32x4*)(a.residual_out + t * a.n + c * 8) = x[i];
+        }
+        unpack8(x[i], u[i]);
+        unpack8(w[i], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            sum = fmaf(u[i][e], u[i][e], sum);
+            u[i][e] *= g[e];
+            top = fmaxf(top, fabsf(u[i][e]));
+        }
+    }
+    join_row<WAVES>(sum, top);
+    const RowScale s(sum, top, a);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = i * kThreads + tid;
+        if (c < chunks)
+            *(u32x2*)(a.codes + t * a.n + c * 8) =
+                u32x2{s.codes(u[i][0], u[i][1], u[i][2], u[i][3]), s.codes(u[i][4], u[i][5], u[i][6], u[i][7])};
+    }
+    if (tid == 0) a.scales[t] = s.scale;
+}
+
+// Rows that registers do not hold: the row is read again for its codes.
+constexpr int kLongThreads = 1024;
+__global__ __launch_bounds__(kLongThreads) void rms_norm8_long_kernel(RmsNorm8Args a) {
+    const int64_t t = grid_block();
+    if (t >= a.T) return;
+    const int chunks = a.n / 8;
+    const uint16_t* row = a.x + t * a.x_stride;
+    float sum = 0.f, top = 0.f;
+    for (int c = threadIdx.x; c < chunks; c += kLongThreads) {
+        float h[8], g[8];
+        u32x4 x = *(const u32x4*)(row + c * 8);
+        unpack8(x, h);
+        if (a.residual != nullptr) {
+            float r[8];
+            unpack8(*(const u32x4*)(a.residual + t * a.n + c * 8), r);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = pack_bf16x2(h[2 * e] + r[2 * e], h[2 * e + 1] + r[2 * e + 1]);
+            *(u32x4*)(a.residual_out + t * a.n + c * 8) = x;
+            unpack8(x, h);
+        }
+        unpack8(*(const u32x4*)(a.weight + c * 8), g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            sum = fmaf(h[e], h[e], sum);
+            top = fmaxf(top, fabsf(h[e] * g[e]));
+        }
+    }
+    join_row<kLongThreads / kWave>(sum, top);
+    const RowScale s(sum, top, a);
+    if (a.residual != nullptr) row = a.residual_out + t * a.n;  // (a lane reads what it wrote itself)
+    for (int c = threadIdx.x; c < chunks; c += kLongThreads) {
+        float h[8], g[8];
+        unpack8(*(const u32x4*)(row + c * 8), h);
+        unpack8(*(const u32x4*)(a.weight + c * 8), g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] *= g[e];
+        *(u32x2*)(a.codes + t * a.n + c * 8) = u32x2{s.codes(h[0], h[1], h[2], h[3]), s.codes(h[4], h[5], h[6], h[7])};
+    }
+    if (threadIdx.x == 0) a.scales[t] = s.scale;
+}
+
+// Waves a row, chunks a lane: rows of up to 512 elements a wave each, then four waves, up to 16384 eight.
+#define PLE_NORM_SHAPES(X) X(1, 1) X(4, 1) X(4, 2) X(4, 4) X(8, 4)
+#define PLE_NORM_KERNEL(WAVES, CH)                                                                                         \
+    __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * kWave) void rms_norm8_##WAVES##x##CH##_kernel(RmsNorm8Args a) { \
+        norm_body<WAVES, CH>(a);                                                                                           \
+    }
+PLE_NORM_SHAPES(PLE_NORM_KERNEL)
+#undef PLE_NORM_KERNEL
+
+hipError_t launch_rms_norm8(const RmsNorm8Args& a, hipStream_t s) {
+    const int chunks = a.n / 8;
+#define PLE_NORM_LAUNCH(WAVES, CH)                                                                                        \
+    if (chunks <= WAVES * kWave * CH) {                                                                                   \
+        const dim3 grid = block_grid(WAVES == 1 ? (a.T + 3) / 4 : a.T);                                                   \
+        hipLaunchKernelGGL(rms_norm8_##WAVES##x##CH##_kernel, grid, dim3(WAVES == 1 ? 256 : WAVES * kWave), 0, s, a);     \
+        return hipGetLastError();                                                                                         \
+    }
+    PLE_NORM_SHAPES(PLE_NORM_LAUNCH)
+#undef PLE_NORM_LAUNCH
+    hipLaunchKernelGGL(rms_norm8_long_kernel, block_grid(a.T), dim3(kLongThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace ple

@@ -172,10 +172,9 @@ def _out(name, t, shape, dtypes, cache, stream):
     return t
 
 
-def ple_kv4_append(cache: KV4Cache, k, v, query_start_loc, seq_lens, page_table, *, inv_freq=None,
-                   interleaved: bool = False, q=None, q_out=None, stream=None):
-    """New keys and values bf16 [T][heads][D] into the cache, keys (and q, if given) rotated by their positions over
-    the first 2 * len(inv_freq) elements.  Returns the rotated queries bf16 [T][q heads][D], or None without q."""
+def _append(name, cache, k, v, query_start_loc, seq_lens, page_table, inv_freq, interleaved, q, q_out, stream,
+            max_request_tokens=0):
+    """What the appends of the paged caches share; name: the library's call."""
     D, T, H = cache.head_dim, k.shape[0], cache.num_kv_heads
     ks, vs = _heads("k", k, T, H, cache), _heads("v", v, T, H, cache)
     qs = hq = rot = 0
@@ -191,51 +190,65 @@ def ple_kv4_append(cache: KV4Cache, k, v, query_start_loc, seq_lens, page_table,
         if inv_freq.get_device() != cache.device:
             _same_device(cache.tensors[0], inv_freq)
         rot, freq_at = 2 * inv_freq.shape[0], inv_freq.data_ptr()
-    b = _kv4_batch(cache, query_start_loc, seq_lens, page_table, T)
+    b = _kv4_batch(cache, query_start_loc, seq_lens, page_table, T, max_request_tokens)
     dev = cache.device
     if k.get_device() != dev or v.get_device() != dev or (q is not None and q.get_device() != dev):
         _same_device(cache.tensors[0], k, v, q)
-    rc = capi.load().ple_kv4_append(
+    rc = getattr(capi.load(), name)(
         ctypes.byref(cache.desc), ctypes.byref(b), k.data_ptr(), ks, v.data_ptr(), vs, q_at, qs, hq, out_at, freq_at,
         rot, 1 if interleaved else 0, _raw_stream(cache.device) if stream is None else _stream(stream))
     if rc:
-        capi.check(rc, "ple_kv4_append")
+        capi.check(rc, name)
     return q_out
 
 
-def ple_kv4_read(cache: KV4Cache, query_start_loc, seq_lens, page_table, num_tokens: int, *, k_out=None, v_out=None,
-                 stream=None):
-    """The new tokens' keys and values as the cache holds them: two bf16 [T][heads][D]."""
+def ple_kv4_append(cache: KV4Cache, k, v, query_start_loc, seq_lens, page_table, *, inv_freq=None,
+                   interleaved: bool = False, q=None, q_out=None, stream=None):
+    """New keys and values bf16 [T][heads][D] into the cache, keys (and q, if given) rotated by their positions over
+    the first 2 * len(inv_freq) elements.  Returns the rotated queries bf16 [T][q heads][D], or None without q."""
+    return _append("ple_kv4_append", cache, k, v, query_start_loc, seq_lens, page_table, inv_freq, interleaved, q, q_out,
+                   stream)
+
+
+def _read(name, cache, query_start_loc, seq_lens, page_table, num_tokens, k_out, v_out, stream):
     T = int(num_tokens)
     shape = (T, cache.num_kv_heads, cache.head_dim)
     k_out = _out("k_out", k_out, shape, _BF16, cache, stream)
     v_out = _out("v_out", v_out, shape, _BF16, cache, stream)
     b = _kv4_batch(cache, query_start_loc, seq_lens, page_table, T)
-    rc = capi.load().ple_kv4_read(ctypes.byref(cache.desc), ctypes.byref(b), _ptr(k_out), _ptr(v_out),
-                                  _raw_stream(cache.device) if stream is None else _stream(stream))
+    rc = getattr(capi.load(), name)(ctypes.byref(cache.desc), ctypes.byref(b), _ptr(k_out), _ptr(v_out),
+                                    _raw_stream(cache.device) if stream is None else _stream(stream))
     if rc:
-        capi.check(rc, "ple_kv4_read")
+        capi.check(rc, name)
     return k_out, v_out
+
+
+def ple_kv4_read(cache: KV4Cache, query_start_loc, seq_lens, page_table, num_tokens: int, *, k_out=None, v_out=None,
+                 stream=None):
+    """The new tokens' keys and values as the cache holds them: two bf16 [T][heads][D]."""
+    return _read("ple_kv4_read", cache, query_start_loc, seq_lens, page_table, num_tokens, k_out, v_out, stream)
+
+
+def _attention_workspace_bytes(name, cache, num_q_heads, num_tokens, num_reqs, table_width, window, max_request_tokens,
+                               max_seq_len) -> int:
+    any_ptr = cache.desc.k_codes  # sizes alone matter here
+    b = capi.ple_kv4_batch(any_ptr, any_ptr, any_ptr, int(num_tokens), int(num_reqs), int(table_width),
+                           min(int(max_request_tokens), _MOST), min(int(max_seq_len), _MOST))
+    return int(getattr(capi.load(), name + "_workspace_bytes")(int(num_q_heads), ctypes.byref(cache.desc), ctypes.byref(b),
+                                                               min(int(window), _MOST)))
 
 
 def ple_kv4_attention_workspace_bytes(cache: KV4Cache, num_q_heads: int, num_tokens: int, num_reqs: int,
                                       table_width: int, *, window: int = 0, max_request_tokens: int = 0,
                                       max_seq_len: int = 0) -> int:
     """Workspace of a call with these sizes and hints (0: none is needed)."""
-    any_ptr = cache.desc.k_codes  # sizes alone matter here
-    b = capi.ple_kv4_batch(any_ptr, any_ptr, any_ptr, int(num_tokens), int(num_reqs), int(table_width),
-                           min(int(max_request_tokens), _MOST), min(int(max_seq_len), _MOST))
-    return int(capi.load().ple_kv4_attention_workspace_bytes(int(num_q_heads), ctypes.byref(cache.desc),
-                                                             ctypes.byref(b), min(int(window), _MOST)))
+    return _attention_workspace_bytes("ple_kv4_attention", cache, num_q_heads, num_tokens, num_reqs, table_width, window,
+                                      max_request_tokens, max_seq_len)
 
 
-def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table, *, window: int = 0, scale=None,
-                      max_request_tokens: int = 0, max_seq_len: int = 0, want_lse: bool = False, out=None, lse=None,
-                      workspace=None, stream=None):
-    """Causal attention of the new tokens q bf16 [T][q heads][D] over the cache (their own keys appended before).
-    scale: 1/sqrt(D) if None.  window: tokens seen, the own one included (0: all).  max_request_tokens and
-    max_seq_len (0: unknown) let the call size its launch; pass them.  Returns (out bf16 [T][q heads][D], lse fp32
-    [T][q heads] or None)."""
+def _attention(name, q, cache, query_start_loc, seq_lens, page_table, window, scale, max_request_tokens, max_seq_len, want_lse,
+               out, lse, workspace, stream):
+    """What the attentions over the paged caches share; name: the library's call."""
     D, T, window = cache.head_dim, q.shape[0], min(window, _MOST)
     qs, hq = _heads("q", q, T, None, cache), q.shape[1]
     out = _out("out", out, (T, hq, D), _BF16, cache, stream)
@@ -245,7 +258,7 @@ def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table,
     if q.get_device() != cache.device:
         _same_device(cache.tensors[0], q)
     lib = capi.load()
-    need = int(lib.ple_kv4_attention_workspace_bytes(hq, ctypes.byref(cache.desc), ctypes.byref(b), window))
+    need = int(getattr(lib, name + "_workspace_bytes")(hq, ctypes.byref(cache.desc), ctypes.byref(b), window))
     if workspace is None:
         if need > 0:  # (given up on return, before the work has ended: taken in the order of the stream it runs on)
             if stream is None:
@@ -256,11 +269,22 @@ def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table,
     else:
         _req_bytes("workspace", workspace, need)
         _same_device(cache.tensors[0], workspace)
-    rc = lib.ple_kv4_attention(
+    rc = getattr(lib, name)(
         q.data_ptr(), qs, hq, ctypes.byref(cache.desc), ctypes.byref(b), window,
         D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse),
         None if workspace is None else _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
         _raw_stream(cache.device) if stream is None else _stream(stream))
     if rc:
-        capi.check(rc, "ple_kv4_attention")
+        capi.check(rc, name)
     return out, lse
+
+
+def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table, *, window: int = 0, scale=None,
+                      max_request_tokens: int = 0, max_seq_len: int = 0, want_lse: bool = False, out=None, lse=None,
+                      workspace=None, stream=None):
+    """Causal attention of the new tokens q bf16 [T][q heads][D] over the cache (their own keys appended before).
+    scale: 1/sqrt(D) if None.  window: tokens seen, the own one included (0: all).  max_request_tokens and
+    max_seq_len (0: unknown) let the call size its launch; pass them.  Returns (out bf16 [T][q heads][D], lse fp32
+    [T][q heads] or None)."""
+    return _attention("ple_kv4_attention", q, cache, query_start_loc, seq_lens, page_table, window, scale,
+                      max_request_tokens, max_seq_len, want_lse, out, lse, workspace, stream)
