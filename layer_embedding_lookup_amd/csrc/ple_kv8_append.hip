@@ -54,16 +54,32 @@ __device__ __forceinline__ Kv8Unit kv8_unit(const ple_kv8_cache& c, const ple_kv
         w.r = (int)(u / each);
         i = u - w.r * each;
     } else {
-        int lo = 0, hi = b.num_reqs - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (start(mid) / 16 + 2 * (int64_t)mid <= u)
-                lo = mid;
-            else
-                hi = mid - 1;
+        const auto number = [&](int64_t first, int r) { return min(max(first, (int64_t)0), T) / 16 + 2 * (int64_t)r; };
+        if (b.num_reqs <= 16 * kWave) {  // the wave counts the requests that begin at or before it: one round of loads
+            const int lane = threadIdx.x & 63;
+            int first[16], count = 0;
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                if (c * kWave < b.num_reqs) first[c] = b.query_start_loc[min(c * kWave + lane, b.num_reqs)];
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                if (c * kWave < b.num_reqs) {
+                    const int r = c * kWave + lane;
+                    count += (int)__popcll(__ballot(r < b.num_reqs && number(first[c], r) <= u));
+                }
+            w.r = max(count - 1, 0);
+        } else {
+            int lo = 0, hi = b.num_reqs - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (number(b.query_start_loc[mid], mid) <= u)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            w.r = lo;
         }
-        w.r = lo;
-        i = u - (start(lo) / 16 + 2 * (int64_t)lo);
+        i = u - number(b.query_start_loc[w.r], w.r);
     }
     // (by the whole length and all of the request's tokens, as kv4_position)
     const int64_t q0 = start(w.r), to = b.query_start_loc[w.r + 1], n = max(min(to, T) - q0, (int64_t)0);
@@ -78,6 +94,16 @@ __device__ __forceinline__ Kv8Unit kv8_unit(const ple_kv8_cache& c, const ple_kv
     w.first = q0 + (p0 - before);
     w.group = w.any ? kv4_group(c, b.page_table + (int64_t)w.r * b.table_width, 0, w.block) : -1;
     return w;
+}
+
+// kv4_position with the request found by the whole wave in one round of loads.
+__device__ __forceinline__ int kv8_position(const ple_kv8_cache& c, const ple_kv8_batch& b, int64_t t) {
+    int r;
+    int64_t start;
+    wave_find_request(b.query_start_loc, b.num_reqs, t, t, 1, 0, threadIdx.x & 63, r, start);
+    const int64_t from = b.query_start_loc[r], to = b.query_start_loc[r + 1];
+    const int64_t p = (int64_t)b.seq_lens[r] - (to - t);
+    return t < from || t >= to || p < 0 || p >= (int64_t)b.table_width * c.page_size ? -1 : (int)p;
 }
 
 // The least power of two s with top <= 448 s, within the cache's range; top >= 0 and finite.
@@ -262,8 +288,7 @@ __device__ __forceinline__ void append_body(const Kv8AppendArgs& a, int64_t unit
     }
     const int64_t t = id - units * parts;
     if (t >= a.batch.num_tokens || a.num_q_heads == 0) return;
-    int r;
-    const int pos = kv4_position(a.cache, a.batch, t, r);
+    const int pos = kv8_position(a.cache, a.batch, t);
     for (int i = threadIdx.x; i < half; i += kAppendThreads) {
         double sn, cs;
         sincos((double)(pos < 0 ? 0 : pos) * (double)a.inv_freq[i], &sn, &cs);
@@ -336,8 +361,7 @@ __device__ __forceinline__ void read_body(const Kv8ReadArgs& a) {
     if (id >= a.units * a.parts) {  // a block per token: those of no request and of no place in the table
         const int64_t t = id - a.units * a.parts;
         if (t >= T) return;
-        int r;
-        if (kv4_position(a.cache, a.batch, t, r) >= 0) return;
+        if (kv8_position(a.cache, a.batch, t) >= 0) return;
         const int row = a.cache.num_kv_heads * D;
         for (int e = threadIdx.x * 8; e < row; e += kAppendThreads * 8)
             *(u32x4*)(a.k_out + t * row + e) = *(u32x4*)(a.v_out + t * row + e) = u32x4{0u, 0u, 0u, 0u};

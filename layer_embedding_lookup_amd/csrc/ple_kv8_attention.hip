@@ -161,13 +161,15 @@ __device__ __forceinline__ void kv8_softmax(f32x4 (&s)[MT][4], const BlockScales
 }
 
 // NaN elements of values in a tile that some row does not see as a whole would reach that row too, as 0 * NaN.  There they
-// enter the product as zeros, LDS keeps which they were (a bit a token of each lane's codes, [element block][lane]), and
-// the rows that do see one are found by a product of ones for NaN elements and ones for seen tokens.
+// enter the product as zeros, and if there were any, the tiles are gone through once more at the end for the rows that do
+// see one.
 
-// Value codes of a lane's block: those of tokens outside [lo, hi), which may be anything, are cleared.  Returns whether the
-// wave has NaN among the others; they are cleared too then, and noted.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u; }
+
+// Value codes of a lane's block without those of tokens outside [lo, hi), which may be anything, and without NaN.  Returns
+// whether the lane had NaN among the others.
 template <int NB>
-__device__ __forceinline__ bool kv8_clear(u32x4 (&v)[NB], bool bad, int tg, int lo, int hi, uint16_t* noted) {
+__device__ __forceinline__ bool kv8_clear(u32x4 (&v)[NB], bool bad, int tg, int lo, int hi) {
     uint32_t keep[4], found = 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -178,53 +180,51 @@ __device__ __forceinline__ bool kv8_clear(u32x4 (&v)[NB], bool bad, int tg, int 
             if (!bad && tok >= lo && tok < hi) keep[i] |= 0xFFu << (8 * e);
         }
     }
-    const auto nans = [](uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u; };
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[b][i] &= keep[i];
-            found |= nans(v[b][i]);
+            const uint32_t x = v[b][i] & keep[i], is = nan_codes(x);
+            v[b][i] = x & ~(is * 0xFFu);
+            found |= is;
         }
-    if (__ballot(found != 0u) == 0) return false;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        uint32_t bits = 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t is = nans(v[b][i]);
-            bits |= (is * 0x10204080u >> 28) << (4 * i);  // bits 0, 8, 16 and 24 side by side
-            v[b][i] &= ~(is * 0xFFu);
-        }
-        noted[b * 64] = (uint16_t)bits;
-    }
-    return true;
+    return found != 0u;
 }
 
-// The elements (bit 4 b + e) of the lane's rows that a noted NaN reaches.
-template <int NB, int MT>
-__device__ __forceinline__ void kv8_see_nans(const uint16_t* noted, int tg, const int (&see_lo)[MT], const int (&see_hi)[MT],
-                                             uint64_t (&nan)[MT]) {
+// The elements (bit 4 b + e: 16 b + 4 g + e) of the lane's rows that a NaN reaches, among the tiles at from, from + step ..
+// below end: a product of ones for NaN elements and ones for seen tokens.
+template <int D, int MT>
+__device__ __forceinline__ void kv8_find_nans(const Kv8AttentionArgs& a, const int32_t* table_row, int head, int from, int step,
+                                              int end, const int (&see_lo)[MT], const int (&see_hi)[MT], uint64_t (&nan)[MT]) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    for (int t0 = from; t0 < end; t0 += step) {
+        const int tg = t0 + 16 * g;
+        const int64_t grp = tg < end ? kv4_group(a.cache, table_row, head, tg >> 4) : -1;
 #pragma unroll 1
-    for (int b = 0; b < NB; ++b) {
-        const uint32_t bits = noted[b * 64];
+        for (int b = 0; b < D / 16; ++b) {
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (grp >= 0) v = *(const u32x4*)(a.cache.v_codes + grp * (16 * D) + (b * 16 + n) * 16);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            f32x4 count = {0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 4; ++i) v[i] = nan_codes(v[i]);
+            if (__ballot((v[0] | v[1] | v[2] | v[3]) != 0u) == 0) continue;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                Frag is, sees;
+            for (int mt = 0; mt < MT; ++mt) {
+                f32x4 count = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int tok = tg + 8 * h + e;
-                    is.v[e] = (_Float16)(bits >> (8 * h + e) & 1u ? 1.f : 0.f);
-                    sees.v[e] = (_Float16)(tok >= see_lo[mt] && tok < see_hi[mt] ? 1.f : 0.f);
+                for (int h = 0; h < 2; ++h) {
+                    Frag is, sees;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int tok = tg + 8 * h + e;
+                        is.v[e] = (_Float16)(v[2 * h + e / 4] >> (8 * (e % 4)) & 1u ? 1.f : 0.f);
+                        sees.v[e] = (_Float16)(tok >= see_lo[mt] && tok < see_hi[mt] ? 1.f : 0.f);
+                    }
+                    count = __builtin_amdgcn_mfma_f32_16x16x32_f16(is.v, sees.v, count, 0, 0, 0);
                 }
-                count = __builtin_amdgcn_mfma_f32_16x16x32_f16(is.v, sees.v, count, 0, 0, 0);
-            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (count[e] > 0.f) nan[mt] |= (uint64_t)1 << (4 * b + e);
+                for (int e = 0; e < 4; ++e)
+                    if (count[e] > 0.f) nan[mt] |= (uint64_t)1 << (4 * b + e);
+            }
         }
     }
 }
@@ -246,8 +246,7 @@ template <int D, int WAVES>
 struct Kv8Shape {
     static constexpr int KS = D / 32;  // k-steps of the first product
     static constexpr int NB = D / 16;  // element blocks
-    static constexpr int LDS = kAttnWaves * 16 * kJoinRow<D> * 4;  // the join's, and before it the waves' notes
-    static_assert(WAVES * NB * 128 <= LDS, "a bit per code of a tile");
+    static constexpr int LDS = kAttnWaves * 16 * kJoinRow<D> * 4;  // the join's
 };
 
 // Few rows: the waves of a block take the tiles of a cache range in turn and join through LDS.  The next tile is on its
@@ -265,7 +264,7 @@ __device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
     if (!attn_tile(a, tile, w)) return;
     const int splits = attn_splits(a, w);
     if (split >= splits) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int begin = w.lo + split * a.chunk;
     const int end = split == splits - 1 ? w.hi : min(w.hi, begin + a.chunk);
@@ -273,8 +272,7 @@ __device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
 
     f32x4 o[MT][Sh::NB];
     float m[MT], l[MT];
-    uint64_t nan[MT] = {};
-    bool wide = false;
+    bool wide = false, nans = false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         m[mt] = -__builtin_inff();
@@ -284,34 +282,37 @@ __device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
     }
 
     const int32_t* table_row = a.batch.page_table + (int64_t)r * a.batch.table_width;
-    uint16_t* const noted = (uint16_t*)lds + wave * (Sh::NB * 64) + lane;
     bool bad_next = false;
     u32x4 kraw[4][D / 64], vraw[Sh::NB];
     float ks, vs;
     const int first = begin + wave * kTile;
     PageWalk walk(a, table_row, head, first + 16 * g, WAVES * kTile / 16, end);
-    auto load = [&](int t0) {
+    int64_t block = 0;  // of the tile whose keys are on their way: this lane's
+    auto load_keys = [&](int t0) {
         const int grp = walk.number(t0 + 16 * g, end);
         walk.fetch();
         bad_next = grp < 0;
-        const int64_t safe = grp < 0 ? 0 : grp;
+        block = grp < 0 ? 0 : grp;
         // (a block that no token was written to may have any scale)
-        ks = grp < 0 ? 1.f : a.cache.k_scales[safe];
-        vs = grp < 0 ? 1.f : a.cache.v_scales[safe];
+        ks = grp < 0 ? 1.f : a.cache.k_scales[block];
+        vs = grp < 0 ? 1.f : a.cache.v_scales[block];
         // keys: block n / 4, token 4 i + n % 4
-        const int64_t kg = __shfl((int)safe, (n >> 2) * 16, kWave);
+        const int64_t kg = __shfl((int)block, (n >> 2) * 16, kWave);
         const uint8_t* kc = a.cache.k_codes + kg * (16 * D) + g * (D / 64) * 256 + (n & 3) * 16;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) kraw[i][c] = *(const u32x4*)(kc + c * 256 + i * 64);
-        const uint8_t* vc = a.cache.v_codes + safe * (16 * D) + n * 16;
+    };
+    auto load_values = [&]() {
+        const uint8_t* vc = a.cache.v_codes + block * (16 * D) + n * 16;
 #pragma unroll
         for (int b = 0; b < Sh::NB; ++b) vraw[b] = *(const u32x4*)(vc + b * 256);
     };
     if (first < end) {
         walk.fetch();
-        load(first);
+        load_keys(first);
+        load_values();
     }
     BFrag q[MT][Sh::KS];
     int see_lo[MT], see_hi[MT];
@@ -335,11 +336,10 @@ __device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
                 for (int k = 0; k < Sh::KS; ++k)
                     s[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[k].v, q[mt][k].v, s[mt][i], 0, 0, 0);
             }
+            __builtin_amdgcn_sched_barrier(0);  // (dequantised keys of one MFMA at a time: registers)
         }
-        u32x4 v[Sh::NB];
-#pragma unroll
-        for (int b = 0; b < Sh::NB; ++b) v[b] = vraw[b];
-        if (t0 + WAVES * kTile < end) load(t0 + WAVES * kTile);
+        const bool more = t0 + WAVES * kTile < end;
+        if (more) load_keys(t0 + WAVES * kTile);
 
         // a tile that not every row sees as a whole
         bool every = t0 >= w.first_seen && t0 + kTile <= end && __ballot(bad) == 0;
@@ -351,19 +351,26 @@ __device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
         for (int mt = 0; mt < MT; ++mt)  // (one after the other: fewer registers than all of them together)
             kv8_softmax<Sh::NB, 1>((f32x4(&)[1][4])s[mt], c, some, bad, tg, (int(&)[1])see_lo[mt], (int(&)[1])see_hi[mt],
                                    (float(&)[1])m[mt], (float(&)[1])l[mt], (f32x4(&)[1][Sh::NB])o[mt], wide, (Frag(&)[1][2])p[mt]);
-        if (some && kv8_clear<Sh::NB>(v, bad, tg, w.first_seen, end, noted)) kv8_see_nans<Sh::NB>(noted, tg, see_lo, see_hi, nan);
+        if (some) nans |= __ballot(kv8_clear<Sh::NB>(vraw, bad, tg, w.first_seen, end)) != 0;
 #pragma unroll
-        for (int b = 0; b < Sh::NB; ++b)
+        for (int b = 0; b < Sh::NB; ++b) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 Frag f;
-                fp8_to_f16(v[b][2 * h], v[b][2 * h + 1], f);
+                fp8_to_f16(vraw[b][2 * h], vraw[b][2 * h + 1], f);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
                     o[mt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.v, p[mt][h].v, o[mt][b], 0, 0, 0);
             }
+            if (b % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+        }
+        if (more) load_values();
     }
-    kv8_give_nans<Sh::NB>(nan, o);
+    if (nans) {
+        uint64_t nan[MT] = {};
+        kv8_find_nans<D, MT>(a, table_row, head, first, WAVES * kTile, end, see_lo, see_hi, nan);
+        kv8_give_nans<Sh::NB>(nan, o);
+    }
     const uint32_t none[MT] = {};
     attn_join_waves<D, MT, WAVES>(a, w, head, split, splits, lds, m, l, o, none);
 }
@@ -371,7 +378,7 @@ __device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
 // D, row tiles, waves, waves per SIMD that registers allow
 #define PLE_ATTN_SHAPES(X)                                                                                        \
     X(64, 1, 4, 3) X(64, 1, 8, 2) X(64, 2, 4, 2) X(64, 2, 8, 2) X(128, 1, 4, 2) X(128, 1, 8, 2) X(128, 2, 4, 2) \
-    X(128, 2, 8, 2) X(256, 1, 4, 1) X(256, 1, 8, 2)
+    X(128, 2, 8, 2) X(256, 1, 4, 1)
 #define PLE_ATTN_KERNEL(D, MT, WAVES, OCC)                                                                                  \
     __global__ __launch_bounds__(WAVES * kWave, OCC) void kv8_attention_##D##_##MT##x##WAVES##_kernel(Kv8AttentionArgs a) { \
         kv8_body<D, MT, WAVES>(a);                                                                                          \
@@ -392,9 +399,8 @@ struct Kv8ChunkShape {
     static constexpr int KS = D / 32, NB = D / 16, WB = D / 64;  // WB: element blocks that a wave dequantises
     static constexpr int K_BYTES = 4 * KS * 1024, V_BYTES = NB * 2 * 1024;
     static constexpr int BUF = K_BYTES + V_BYTES;
-    static constexpr int NOTES_AT = 2 * BUF, NOTES = NB * 128;         // NaN values of a tile, and whether there are any
-    static constexpr int ANY_AT = NOTES_AT + 2 * NOTES;
-    static constexpr int LDS = ANY_AT + 2 * kAttnWaves * 4;
+    static constexpr int NANS_AT = 2 * BUF;  // whether some wave has met NaN values
+    static constexpr int LDS = NANS_AT + 16;
 };
 
 // Rows [w.row0, w.row1) against the cache's tokens [begin, end).  Results go to the call's outputs (at < 0), or to the
@@ -452,8 +458,7 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
     kv8_queries<D, MT>(a, w, w.row0 + wave * (16 * MT), head, begin, end, q, see_lo, see_hi);
     f32x4 o[MT][Sh::NB];
     float m[MT], l[MT];
-    uint64_t nan[MT] = {};
-    bool wide = false;
+    bool wide = false, nans = false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         m[mt] = -__builtin_inff();
@@ -476,12 +481,7 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
             *(bf16x8*)(kb + k * 1024) = f.v;
         }
         if (partial(t0, bad_next)) {
-            uint16_t* const noted = (uint16_t*)(lds + Sh::NOTES_AT + buf * Sh::NOTES) + wave * (Sh::WB * 64) + lane;
-            const bool nans = kv8_clear<Sh::WB>(vraw, bad_next, t0 + 16 * g, w.first_seen, end, noted);
-            if (!nans)
-#pragma unroll
-                for (int b = 0; b < Sh::WB; ++b) noted[b * 64] = 0;  // (another wave's may be looked through)
-            if (lane == 0) *(int*)(lds + Sh::ANY_AT + (buf * kAttnWaves + wave) * 4) = nans;
+            nans |= kv8_clear<Sh::WB>(vraw, bad_next, t0 + 16 * g, w.first_seen, end);
         }
 #pragma unroll
         for (int b = 0; b < Sh::WB; ++b)
@@ -495,10 +495,13 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
 
     bool bad = false;
     BlockScales c = {};
+    if (threadIdx.x == 0) *(volatile int*)(lds + Sh::NANS_AT) = 0;
     if (begin < end) {
         fill(begin, 0);
         bad = bad_next;
         c.set(base, ks, vs);
+    } else {
+        __syncthreads();
     }
     int buf = 0;
     for (int t0 = begin; t0 < end; t0 += kTile, buf ^= 1) {
@@ -535,14 +538,6 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
                     o[mt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[mt][h].v, o[mt][b], 0, 0, 0);
             }
         reads_ahead<2 * Sh::NB, MT>();
-        if (some) {
-            int any = 0;
-#pragma unroll
-            for (int k = 0; k < kAttnWaves; ++k) any |= *(const int*)(lds + Sh::ANY_AT + (buf * kAttnWaves + k) * 4);
-            if (any != 0)
-                kv8_see_nans<Sh::NB>((const uint16_t*)(lds + Sh::NOTES_AT + buf * Sh::NOTES) + lane, t0 + 16 * g, see_lo,
-                                     see_hi, nan);
-        }
         if (more) {
             fill(t0 + kTile, buf ^ 1);
             bad = bad_next;
@@ -550,7 +545,14 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
         }
     }
 
-    kv8_give_nans<Sh::NB>(nan, o);
+    // (a wave has met its quarter of the elements alone)
+    if (nans) *(volatile int*)(lds + Sh::NANS_AT) = 1;
+    __syncthreads();
+    if (*(volatile int*)(lds + Sh::NANS_AT) != 0) {
+        uint64_t nan[MT] = {};
+        kv8_find_nans<D, MT>(a, table_row, head, begin, kTile, end, see_lo, see_hi, nan);
+        kv8_give_nans<Sh::NB>(nan, o);
+    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         float total = l[mt];
@@ -630,14 +632,14 @@ void plan_kv8_attention(Kv8AttentionArgs& a) {
         a.splits = 1;
         return;
     }
-    a.waves = blocks <= 256 && a.rows < kChunkRows ? 8 : 4;
-    const int64_t slots = a.waves == 8 ? 256 : (a.rows == 16 && a.cache.head_dim == 64 ? 768 : 512);
+    a.waves = blocks <= 256 && a.rows < kChunkRows && a.cache.head_dim < 256 ? 8 : 4;
+    const int64_t slots = a.waves == 8 || a.cache.head_dim == 256 ? 256 : (a.rows == 16 ? 1024 : 512);
     int64_t splits = blocks <= 0 || a.rows == kChunkRows ? 1 : slots / blocks;
     const int64_t most_splits = (len + 1023) / 1024;
     splits = splits < most_splits ? splits : most_splits;
     splits = splits < 1 ? 1 : (splits < kMostSplits - 1 ? splits : kMostSplits - 1);
     int64_t chunk = (len + splits - 1) / splits;
-    const int64_t round = a.rows == kChunkRows ? kTile : kTile * a.waves;  // what a block goes through at a time
+    const int64_t round = a.rows == kChunkRows || a.waves == 8 ? kTile : kTile * a.waves;
     chunk = (chunk + round - 1) / round * round;
     a.chunk = (int)chunk;
     // (a range starts at a multiple of 16, up to 15 tokens before the first that is seen; the last split takes those)

@@ -428,6 +428,19 @@ __device__ __forceinline__ void attn_join_body(const A& a) {
     const int64_t rows = a.batch.num_tokens * a.num_q_heads;
     const int64_t orow = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
     if (orow >= rows) return;
+    const float* lse = a.part + rows * a.splits * D + orow * a.splits;
+    const float* src = a.part + orow * a.splits * D + lane * E;
+    // The first splits' results come in while the row's request and its number of splits are found (those past it, not
+    // written by this call, are dropped again).
+    constexpr int kAhead = 8;
+    const float first_lse = lane < a.splits ? lse[lane] : 0.f;
+    float ahead[kAhead][E];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int s = (WAVES == 1 ? 0 : wave) + i * WAVES;
+#pragma unroll
+        for (int e = 0; e < E; ++e) ahead[i][e] = s < a.splits ? src[(int64_t)s * D + e] : 0.f;
+    }
     const int64_t t = orow / a.num_q_heads;
     const int hq = (int)(orow - t * a.num_q_heads), head = hq / a.group;
     int r;
@@ -440,18 +453,26 @@ __device__ __forceinline__ void attn_join_body(const A& a) {
     if (!attn_tile(a, row / a.rows, w)) return;
     const int splits = attn_splits(a, w);
     if (splits == 1) return;
-    const float* lse = a.part + rows * a.splits * D + orow * a.splits;
-    const float* src = a.part + orow * a.splits * D + lane * E;
-    float top = -__builtin_inff();
-    for (int s = lane; s < splits; s += kWave) top = fmaxf(top, lse[s]);
+    float top = lane < splits ? first_lse : -__builtin_inff();
+    for (int s = lane + kWave; s < splits; s += kWave) top = fmaxf(top, lse[s]);
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
     float total = 0.f, v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = 0.f;
+    const auto weight = [&](float l) { return l == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(l - top); };  // NaN stays
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int s = (WAVES == 1 ? 0 : wave) + i * WAVES;
+        if (s >= splits) break;
+        const float by = weight(__shfl(first_lse, s, kWave));
+        total += by;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = fmaf(ahead[i][e], by, v[e]);
+    }
 #pragma unroll 8
-    for (int s = WAVES == 1 ? 0 : wave; s < splits; s += WAVES) {
-        const float l = lse[s], by = l == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(l - top);  // NaN stays
+    for (int s = (WAVES == 1 ? 0 : wave) + kAhead * WAVES; s < splits; s += WAVES) {
+        const float by = weight(lse[s]);
         total += by;
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = fmaf(src[(int64_t)s * D + e], by, v[e]);
