@@ -38,10 +38,10 @@ struct W8Args {
     int32_t x_stride;
     uint16_t* out;
 };
-// The kernel of a call: few tokens (mt token tiles, nt feature tiles of 16 a block) or tiles of `block` tokens and features.
+// The kernel of a call.  block = 256: tiles of 256 x 256; 64: tiles of `rows` x `nt` blocks of 64 x 64; 0: few tokens, `rows`
+// rows of x and `nt` tiles of 16 features a block, `step` bytes of K a wave at a time.
 struct W8Shape {
-    int block;  // 0: few tokens
-    int mt, nt;
+    int block, rows, nt, step;
 };
 W8Shape w8_linear_shape(int64_t T, int32_t out_dim);
 hipError_t launch_w8_linear(const W8Args& a, hipStream_t s);

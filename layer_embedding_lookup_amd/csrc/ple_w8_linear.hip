@@ -1,19 +1,20 @@
 // Products of 8-bit integers: out = (x W^T) scaled by token and by output
 // channel, sums exact in 32-bit integers.
 //
-// Many tokens: the pipelines of the bf16 projection (ple_kv_proj.hip) with
-// 16x16x64 and 32x32x32 integer MFMAs, whose operands are 16 bytes of K per
-// lane as bf16's are: a slice of 128 bytes is 128 inputs, and tiles, copies,
-// LDS layout and the order of products are as there.  What differs: rows of x
-// may be strided, K may end inside a slice, O may be any number, and the
-// scales multiply the sums on the way out.  Bound by the products.
-//
-// Few tokens (decode): bound by reading the weights once, and below that by
-// the latency of the rounds of loads.  A block's eight waves share its
-// features (NT x 16) and split K between them in steps of 256 bytes; a step's
-// rows of inputs and weights come straight into LDS in whole rows, 1 KiB an
-// instruction, and go to the matrix cores from there.  The waves' sums are
-// joined through LDS: no second launch and no atomics.
+// Integer MFMAs take 16 bytes of K per lane, so a row of either operand is
+// read as it lies.  Three kinds of kernels, chosen in w8_linear_shape:
+//  - few tokens (decode): bound by reading the weights once, and below that
+//    by the latency of the rounds of loads.  A block's eight waves share its
+//    features and split K between them in steps; a step's rows come straight
+//    into LDS, whole rows of 128 or 256 bytes at a time, and the waves' sums
+//    are joined through LDS: no second launch and no atomics.
+//  - tiles of four waves for all in between, bound by the weights while 64 x
+//    64 tiles do (1 token, 4096 -> 8192: 8.6 us, 3.9 TB/s; 128 tokens 9.5;
+//    256 tokens 2048 -> 4096 7.2), then by LDS and the products.
+//  - 256 x 256 tiles of eight waves, the pipeline of the bf16 projection
+//    (ple_kv_proj.hip) on 16x16x64 products, where there are many: bound by
+//    the products (8192 tokens 4096 -> 8192: 219 us, 2.5 PFLOP/s, 50% of the
+//    dense peak; the library's product into 32-bit sums 238).
 #include "ple_8bit_launch.h"
 
 namespace ple {
@@ -55,74 +56,8 @@ __device__ __forceinline__ void tile_of_block(int bid, int tiles_m, int tiles_n,
     tn = in_group / gm;
 }
 
-// ---------------------------------------------------------------------------
-// Pipelined kernel body for batches too small to give 256 blocks of 256 x
-// 256: BT x BT block tile, 4 waves (one per SIMD), each a (BT/2) x (BT/2)
-// block held in accumulator tiles of 32 x 32.  For BT = 128 that is 4 tiles
-// and LDS stages of 32 KiB; for BT = 64, one tile and stages of 16 KiB.
-// K-slices of 64.
-//
-// Why this shape: the fragment reads of the next 16-deep K-step are spread
-// between the current step's MFMAs, so with one wave per SIMD the matrix core
-// stays fed without a second wave to cover for it; the narrow tiles give
-// blocks: a 1024-token batch gets 256 blocks of 128 x 128, a 256-token decode
-// batch 256 blocks of 64 x 64 (there the W panels, read by four blocks each
-// from the XCD's L2, bound the kernel, not the matrix cores).
-//
-// Operands go global -> LDS with buffer loads that write LDS directly
-// (buffer_load_dwordx4 ... lds): a scalar buffer resource per operand panel
-// and a 32-bit per-lane offset.  Each copy instruction fills 1 KiB = 8 whole
-// 128-byte K-slice rows, so every request is a full cache line.  The copies
-// of slice kt+2 go into the stage slice kt has just left: they start between
-// the last K-step's MFMAs of slice kt (after the barrier that ends every read
-// of that stage) and finish between the first K-step's MFMAs of slice kt+1,
-// and the barrier at the end of slice kt+1 waits for them.
-//
-// LDS layout of one operand slice: row r holds 8 chunks of 16 bytes (64
-// bf16 of K); chunk kc sits at position r*8 + (kc ^ ((r >> 1) & 7)).  A
-// fragment read takes one k-chunk of 32 consecutive rows; the LDS serves 16
-// lanes (256 bytes, 64 banks) per cycle and any 16 consecutive rows land on
-// distinct 16-byte bank groups.  The MFMA operands are swapped (W fragment
-// first) so each lane's accumulators are 4 consecutive output features of one
-// token, which the epilogue writes to LDS as 8-byte pairs before coalesced
-// 16-byte stores.
-//
-// The LDS fragment reads are inline assembly with explicit waits: the
-// compiler's own waits would drain every read in flight before each MFMA
-// group, which exposes the LDS latency on every K-step.  Each wait lists the
-// fragment registers it covers as operands, so no MFMA can be scheduled
-// above the wait for its inputs.
-// ---------------------------------------------------------------------------
-constexpr int kBigThreads = 256;
-constexpr int kSliceBytes = 128;  // of K: 64 bf16, 128 bytes of 8-bit codes
-constexpr int kNStage = 2;
-
-// Block tile BT x BT (256, or 128 / 64 for problems too small to fill the
-// chip with wider tiles); each of the 4 waves holds a (BT/2) x (BT/2) block
-// as NB x NB accumulator tiles of 32 x 32.
-template <int BT>
-struct W8PipeShape {
-    static constexpr int NB = BT / 64;                    // 32-row blocks per wave and operand
-    static constexpr int NCOPY = BT / 32;                 // copy instructions per operand, wave and slice
-    static constexpr int COPY_SPLIT = NCOPY / 2;          // of those, issued in a slice's last K-step (2 stages)
-    static constexpr int OP_BYTES = BT * kSliceBytes;     // one operand's slice
-    static constexpr int STAGE_BYTES = 2 * OP_BYTES;      // x + W slices
-    // LDS stages: the narrower tiles run fewer MFMAs per slice, so more
-    // slices are kept in flight to cover the copy latency (128 KiB each way)
-    static constexpr int NS = BT == 256 ? kNStage : (128 * 1024) / STAGE_BYTES;
-    static constexpr int OUT_ROW = BT + 8;                // epilogue row (elements)
-    static constexpr int LDS_BYTES = (NS * STAGE_BYTES > BT * OUT_ROW * 2) ? NS * STAGE_BYTES : BT * OUT_ROW * 2;
-    // copy instructions of one slice (both operands) per wave
-    static constexpr int SLICE_COPIES = 2 * NCOPY;
-    static_assert((NS & (NS - 1)) == 0 && (NS - 1) * SLICE_COPIES <= 63, "stages must fit the vmcnt counter");
-};
-
+constexpr int kSliceBytes = 128;  // of K
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
-
-// Wait for this wave's copies and LDS reads, then join the workgroup barrier.
-// The "memory" clobber keeps the compiler from moving LDS or global accesses
-// across it.
-#define PLE_WAIT_VM_BARRIER0() asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory")
 
 // The operands' rows in bytes.
 struct W8Rows {
@@ -132,285 +67,211 @@ struct W8Rows {
     __device__ __forceinline__ int x_bytes(int n) const { return (n - 1) * x + k; }
 };
 
-// A block's BT x BT outputs out of LDS.
-template <int BT, int THREADS>
-__device__ __forceinline__ void pipe_store(const uint16_t* Cs, int out_row, const W8Args& a, int m0, int n0) {
+// A block's BM x BN outputs out of LDS.
+template <int BM, int BN, int THREADS>
+__device__ __forceinline__ void pipe_store(const uint16_t* Cs, const W8Args& a, int m0, int n0) {
     const int M = a.M, O = a.O;
     const bool whole = O % 8 == 0;  // rows of `out` begin at 16 bytes
 #pragma unroll 4
-    for (int c = threadIdx.x; c < BT * BT / 8; c += THREADS) {
-        const int row = c / (BT / 8);  // BT/8 chunks of 8 features per row
-        const int col = (c % (BT / 8)) * 8;
+    for (int c = threadIdx.x; c < BM * BN / 8; c += THREADS) {
+        const int row = c / (BN / 8);  // BN/8 chunks of 8 features per row
+        const int col = (c % (BN / 8)) * 8;
         const int gr = m0 + row, gc = n0 + col;
         if (gr >= M || gc >= O) continue;
         if (whole) {
-            *(u32x4*)(a.out + (int64_t)gr * O + gc) = *(const u32x4*)(Cs + row * out_row + col);
+            *(u32x4*)(a.out + (int64_t)gr * O + gc) = *(const u32x4*)(Cs + row * (BN + 8) + col);
         } else {
-            for (int e = 0; e < 8 && gc + e < O; ++e) a.out[(int64_t)gr * O + gc + e] = Cs[row * out_row + col + e];
+            for (int e = 0; e < 8 && gc + e < O; ++e) a.out[(int64_t)gr * O + gc + e] = Cs[row * (BN + 8) + col + e];
         }
     }
 }
 
-template <int NB>
-struct W8Frag {
-    u32x4 a[NB], b[NB];  // x fragments of the token blocks, W fragments of the feature blocks
+// ---------------------------------------------------------------------------
+// Tiles of 64 MB tokens x 64 NB features, four waves (one per SIMD) of 32 MB x
+// 32 NB in 32x32x32 products.  K's slices of 128 go round a ring of NS in LDS.
+// A slice's fragments are read as a whole while the last one's products run,
+// so a slice costs one barrier and the reads' latency is behind the products;
+// NS slices are on their way from memory.  128 tokens 4096 -> 8192 in 64 x 64
+// tiles: 9.5 us (3.7 TB/s); reading each 32 of K for itself before its product
+// 18.5, eight waves that share K 9.9.  512 tokens in 128 x 128 tiles: 20.6 us,
+// 1.67 PFLOP/s, about 1400 cycles a slice where its products take 512 and LDS
+// is busy for 770 (64 fragment reads and 32 KiB of copies).
+//
+// Operands go global -> LDS with buffer loads that write LDS directly: a
+// scalar buffer resource per operand panel and a 32-bit per-lane offset.  Each
+// copy instruction fills 1 KiB = 8 whole rows of the slice, so every request
+// is a full cache line.  Row r holds 8 chunks of 16 bytes, chunk c at place
+// c ^ ((r >> 1) & 7): a fragment read takes one chunk of 32 consecutive rows,
+// and any 16 of them touch distinct banks.  W's fragment is the first operand,
+// so each lane's sums are 4 consecutive features of one token.
+//
+// The LDS reads are inline assembly with explicit waits (the compiler's own
+// would wait for the copies too); a wait names the registers it covers, so no
+// product reading them can be scheduled above it.  The loop has no branch
+// between a read and its wait but those that leave the fragments alone, so
+// that nothing copies a register on its way: slices past the last one are gone
+// through with x as zeros, and their copies are out of the buffer's range.
+// ---------------------------------------------------------------------------
+template <int MB, int NB, int NS>
+struct W8Tile {
+    static constexpr int BM = 64 * MB, BN = 64 * NB;
+    static constexpr int X_BYTES = BM * kSliceBytes, STAGE = X_BYTES + BN * kSliceBytes;
+    static constexpr int COPIES = 2 * MB + 2 * NB;  // of a wave and slice
+    static constexpr int FRAGS = 4 * (MB + NB);     // of a wave and slice: x blocks, then W blocks of each 32 of K
+    static constexpr int OUT = BM * (BN + 8) * 2;
+    static constexpr int LDS = NS * STAGE > OUT ? NS * STAGE : OUT;
+    static_assert(NS >= 2 && (NS - 1) * COPIES <= 63, "the slices on their way must fit the wait's counter");
+    static_assert(LDS <= 160 * 1024, "more LDS than a CU has");
 };
-// A wait names the fragment registers it covers, so no MFMA reading them can
-// be scheduled above it.
-#define PLE_W8_FRAG_REGS4(f) \
-    "+v"(f.a[0]), "+v"(f.a[1]), "+v"(f.a[2]), "+v"(f.a[3]), "+v"(f.b[0]), "+v"(f.b[1]), "+v"(f.b[2]), "+v"(f.b[3])
-#define PLE_W8_FRAG_REGS2(f) "+v"(f.a[0]), "+v"(f.a[1]), "+v"(f.b[0]), "+v"(f.b[1])
-#define PLE_W8_FRAG_REGS1(f) "+v"(f.a[0]), "+v"(f.b[0])
 
-template <int BT>
-__device__ __forceinline__ void w8_pipe(const W8Args& a) {
-    using P = W8PipeShape<BT>;
-    constexpr int NB = P::NB;
-    constexpr int WT = BT / 2;  // wave block
-    using Frag = W8Frag<NB>;
+constexpr int kTileThreads = 256;
+
+template <int OFFSET>
+__device__ __forceinline__ void read_lds(u32x4& f, uint32_t at) {
+    asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(f) : "v"(at), "i"(OFFSET));
+}
+#define PLE_W8_REGS4(f, i) "+v"(f[i]), "+v"(f[i + 1]), "+v"(f[i + 2]), "+v"(f[i + 3])
+// Names further fragments to a wait before it.
+template <int N>
+__device__ __forceinline__ void name_frags(u32x4 (&f)[N]) {
+    if constexpr (N == 12) asm volatile("" : PLE_W8_REGS4(f, 8));
+    if constexpr (N >= 16) asm volatile("" : PLE_W8_REGS4(f, 8), PLE_W8_REGS4(f, 12));
+    if constexpr (N == 24) asm volatile("" : PLE_W8_REGS4(f, 16), PLE_W8_REGS4(f, 20));
+    static_assert(N == 8 || N == 12 || N == 16 || N == 24, "fragments without a wait");
+}
+// Waits for these fragments and all copies but the newest V, then for the block's other waves.
+template <int V, int N>
+__device__ __forceinline__ void wait_slice(u32x4 (&f)[N]) {
+    asm volatile("s_waitcnt vmcnt(%8) lgkmcnt(0)\n\ts_barrier" : PLE_W8_REGS4(f, 0), PLE_W8_REGS4(f, 4) : "i"(V) : "memory");
+    name_frags(f);
+}
+
+template <int MB, int NB, int NS>
+__device__ __forceinline__ void w8_tile(const W8Args& a) {
+    using Sh = W8Tile<MB, NB, NS>;
+    constexpr int BM = Sh::BM, BN = Sh::BN, N = Sh::FRAGS;
     extern __shared__ __align__(16) char lds_raw[];
-    const int tid = threadIdx.x;
-    const int lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 1, wn = wave & 1;  // 2 x 2 waves: WT tokens x WT features each
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;  // 2 x 2 waves
     const int M = a.M, O = a.O;
     const W8Rows rows(a);
-
-    const int tiles_m = (M + BT - 1) / BT;
-    const int tiles_n = (O + BT - 1) / BT;
     int tm, tn;
-    tile_of_block<8>(blockIdx.x, tiles_m, tiles_n, tm, tn);
-    const int m0 = tm * BT, n0 = tn * BT;
+    tile_of_block<8>(blockIdx.x, (M + BM - 1) / BM, (O + BN - 1) / BN, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
 
-    // Copy instruction i (0..NCOPY-1) of wave `wave` fills rows g*8 .. g*8+7
-    // of an operand slice, g = i*4 + wave; lane L lands at position g*64 + L:
-    // row g*8 + L/8, chunk kc = (L & 7) ^ ((row >> 1) & 7).  Rows past the end
-    // of x or W read the last row (their outputs are never stored).
-    const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)((const char*)a.x + (int64_t)m0 * rows.x), (short)0, rows.x_bytes(min(M - m0, BT)), 0x00020000);
-    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)((const char*)a.w + (int64_t)n0 * rows.k), (short)0, min(O - n0, BT) * rows.k, 0x00020000);
-    uint32_t aoff[P::NCOPY], boff[P::NCOPY];
+    // Copy instruction i of a wave fills rows 8 (4 i + wave) .. + 7 of an operand's slice; rows past the end of x or W read
+    // the last row (their outputs are never stored).
+    const int x_bytes = rows.x_bytes(min(M - m0, BM)), w_bytes = min(O - n0, BN) * rows.k;
+    void* const x0 = (void*)((const char*)a.x + (int64_t)m0 * rows.x);
+    void* const w0 = (void*)((const char*)a.w + (int64_t)n0 * rows.k);
+    uint32_t xoff[2 * MB], woff[2 * NB];
 #pragma unroll
-    for (int i = 0; i < P::NCOPY; ++i) {
+    for (int i = 0; i < 2 * MB || i < 2 * NB; ++i) {
         const int row = (i * 4 + wave) * 8 + (lane >> 3);
         const int kc = (lane & 7) ^ ((row >> 1) & 7);
-        aoff[i] = (uint32_t)((min(m0 + row, M - 1) - m0) * rows.x + kc * 16);
-        boff[i] = (uint32_t)((min(n0 + row, O - 1) - n0) * rows.k + kc * 16);
+        if (i < 2 * MB) xoff[i] = (uint32_t)(min(row, M - 1 - m0) * rows.x + kc * 16);
+        if (i < 2 * NB) woff[i] = (uint32_t)(min(row, O - 1 - n0) * rows.k + kc * 16);
     }
     const int nk = rows.slices;
-    // copy instruction i of slice kt into stage kt % NS; slices past the end
-    // (the loop below is uniform) re-read the last slice into a stage that no
-    // later read uses
-    auto copy_one = [&](int kt, int i) {
-        char* base = lds_raw + (kt & (P::NS - 1)) * P::STAGE_BYTES;
-        const int g = i * 4 + wave;
-        const int ko = min(kt, nk - 1) * kSliceBytes;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr_t)(base + g * 1024), 16, aoff[i], ko, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr_t)(base + P::OP_BYTES + g * 1024), 16, boff[i], ko, 0,
-                                                 0);
+    // copy instruction c of slice s into a stage of the ring; slices past the last one copy nothing
+    auto copy_one = [&](int s, int stage, int c) {
+        char* base = lds_raw + stage * Sh::STAGE;
+        const bool in = s < nk;
+        const __amdgpu_buffer_rsrc_t r = c < 2 * MB ? __builtin_amdgcn_make_buffer_rsrc(x0, (short)0, in ? x_bytes : 0, 0x00020000)
+                                                    : __builtin_amdgcn_make_buffer_rsrc(w0, (short)0, in ? w_bytes : 0, 0x00020000);
+        const int i = c < 2 * MB ? c : c - 2 * MB;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(base + (c < 2 * MB ? 0 : Sh::X_BYTES) + (i * 4 + wave) * 1024), 16,
+                                                 c < 2 * MB ? xoff[i < 2 * MB ? i : 0] : woff[i < 2 * NB ? i : 0],
+                                                 in ? s * kSliceBytes : 0, 0, 0);
     };
 
-    i32x16 acc[NB][NB];  // [W block j][x block i]
+    i32x16 acc[NB][MB];
 #pragma unroll
     for (int j = 0; j < NB; ++j)
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[j][i][e] = 0;
 
-    const int frow = lane & 31;
-    const int fk = lane >> 5;
-    const int sw = (frow >> 1) & 7;  // the chunk swizzle, the same for every 32-row block
-    // LDS byte address of this lane's fragment chunk for K-step kk in stage 0,
-    // first 32-row block (the others are +4096 bytes each)
-    uint32_t a_addr[4], b_addr[4];
+    const int frow = lane & 31, fk = lane >> 5;
+    uint32_t x_at[4], w_at[4];  // of the lane's chunk for step kk in stage 0, first 32-row block (the others 4 KiB on each)
     const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds_raw;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-        const uint32_t col = (uint32_t)(((kk * 2 + fk) ^ sw) * 16);
-        a_addr[kk] = lds_base + (wm * WT + frow) * 128 + col;
-        b_addr[kk] = lds_base + P::OP_BYTES + (wn * WT + frow) * 128 + col;
+        const uint32_t col = (uint32_t)(((kk * 2 + fk) ^ ((frow >> 1) & 7)) * 16);
+        x_at[kk] = lds_base + (wm * (32 * MB) + frow) * kSliceBytes + col;
+        w_at[kk] = lds_base + Sh::X_BYTES + (wn * (32 * NB) + frow) * kSliceBytes + col;
     }
-    // fragment read q (0..2*NB-1) of K-step kk of slice kt: x blocks, then W blocks
-    auto read_one = [&](int q, int kt, int kk, Frag& f) {
-        const uint32_t so = (uint32_t)(kt & (P::NS - 1)) * P::STAGE_BYTES;
-        const uint32_t pa = a_addr[kk] + so, pb = b_addr[kk] + so;
-        if constexpr (NB == 4) {
-            switch (q) {
-                case 0: asm volatile("ds_read_b128 %0, %1" : "=v"(f.a[0]) : "v"(pa)); break;
-                case 1: asm volatile("ds_read_b128 %0, %1 offset:4096" : "=v"(f.a[1]) : "v"(pa)); break;
-                case 2: asm volatile("ds_read_b128 %0, %1 offset:8192" : "=v"(f.a[2]) : "v"(pa)); break;
-                case 3: asm volatile("ds_read_b128 %0, %1 offset:12288" : "=v"(f.a[3]) : "v"(pa)); break;
-                case 4: asm volatile("ds_read_b128 %0, %1" : "=v"(f.b[0]) : "v"(pb)); break;
-                case 5: asm volatile("ds_read_b128 %0, %1 offset:4096" : "=v"(f.b[1]) : "v"(pb)); break;
-                case 6: asm volatile("ds_read_b128 %0, %1 offset:8192" : "=v"(f.b[2]) : "v"(pb)); break;
-                default: asm volatile("ds_read_b128 %0, %1 offset:12288" : "=v"(f.b[3]) : "v"(pb)); break;
-            }
-        } else if constexpr (NB == 2) {
-            switch (q) {
-                case 0: asm volatile("ds_read_b128 %0, %1" : "=v"(f.a[0]) : "v"(pa)); break;
-                case 1: asm volatile("ds_read_b128 %0, %1 offset:4096" : "=v"(f.a[1]) : "v"(pa)); break;
-                case 2: asm volatile("ds_read_b128 %0, %1" : "=v"(f.b[0]) : "v"(pb)); break;
-                default: asm volatile("ds_read_b128 %0, %1 offset:4096" : "=v"(f.b[1]) : "v"(pb)); break;
-            }
-        } else {
-            if (q == 0)
-                asm volatile("ds_read_b128 %0, %1" : "=v"(f.a[0]) : "v"(pa));
-            else
-                asm volatile("ds_read_b128 %0, %1" : "=v"(f.b[0]) : "v"(pb));
+    // fragment q of a slice: step q / (MB + NB); x blocks, then W blocks
+    auto read_one = [&](int q, uint32_t stage, u32x4 (&f)[N]) {
+        const int kk = q / (MB + NB), b = q % (MB + NB);
+        const uint32_t at = (b < MB ? x_at[kk] : w_at[kk]) + stage;
+        switch (b < MB ? b : b - MB) {
+            case 0: read_lds<0>(f[q], at); break;
+            case 1: read_lds<4096>(f[q], at); break;
+            case 2: read_lds<8192>(f[q], at); break;
+            default: read_lds<12288>(f[q], at); break;
         }
     };
-    auto wait_frag = [&](Frag& f) {
-        if constexpr (NB == 4)
-            asm volatile("s_waitcnt lgkmcnt(0)" : PLE_W8_FRAG_REGS4(f));
-        else if constexpr (NB == 2)
-            asm volatile("s_waitcnt lgkmcnt(0)" : PLE_W8_FRAG_REGS2(f));
-        else
-            asm volatile("s_waitcnt lgkmcnt(0)" : PLE_W8_FRAG_REGS1(f));
-    };
-    // the barrier of an NS-stage slice: this wave's copies of every slice but
-    // the next NS-2 have landed
-    auto wait_barrier_vm = [&](Frag& f) {
-        constexpr int V = (P::NS - 2) * P::SLICE_COPIES;
-        if constexpr (NB == 2)
-            asm volatile("s_waitcnt vmcnt(%4) lgkmcnt(0)\n\ts_barrier" : PLE_W8_FRAG_REGS2(f) : "i"(V) : "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(%2) lgkmcnt(0)\n\ts_barrier" : PLE_W8_FRAG_REGS1(f) : "i"(V) : "memory");
-    };
-    auto wait_barrier = [&](Frag& f) {
-        if constexpr (NB == 4)
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : PLE_W8_FRAG_REGS4(f) : : "memory");
-        else if constexpr (NB == 2)
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : PLE_W8_FRAG_REGS2(f) : : "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : PLE_W8_FRAG_REGS1(f) : : "memory");
-    };
-    // One K-step: NB*NB MFMAs on `cur`.  After MFMA t < 2*NB comes fragment
-    // read t of (rkt, rkk) into `nxt`, and copy instructions [c0, c1) of slice
-    // ckt are spread over the MFMAs.  The order is pinned.
-    auto kstep = [&](const Frag& cur, Frag& nxt, int rkt, int rkk, int ckt, int c0, int c1) {
-        constexpr int NT = NB * NB;
-        const int nc = c1 - c0;
+    // Slice s: cur's products; between them the reads of the next slice into nxt, and the copies of the NS-th after this one
+    // into the stage that this one has left.
+    auto slice = [&](int s, int stage, int next, u32x4 (&cur)[N], u32x4 (&nxt)[N]) {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_slice<(NS - 2) * Sh::COPIES>(cur);
+        __builtin_amdgcn_sched_barrier(0);
+        if ((s + 1) * kSliceBytes > a.K) {  // past K x is zero (W holds the next row's there, the ring anything)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int j = t / NB, i = t % NB;
-            acc[j][i] = mfma32(cur.b[j], cur.a[i], acc[j][i]);
-            if (rkk >= 0) {
-                if constexpr (2 * NB <= NT) {
-                    if (t < 2 * NB) read_one(t, rkt, rkk, nxt);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 2 * NB; ++q) read_one(q, rkt, rkk, nxt);  // NT == 1
-                }
-            }
-            if (nc > 0 && nc <= NT && (t * nc) % NT < nc) copy_one(ckt, c0 + (t * nc) / NT);
-            if (nc > NT)
-#pragma unroll
-                for (int c = (t * nc) / NT; c < ((t + 1) * nc) / NT; ++c) copy_one(ckt, c0 + c);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int q = 0; q < N; ++q)
+                if (q % (MB + NB) < MB)
+                    cur[q] &= s * kSliceBytes + (q / (MB + NB) * 2 + fk) * 16 < a.K ? 0xFFFFFFFFu : 0u;
         }
-    };
-    // a last slice that K ends in: x past K becomes zero (W holds the next row's there)
-    auto trim = [&](Frag& f, int kt, int kk) {
-        if (kt == nk - 1 && rows.tail != 0) {
-            const uint32_t keep = (kk * 2 + fk) * 16 < rows.tail ? 0xFFFFFFFFu : 0u;
+        constexpr int P = 4 * MB * NB;          // products
+        constexpr int R = P >= 4 ? P * 3 / 4 : P;  // the reads go behind the first of them, the copies behind all
 #pragma unroll
-            for (int i = 0; i < NB; ++i) f.a[i] &= keep;
-        }
-    };
-    // One slice.  On entry f0 is receiving K-step 0 of slice kt.  LDS reads
-    // return in order, so when a K-step starts, the reads issued during the
-    // previous one are the only ones in flight and waiting for all of them
-    // covers its fragments.  The first K-step finishes the copies of slice
-    // kt+1 that slice kt-1 began; the last begins those of slice kt+2, into
-    // the stage this slice has just left.  The last slice's look-ahead reads
-    // and copies land in the other stage and are never used.
-    auto slice = [&](int kt, Frag& f0, Frag& f1) {
-        if constexpr (P::NS == 2) {
-            wait_frag(f0);
-            trim(f0, kt, 0);
-            kstep(f0, f1, kt, 1, kt + 1, P::COPY_SPLIT, P::NCOPY);
-            wait_frag(f1);
-            trim(f1, kt, 1);
-            kstep(f1, f0, kt, 2, 0, 0, 0);
-            wait_frag(f0);
-            trim(f0, kt, 2);
-            kstep(f0, f1, kt, 3, 0, 0, 0);
-            // every read of this stage is complete (all waves) and slice kt+1 has landed
+        for (int t = 0; t < P; ++t) {
+            const int kk = t / (MB * NB), j = t % (MB * NB) / MB, i = t % MB, at = kk * (MB + NB);
+            acc[j][i] = mfma32(cur[at + MB + j], cur[at + i], acc[j][i]);
+#pragma unroll
+            for (int q = t * N / R; q < (t + 1) * N / R && q < N; ++q) read_one(q, (uint32_t)(next * Sh::STAGE), nxt);
+#pragma unroll
+            for (int c = t * Sh::COPIES / P; c < (t + 1) * Sh::COPIES / P; ++c) copy_one(s + NS, stage, c);
             __builtin_amdgcn_sched_barrier(0);
-            wait_barrier(f1);
-            __builtin_amdgcn_sched_barrier(0);
-            trim(f1, kt, 3);
-            kstep(f1, f0, kt + 1, 0, kt + 2, 0, P::COPY_SPLIT);
-        } else {
-            // NS stages: slices kt+1 .. kt+NS-1 are in flight or landed; after
-            // the barrier (this wave's copies of slice kt+1 done, every read of
-            // slice kt done) the last K-step refills slice kt's stage with
-            // slice kt+NS
-            wait_frag(f0);
-            trim(f0, kt, 0);
-            kstep(f0, f1, kt, 1, 0, 0, 0);
-            wait_frag(f1);
-            trim(f1, kt, 1);
-            kstep(f1, f0, kt, 2, 0, 0, 0);
-            wait_frag(f0);
-            trim(f0, kt, 2);
-            kstep(f0, f1, kt, 3, 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            wait_barrier_vm(f1);
-            __builtin_amdgcn_sched_barrier(0);
-            trim(f1, kt, 3);
-            kstep(f1, f0, kt + 1, 0, kt + P::NS, 0, P::NCOPY);
         }
     };
 
-    Frag f0, f1;
-    if constexpr (P::NS == 2) {
-        // slice 0 whole, then the first part of slice 1
+    u32x4 f0[N], f1[N];
 #pragma unroll
-        for (int i = 0; i < P::NCOPY; ++i) copy_one(0, i);
-        PLE_WAIT_VM_BARRIER0();
+    for (int k = 0; k < NS; ++k)
 #pragma unroll
-        for (int i = 0; i < P::COPY_SPLIT; ++i) copy_one(1, i);
-    } else {
-        // slices 0 .. NS-1, then wait for slice 0
+        for (int c = 0; c < Sh::COPIES; ++c) copy_one(k, k, c);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "i"((NS - 1) * Sh::COPIES) : "memory");
 #pragma unroll
-        for (int k = 0; k < P::NS; ++k)
-#pragma unroll
-            for (int i = 0; i < P::NCOPY; ++i) copy_one(k, i);
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "i"((P::NS - 1) * P::SLICE_COPIES) : "memory");
+    for (int q = 0; q < N; ++q) read_one(q, 0u, f0);
+    int stage = 0;
+    for (int s = 0; s < nk; s += 2) {
+        const int s1 = stage + 1 == NS ? 0 : stage + 1, s2 = s1 + 1 == NS ? 0 : s1 + 1;
+        slice(s, stage, s1, f0, f1);
+        slice(s + 1, s1, s2, f1, f0);
+        stage = s2;
     }
-#pragma unroll
-    for (int q = 0; q < 2 * NB; ++q) read_one(q, 0, 0, f0);
-    for (int kt = 0; kt < nk; ++kt) slice(kt, f0, f1);
-    // The last slice's look-ahead reads into f0 are still in flight and
-    // opaque to the compiler's own waits: this wait names f0's registers, so
-    // no epilogue value is placed in them before the reads have landed.
-    if constexpr (NB == 4)
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : PLE_W8_FRAG_REGS4(f0) : : "memory");
-    else if constexpr (NB == 2)
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : PLE_W8_FRAG_REGS2(f0) : : "memory");
-    else
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : PLE_W8_FRAG_REGS1(f0) : : "memory");
-    __syncthreads();  // every wave is done with the stages before the epilogue reuses LDS
+    // the last look-ahead reads (of a stage that holds anything) have landed before their registers are used again
+    wait_slice<0>(f0);
 
-    // epilogue: acc[j][i][e] is feature n0 + wn*WT + j*32 + 8*(e/4) + 4*(lane/32) + e%4
-    // of token m0 + wm*WT + i*32 + lane%32
+    // acc[j][i][e] is feature n0 + wn*32*NB + j*32 + 8*(e/4) + 4*(lane/32) + e%4 of token m0 + wm*32*MB + i*32 + lane%32
     uint16_t* Cs = (uint16_t*)lds_raw;
 #pragma unroll
     for (int j = 0; j < NB; ++j)
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const int m = wm * WT + i * 32 + frow;
-                const int o = wn * WT + j * 32 + 8 * g + 4 * fk;
-                *(u32x2*)(Cs + m * P::OUT_ROW + o) = out4(a, m0 + m, n0 + o, acc[j][i][4 * g], acc[j][i][4 * g + 1],
-                                                              acc[j][i][4 * g + 2], acc[j][i][4 * g + 3]);
+                const int m = wm * (32 * MB) + i * 32 + frow;
+                const int o = wn * (32 * NB) + j * 32 + 8 * g + 4 * fk;
+                *(u32x2*)(Cs + m * (BN + 8) + o) = out4(a, m0 + m, n0 + o, acc[j][i][4 * g], acc[j][i][4 * g + 1],
+                                                        acc[j][i][4 * g + 2], acc[j][i][4 * g + 3]);
             }
     __syncthreads();
-    pipe_store<BT, kBigThreads>(Cs, P::OUT_ROW, a, m0, n0);
+    pipe_store<BM, BN, kTileThreads>(Cs, a, m0, n0);
 }
 
 // ---------------------------------------------------------------------------
@@ -428,8 +289,8 @@ __device__ __forceinline__ void w8_pipe(const W8Args& a) {
 // ---------------------------------------------------------------------------
 constexpr int kWideThreads = 512;
 // five operand-slice slots (160 KiB, all of the LDS), which also hold the epilogue's rows
-constexpr int kWideLdsBytes = 5 * W8PipeShape<256>::OP_BYTES;
-static_assert(kWideLdsBytes >= W8PipeShape<256>::LDS_BYTES, "the epilogue's rows fit in the ring");
+constexpr int kWideSlot = 256 * kSliceBytes, kWideLdsBytes = 5 * kWideSlot;
+static_assert(kWideLdsBytes >= 256 * (256 + 8) * 2, "the epilogue's rows fit in the ring");
 struct W8WideFrag {
     u32x4 a[8], b[4];
 };
@@ -438,7 +299,6 @@ struct W8WideFrag {
         "+v"(f.b[0]), "+v"(f.b[1]), "+v"(f.b[2]), "+v"(f.b[3])
 
 __device__ __forceinline__ void w8_pipe8w(const W8Args& a) {
-    using P = W8PipeShape<256>;
     constexpr int BT = 256, NC = 4;  // copy instructions per operand, wave and slice
     extern __shared__ __align__(16) char lds_raw[];
     const int tid = threadIdx.x;
@@ -471,11 +331,11 @@ __device__ __forceinline__ void w8_pipe8w(const W8Args& a) {
     // ahead of their use and x slices one ahead, each into the slot its
     // operand's slice three (W) or two (x) back has just left.
     auto copy_x = [&](int k, int i) {  // k uniform
-        char* base = lds_raw + (3 + (k & 1)) * P::OP_BYTES + (i * 8 + wave) * 1024;
+        char* base = lds_raw + (3 + (k & 1)) * kWideSlot + (i * 8 + wave) * 1024;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr_t)base, 16, aoff[i], min(k, nk - 1) * kSliceBytes, 0, 0);
     };
     auto copy_w = [&](int k, int i) {
-        char* base = lds_raw + (k % 3) * P::OP_BYTES + (i * 8 + wave) * 1024;
+        char* base = lds_raw + (k % 3) * kWideSlot + (i * 8 + wave) * 1024;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr_t)base, 16, boff[i], min(k, nk - 1) * kSliceBytes, 0, 0);
     };
 
@@ -497,8 +357,8 @@ __device__ __forceinline__ void w8_pipe8w(const W8Args& a) {
         b_addr[ks] = lds_base + (wn * 64 + frow) * 128 + col;
     }
     auto read_one = [&](int q, int kt, int ks, W8WideFrag& f) {
-        const uint32_t pa = a_addr[ks] + (uint32_t)(3 + (kt & 1)) * P::OP_BYTES;
-        const uint32_t pb = b_addr[ks] + (uint32_t)(kt % 3) * P::OP_BYTES;
+        const uint32_t pa = a_addr[ks] + (uint32_t)(3 + (kt & 1)) * kWideSlot;
+        const uint32_t pb = b_addr[ks] + (uint32_t)(kt % 3) * kWideSlot;
         switch (q) {
             case 0: asm volatile("ds_read_b128 %0, %1" : "=v"(f.a[0]) : "v"(pa)); break;
             case 1: asm volatile("ds_read_b128 %0, %1 offset:2048" : "=v"(f.a[1]) : "v"(pa)); break;
@@ -584,63 +444,71 @@ __device__ __forceinline__ void w8_pipe8w(const W8Args& a) {
         for (int i = 0; i < 8; ++i) {
             const int m = wm * 128 + i * 16 + frow;
             const int o = wn * 64 + j * 16 + 4 * fk;
-            *(u32x2*)(Cs + m * P::OUT_ROW + o) =
+            *(u32x2*)(Cs + m * (256 + 8) + o) =
                 out4(a, m0 + m, n0 + o, acc[j][i][0], acc[j][i][1], acc[j][i][2], acc[j][i][3]);
         }
     __syncthreads();
-    pipe_store<BT, kWideThreads>(Cs, P::OUT_ROW, a, m0, n0);
+    pipe_store<BT, BT, kWideThreads>(Cs, a, m0, n0);
 }
 #undef PLE_W8_WIDE_FRAG_REGS
 
-#undef PLE_W8_FRAG_REGS4
-#undef PLE_W8_FRAG_REGS2
-#undef PLE_W8_FRAG_REGS1
+#undef PLE_W8_REGS4
 
 __global__ __launch_bounds__(kWideThreads, 1) void w8_gemm_256_kernel(W8Args a) { w8_pipe8w(a); }
-__global__ __launch_bounds__(kBigThreads, 1) void w8_gemm_128_kernel(W8Args a) { w8_pipe<128>(a); }
-__global__ __launch_bounds__(kBigThreads, 1) void w8_gemm_64_kernel(W8Args a) { w8_pipe<64>(a); }
+// Tiles of four waves: 64-token blocks, 64-feature blocks, slices in LDS, what 256 of them (one per CU) take against
+// others' (half us with 4096 inputs: 7.0, 11.6, 19 and 32.5 us beyond a launch; of the eight-wave kernel 54).
+#define PLE_W8_TILES(X) X(1, 1, 4, 14) X(2, 1, 6, 23) X(2, 2, 4, 38) X(4, 2, 3, 65)
+constexpr int kWideCost = 106;
+#define PLE_W8_KERNEL(MB, NB, NS, COST)                                                                                        \
+    __global__ __launch_bounds__(kTileThreads, 1) void w8_tile_##MB##x##NB##_kernel(W8Args a) { w8_tile<MB, NB, NS>(a); }
+PLE_W8_TILES(PLE_W8_KERNEL)
+#undef PLE_W8_KERNEL
 
-// The few-token kernel's LDS: a step's inputs and weights of every wave, then the joined sums.
-constexpr int kStep = 256;  // bytes of K
+// The few-token kernel's LDS: a step's inputs and weights of every wave, then the joined sums.  ROWS: rows of x it has room
+// for (4, or 16 a token tile), STEP: bytes of K.
 constexpr int kRowsWaves = 8;
-template <int MT, int NT>
+template <int ROWS, int NT, int STEP>
 struct W8RowsShape {
-    static constexpr int X = MT * 16 * kStep;             // bytes of a wave's inputs
-    static constexpr int STEP = X + NT * 16 * kStep;
+    static constexpr int MT = (ROWS + 15) / 16;
+    static constexpr int X = ROWS * STEP;                 // bytes of a wave's inputs
+    static constexpr int ALL = X + NT * 16 * STEP;        // and weights
     static constexpr int JOIN = 4;                        // waves whose sums are in LDS at once
-    static constexpr int LDS = kRowsWaves * STEP > JOIN * MT * NT * 1024 ? kRowsWaves * STEP : JOIN * MT * NT * 1024;
+    static constexpr int LDS = kRowsWaves * ALL > JOIN * MT * NT * 1024 ? kRowsWaves * ALL : JOIN * MT * NT * 1024;
     static_assert(LDS <= 160 * 1024, "more LDS than a CU has");
+    static constexpr int CHUNKS = STEP / 16;              // of 16 bytes in a row
+    static constexpr int FILL = 64 / CHUNKS;              // rows that an instruction fills
+    // Row r's chunk c stands at place c ^ turn(r), so that the 16 rows of a fragment read touch different banks.
+    static __device__ __forceinline__ int turn(int r) { return CHUNKS == 8 ? (r >> 1) & 7 : r & 15; }
 };
 
-template <int MT, int NT>
+template <int ROWS, int NT, int STEP>
 __device__ __forceinline__ void w8_rows_body(const W8Args& a) {
-    using Sh = W8RowsShape<MT, NT>;
-    constexpr int kJoin = Sh::JOIN;
+    using Sh = W8RowsShape<ROWS, NT, STEP>;
+    constexpr int kJoin = Sh::JOIN, MT = Sh::MT;
     extern __shared__ __align__(16) char lds[];
     int(*const join)[MT * NT][64][4] = (int(*)[MT * NT][64][4])lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int tiles_o = (a.O + 16 * NT - 1) / (16 * NT), o0 = (blockIdx.x % tiles_o) * (16 * NT);
     const int t0 = (int)(blockIdx.x / tiles_o) * (16 * MT);
-    const int live = min(a.M - t0, 16 * MT);
-    char* const mine = lds + wave * Sh::STEP;
-    // An instruction fills four rows of 256 bytes: row r's 16 chunks of 16 bytes, chunk c at place c ^ (r % 16), so that
-    // the 16 rows of a fragment read touch different banks.  Rows past the end repeat the last one (their sums are not
-    // stored), chunks past K the first one (zeroed in x where they are used).
-    const int64_t wrow = (int64_t)o0 * a.K;
+    const int live = min(a.M - t0, ROWS);
+    char* const mine = lds + wave * Sh::ALL;
+    // Rows past the end repeat the last one (their sums are not stored), chunks past K the first one (zeroed in x where they
+    // are used).
+    const int8_t* const w0 = a.w + (int64_t)o0 * a.K;
     auto load = [&](int k0) {
 #pragma unroll
-        for (int i = 0; i < 4 * MT; ++i) {
-            if (4 * i >= live) break;
-            const int r = 4 * i + g, k = k0 + (n ^ (r & 15)) * 16;
+        for (int i = 0; i < ROWS / Sh::FILL; ++i) {
+            if (Sh::FILL * i >= live) break;
+            const int r = Sh::FILL * i + lane / Sh::CHUNKS, k = k0 + ((lane % Sh::CHUNKS) ^ Sh::turn(r)) * 16;
             const int8_t* src = a.x + (int64_t)(t0 + min(r, live - 1)) * a.x_stride + (k < a.K ? k : 0);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                              (__attribute__((address_space(3))) void*)(mine + i * 1024), 16, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 4 * NT; ++i) {
-            const int r = 4 * i + g, k = k0 + (n ^ (r & 15)) * 16;
-            const int8_t* src = a.w + wrow + (int64_t)(min(o0 + r, a.O - 1) - o0) * a.K + (k < a.K ? k : 0);
+        for (int i = 0; i < 16 * NT / Sh::FILL; ++i) {
+            const int r = Sh::FILL * i + lane / Sh::CHUNKS, k = k0 + ((lane % Sh::CHUNKS) ^ Sh::turn(r)) * 16;
+            const int8_t* src = w0 + (int64_t)(min(o0 + r, a.O - 1) - o0) * a.K + (k < a.K ? k : 0);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                              (__attribute__((address_space(3))) void*)(mine + Sh::X + i * 1024), 16, 0, 0);
         }
@@ -650,20 +518,22 @@ __device__ __forceinline__ void w8_rows_body(const W8Args& a) {
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = i32x4{0, 0, 0, 0};
-    for (int k0 = wave * kStep; k0 < a.K; k0 += kRowsWaves * kStep) {
+    for (int k0 = wave * STEP; k0 < a.K; k0 += kRowsWaves * STEP) {
         load(k0);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-        for (int j = 0; j < kStep / 64; ++j) {
-            const int at = n * kStep + ((4 * j + g) ^ n) * 16;
+        for (int j = 0; j < STEP / 64; ++j) {
+            const int c = 4 * j + g;
             u32x4 x[MT], w[NT];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                x[mt] = *(const u32x4*)(mine + mt * (16 * kStep) + at);
-                if (k0 + kStep > a.K && k0 + (4 * j + g) * 16 >= a.K) x[mt] = u32x4{0u, 0u, 0u, 0u};
+                const int r = ROWS < 16 ? n % ROWS : mt * 16 + n;  // (tokens past ROWS: any row, not stored)
+                x[mt] = *(const u32x4*)(mine + r * STEP + (c ^ Sh::turn(r)) * 16);
+                if (k0 + STEP > a.K && k0 + c * 16 >= a.K) x[mt] = u32x4{0u, 0u, 0u, 0u};
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) w[nt] = *(const u32x4*)(mine + Sh::X + nt * (16 * kStep) + at);
+            for (int nt = 0; nt < NT; ++nt)
+                w[nt] = *(const u32x4*)(mine + Sh::X + (nt * 16 + n) * STEP + (c ^ Sh::turn(n)) * 16);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -703,21 +573,42 @@ __device__ __forceinline__ void w8_rows_body(const W8Args& a) {
     }
 }
 
-// Token tiles, feature tiles, waves per SIMD that registers are kept to.
-#define PLE_W8_SHAPES(X) X(1, 1, 4) X(2, 1, 4) X(4, 1, 2)
-#define PLE_W8_KERNEL(MT, NT, OCC) \
-    __global__ __launch_bounds__(kRowsWaves * kWave, OCC) void w8_rows_##MT##x##NT##_kernel(W8Args a) { w8_rows_body<MT, NT>(a); }
+// Rows, feature tiles, bytes of a step, waves per SIMD that registers are kept to.
+#define PLE_W8_SHAPES(X) X(16, 1, 256, 4) X(32, 2, 128, 4) X(64, 2, 128, 2)
+#define PLE_W8_KERNEL(ROWS, NT, STEP, OCC)                                                                             \
+    __global__ __launch_bounds__(kRowsWaves * kWave, OCC) void w8_rows_##ROWS##x##NT##_##STEP##_kernel(W8Args a) {     \
+        w8_rows_body<ROWS, NT, STEP>(a);                                                                               \
+    }
 PLE_W8_SHAPES(PLE_W8_KERNEL)
 #undef PLE_W8_KERNEL
 
+// Few 64 x 64 tiles leave CUs idle: there the waves of a block share K instead (with 4096 inputs: 37 tokens, 5003 features
+// 8.9 us against 11.0, 100 and 2048 7.2 and 8.6, 4 and 4096 6.5 and 8.3; but 64 and 6400 9.7 and 9.3, 16 and 8192 10.2 and
+// 8.7, 1 and 8192 8.8 and 8.6).  Of those kernels the one with the fewest rows that hold the tokens; blocks of 32 rows also
+// for more tokens as long as the CUs hold them (48 tokens, 4096 features 7.6 us, in blocks of 64 rows 8.5; 37 and 5003 12.8
+// and 8.9).  Otherwise the tiles whose rounds over the CUs take least: a last round that is not full still takes most of one
+// (64 tiles of 128 x 128 12.5 us, 128 14.6, 256 19).
+constexpr int kFewTiles = 100;
 W8Shape w8_linear_shape(int64_t T, int32_t O) {
-    if (T <= 64) return {0, T <= 16 ? 1 : (T <= 32 ? 2 : 4), 1};
-    // the widest tile that still gives 256 blocks, one per CU (64-wide tiles take 128 KiB of LDS, so only while one block
-    // per CU covers them)
-    const auto tiles = [&](int64_t b) { return ((T + b - 1) / b) * ((O + b - 1) / b); };
-    if (tiles(256) >= 256) return {256, 0, 0};
-    if (tiles(128) >= 256 || tiles(64) > 256) return {128, 0, 0};
-    return {64, 0, 0};
+    const auto tiles = [&](int64_t m, int64_t n) { return ((T + m - 1) / m) * ((O + n - 1) / n); };
+    if (tiles(64, 64) < kFewTiles) {
+        if (T <= 16) return {0, 16, 1, 256};
+        return T <= 32 || tiles(32, 32) <= 256 ? W8Shape{0, 32, 2, 128} : W8Shape{0, 64, 2, 128};
+    }
+    W8Shape best = {256, 0, 0, 0};
+    const auto cost = [&](int64_t n, int64_t one) { return n / 256 * 256 * one + (n % 256 ? one * (160 + n % 256 * 3 / 8) : 0); };
+    int64_t least = cost(tiles(256, 256), kWideCost);
+    const auto consider = [&](int mb, int nb, int64_t one) {
+        const int64_t c = cost(tiles(64 * mb, 64 * nb), one);
+        if (c < least) {
+            least = c;
+            best = {64, mb, nb, 0};
+        }
+    };
+#define PLE_W8_CONSIDER(MB, NB, NS, COST) consider(MB, NB, COST);
+    PLE_W8_TILES(PLE_W8_CONSIDER)
+#undef PLE_W8_CONSIDER
+    return best;
 }
 
 template <void (*FN)(W8Args), int LDS>
@@ -732,12 +623,15 @@ hipError_t launch_w8_linear(const W8Args& a, hipStream_t s) {
     const W8Shape f = w8_linear_shape(a.M, a.O);
     const auto tiles = [&](int64_t m, int64_t n) { return ((a.M + m - 1) / m) * ((a.O + n - 1) / n); };
     if (f.block == 256) return launch_w8<w8_gemm_256_kernel, kWideLdsBytes>(a, tiles(256, 256), kWideThreads, s);
-    if (f.block == 128) return launch_w8<w8_gemm_128_kernel, W8PipeShape<128>::LDS_BYTES>(a, tiles(128, 128), kBigThreads, s);
-    if (f.block == 64) return launch_w8<w8_gemm_64_kernel, W8PipeShape<64>::LDS_BYTES>(a, tiles(64, 64), kBigThreads, s);
-#define PLE_W8_LAUNCH(MT, NT, OCC)                                                                                     \
-    if (f.mt == MT && f.nt == NT)                                                                                      \
-        return launch_w8<w8_rows_##MT##x##NT##_kernel, W8RowsShape<MT, NT>::LDS>(a, tiles(16 * MT, 16 * NT),           \
-                                                                                kRowsWaves * kWave, s);
+#define PLE_W8_LAUNCH(MB, NB, NS, COST)                                                                               \
+    if (f.block == 64 && f.rows == MB && f.nt == NB)                                                                  \
+        return launch_w8<w8_tile_##MB##x##NB##_kernel, W8Tile<MB, NB, NS>::LDS>(a, tiles(64 * MB, 64 * NB), kTileThreads, s);
+    PLE_W8_TILES(PLE_W8_LAUNCH)
+#undef PLE_W8_LAUNCH
+#define PLE_W8_LAUNCH(ROWS, NT, STEP, OCC)                                                                            \
+    if (f.rows == ROWS && f.nt == NT && f.step == STEP)                                                               \
+        return launch_w8<w8_rows_##ROWS##x##NT##_##STEP##_kernel, W8RowsShape<ROWS, NT, STEP>::LDS>(                   \
+            a, tiles(16 * W8RowsShape<ROWS, NT, STEP>::MT, 16 * NT), kRowsWaves * kWave, s);
     PLE_W8_SHAPES(PLE_W8_LAUNCH)
 #undef PLE_W8_LAUNCH
     return hipErrorInvalidValue;

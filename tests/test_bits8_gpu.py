@@ -125,10 +125,10 @@ def scales_of(g, n):
     return torch.exp(3 * torch.randn(n, generator=g))
 
 
-# every kernel: few tokens in one, two and four tiles, blocks of 64, 128 and 256; K in whole steps, ending inside one, of one piece
-LINEAR_T_O = [(1, 1), (1, 300), (5, 17), (16, 48), (17, 333), (32, 100), (33, 70), (64, 1000), (65, 100), (100, 4200), (600, 333),
-              (700, 5003), (2051, 4099), (4100, 4104)]
-LINEAR_K = [16, 112, 128, 144, 1040]
+# every kernel; K in whole steps and slices, ending inside one, of one piece, and of more slices than are on their way at once
+LINEAR_T_O = [(1, 1), (1, 300), (5, 17), (16, 48), (17, 333), (32, 100), (33, 70), (37, 5003), (64, 1000), (65, 100), (1, 6500), (100, 4200),
+              (130, 8100), (600, 333), (700, 5003), (2051, 4099), (4100, 4104)]
+LINEAR_K = [16, 112, 128, 144, 384, 1040]
 
 
 @pytest.mark.parametrize("K", LINEAR_K)
