@@ -25,11 +25,6 @@ from .fp4 import (_BF, _FP8, _MOST, _attention, _attention_workspace_bytes, _fit
 _I8, _FLOAT = torch.int8, torch.float32
 
 
-def _new1(n, device, stream):
-    """A new fp32 [n] for a call on `stream`."""
-    return _new((n, 1), _FLOAT, device, stream).view(n)
-
-
 def ple_rms_norm8(x, weight, *, residual=None, eps: float = 1e-6, codes=None, scales=None, residual_out=None, stream=None):
     """x bf16 [T][N] (rows may be strided), residual bf16 [T][N] or None, weight bf16 [N] -> (codes int8 [T][N], scales fp32
     [T], residual_out bf16 [T][N]: x + residual, or None without one).  residual_out may be residual."""
@@ -37,26 +32,24 @@ def ple_rms_norm8(x, weight, *, residual=None, eps: float = 1e-6, codes=None, sc
     if len(shape) != 2 or x.dtype not in _BF16 or (shape[0] and x.stride(1) != 1):
         raise ValueError(f"x must be bf16 [T][N] with contiguous rows, got {tuple(shape)} {x.dtype}")
     T, N = shape
-    dev = x.get_device()
-    if not _fits(weight, _BF, (N,), dev):
-        _req("weight", weight, (N,), _BF16)
-    if residual is not None:
-        if not _fits(residual, _BF, shape, dev):
-            _req("residual", residual, (T, N), _BF16)
-        if residual_out is None:
-            _same_device(x, residual)
-            residual_out = _new((T, N), _BF, x.device, stream)
-        else:
-            _req("residual_out", residual_out, (T, N), _BF16)
-    elif residual_out is not None:
+    dev, device = x.get_device(), x.device
+    if residual is None and residual_out is not None:
         raise ValueError("residual_out given without residual")
-    _req("codes", codes, (T, N), (_I8,), optional=True)
-    _req("scales", scales, (T,), _F32, optional=True)
-    _same_device(x, weight, residual, codes, scales, residual_out)
+    # (what most calls pass goes through the checks that name the fault only where one is off)
+    if (dev < 0 or not _fits(weight, _BF, (N,), dev) or not (residual is None or _fits(residual, _BF, shape, dev))
+            or codes is not None or scales is not None or residual_out is not None):
+        _req("weight", weight, (N,), _BF16)
+        _req("residual", residual, (T, N), _BF16, optional=True)
+        _req("residual_out", residual_out, (T, N), _BF16, optional=True)
+        _req("codes", codes, (T, N), (_I8,), optional=True)
+        _req("scales", scales, (T,), _F32, optional=True)
+        _same_device(x, weight, residual, codes, scales, residual_out)
+    if residual is not None and residual_out is None:
+        residual_out = _new((T, N), _BF, device, stream)
     if codes is None:
-        codes = _new((T, N), _I8, x.device, stream)
+        codes = _new((T, N), _I8, device, stream)
     if scales is None:
-        scales = _new1(T, x.device, stream)
+        scales = _new((T,), _FLOAT, device, stream)
     rc = capi.load().ple_rms_norm8(x.data_ptr(), x.stride(0) if T > 1 else N, _ptr(residual), _ptr(weight), T, N, eps,
                                    _ptr(codes), _ptr(scales), _ptr(residual_out),
                                    _raw_stream(dev) if stream is None else _stream(stream))

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArg
         const double angle = (double)(pos < 0 ? 0 : pos) * (double)a.inv_freq[i];
         double sn, cs;
         sincos(angle, &sn, &cs);
-        turn[i] = make_double2(cs, sn);
+        turn[turn_place(i, half)] = make_double2(cs, sn);
     }
     __syncthreads();
     const int64_t group0 = first_group(a.cache, a.batch.page_table + (int64_t)r * a.batch.table_width, pos);

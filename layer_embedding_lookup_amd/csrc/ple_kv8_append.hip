@@ -13,16 +13,18 @@
 // request r has those from floor(start of r / 16) + 2 r on, which is enough
 // for any position it begins at.
 //
-// Angles are formed in 64 bits (positions of 10^5 and more lose them in 32):
-// two sines and cosines a thread, of its four tokens' first angle and of the
-// angle from one token to the next, then by products (2^-51 of the angle's
-// sine and cosine after three).
+// Angles are formed in 64 bits (positions of 10^5 and more lose them in 32),
+// in turns: position * (frequency / 2 pi), whose two roundings are 2^-52 of
+// the angle, needs no reduction by pi.  A thread forms sine and cosine of its
+// first new token of four and of the step from one token to the next; the
+// others follow by products (2^-51 after three).
 #include "ple_8bit_launch.h"
 #include "ple_rotate.h"
 
 namespace ple {
 
 constexpr int kAppendThreads = 256;
+constexpr double kPerTurn = 0.15915494309189533577;  // 1 / (2 pi)
 constexpr int kAppendWaves = kAppendThreads / kWave;
 
 // What a unit of the launch writes or reads: new tokens of request r at places [from, to) of a block.
@@ -32,6 +34,8 @@ struct Kv8Unit {
     int block;        // position / 16
     int from, to;     // (from > 0: earlier tokens of the request stand before it)
     bool any;
+    int64_t index;    // of the request's blocks
+    int64_t q0, n, lo, hi;  // its new tokens q0 .. q0 + n, of which those from lo up to hi stand on some place
 };
 
 // Blocks that the launch has for requests: with a hint as many as a request can reach, times the requests; or by their
@@ -49,7 +53,7 @@ __device__ __forceinline__ Kv8Unit kv8_unit(const ple_kv8_cache& c, const ple_kv
     Kv8Unit w;
     const int64_t T = b.num_tokens, each = hint ? kv8_units_each(b) : 0;
     const auto start = [&](int r) { return min(max((int64_t)b.query_start_loc[r], (int64_t)0), T); };
-    int64_t i;  // of the request's blocks
+    int64_t i;
     if (each > 0 && each * b.num_reqs == kv8_units(b, hint)) {
         w.r = (int)(u / each);
         i = u - w.r * each;
@@ -88,6 +92,11 @@ __device__ __forceinline__ Kv8Unit kv8_unit(const ple_kv8_cache& c, const ple_kv
     const int64_t block = lo / 16 + i;
     const int64_t p0 = max(lo, block * 16), p1 = min(hi, block * 16 + 16);
     w.any = i >= 0 && p0 < p1;
+    w.index = i;
+    w.q0 = q0;
+    w.n = n;
+    w.lo = min(lo - before, n);
+    w.hi = max(min(hi - before, n), w.lo);
     w.block = (int)block;
     w.from = (int)(p0 - block * 16);
     w.to = (int)(p1 - block * 16);
@@ -137,73 +146,111 @@ __device__ __forceinline__ float wave_max(float x) {
 }
 
 // The scale of a block: the one its new tokens need, or the one it has; `by`: what the earlier tokens' codes change by.
-__device__ __forceinline__ float joined_scale(const float* at, bool earlier, float top, float& by) {
-    const float need = block_scale(top), old = earlier ? *at : 0.f;
-    const float s = fmaxf(need, old);
+__device__ __forceinline__ float joined_scale(float old, bool earlier, float top, float& by) {
+    const float s = fmaxf(block_scale(top), old);
     by = earlier ? old / s : 1.f;
     return s;
 }
 
+// What a wave's unit reads, on its way before the angles are formed.  Keys: 16 bytes a lane, whole rows (lane l of load i:
+// elements 8 (l % (D/8)) .. of token i * 512/D + l / (D/8)); values: E elements of each of the 16 tokens.
 template <int D>
-__device__ __forceinline__ void append_keys(const Kv8AppendArgs& a, const Kv8Unit& w, int head, const double2 (*turn)[D / 2]) {
-    constexpr int N = D / 64;  // pieces of 16 elements of a token that a lane has
-    const int lane = threadIdx.x & 63, j = lane & 15;
-    const int64_t grp = w.group + (int64_t)head * (a.cache.page_size >> 4);
-    const bool mine = j >= w.from && j < w.to;
-    const uint16_t* src = a.src[1] + (w.first + (j - w.from)) * a.stride[1] + head * D;
-    float x[N][2][8], top = 0.f;
+struct AppendRows {
+    static constexpr int PER = D / 8, TOKENS = kWave / PER, LOADS = 16 / TOKENS;
+    static constexpr int E = D == 256 ? 4 : 2;
+    union {
+        u32x4 key[LOADS];
+        uint32_t value[16][E / 2];
+    };
+
+    __device__ __forceinline__ void load_keys(const Kv8AppendArgs& a, const Kv8Unit& w, int head) {
+        const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][h][e] = 0.f;
-            if (mine) load_rotated(src, (4 * i + (lane >> 4)) * 16 + h * 8, a.rot_dim, a.interleaved, turn[j], x[i][h]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_size(x[i][h][e]));
+        for (int i = 0; i < LOADS; ++i) {
+            const int j = i * TOKENS + lane / PER;
+            const uint16_t* src = a.src[1] + (w.first + (j - w.from)) * a.stride[1] + head * D + (lane % PER) * 8;
+            key[i] = j >= w.from && j < w.to ? *(const u32x4*)src : u32x4{0u, 0u, 0u, 0u};
         }
-    float by;
+    }
+    __device__ __forceinline__ void load_values(const Kv8AppendArgs& a, const Kv8Unit& w, int head) {
+        const int d0 = (threadIdx.x & 63) * E;
+        const uint16_t* src = a.src[2] + (w.first - w.from) * a.stride[2] + head * D + d0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e)
+                value[j][e] = d0 < D && j >= w.from && j < w.to ? ((const uint32_t*)(src + j * a.stride[2]))[e] : 0u;
+    }
+};
+
+template <int D>
+__device__ __forceinline__ void append_keys(const Kv8AppendArgs& a, const Kv8Unit& w, int head, const AppendRows<D>& raw,
+                                            const double2 (*turn)[D / 2], char* lds) {
+    using Rows = AppendRows<D>;
+    constexpr int L = Rows::LOADS;
+    const int lane = threadIdx.x & 63, c = lane % Rows::PER, half = a.rot_dim / 2;
+    const int64_t grp = w.group + (int64_t)head * (a.cache.page_size >> 4);
     float* const scale = a.cache.k_scales + grp;
-    const float s = joined_scale(scale, w.from > 0, wave_max(top), by), inv = 1.f / s;
-    uint8_t* const codes = a.cache.k_codes + grp * (16 * D) + lane * 16;
+    const float held_scale = w.from > 0 ? *scale : 0.f;
+    float x[L][8], top = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        u32x4* const at = (u32x4*)(codes + i * 1024);
-        if (mine) {
-            u32x4 c;
+    for (int i = 0; i < L; ++i) {
+        const int token = i * Rows::TOKENS + lane / Rows::PER;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+        for (int e = 0; e < 4; ++e) {
+            x[i][2 * e] = bf16_lo(raw.key[i][e]);
+            x[i][2 * e + 1] = bf16_hi(raw.key[i][e]);
+        }
+        if (half > 0) {
+            u32x4 other;  // the pairs' other elements (half a rotation away), in another lane of the token
+            const int from = a.interleaved ? lane : (c * 8 < half ? lane + half / 8 : (c * 8 < 2 * half ? lane - half / 8 : lane));
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    c[2 * h + e] = codes4(coded(x[i][h][4 * e], inv), coded(x[i][h][4 * e + 1], inv),
-                                          coded(x[i][h][4 * e + 2], inv), coded(x[i][h][4 * e + 3], inv));
-            *at = c;
+            for (int e = 0; e < 4; ++e) other[e] = __shfl(raw.key[i][e], from, kWave);
+            if (c * 8 < a.rot_dim && token >= w.from && token < w.to) turn8(x[i], other, c * 8, half, a.interleaved, turn[token]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_size(x[i][e]));
+    }
+    float by;
+    const float s = joined_scale(held_scale, w.from > 0, wave_max(top), by), inv = 1.f / s;
+    // through LDS into the cache's order: pieces of 16 elements, 16 tokens each
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        const int j = i * Rows::TOKENS + lane / Rows::PER;
+        u32x2 codes;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            codes[e] = codes4(coded(x[i][4 * e], inv), coded(x[i][4 * e + 1], inv), coded(x[i][4 * e + 2], inv),
+                              coded(x[i][4 * e + 3], inv));
+        *(u32x2*)(lds + (c / 2) * 256 + j * 16 + (c & 1) * 8) = codes;
+    }
+    __builtin_amdgcn_wave_barrier();  // (the wave's own part of LDS)
+    const int j = lane & 15;
+    uint8_t* const to = a.cache.k_codes + grp * (16 * D) + lane * 16;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        u32x4* const at = (u32x4*)(to + i * 1024);
+        if (j >= w.from && j < w.to) {
+            *at = *(const u32x4*)(lds + i * 1024 + lane * 16);
         } else if (by != 1.f && j < w.from) {
-            u32x4 c = *at;
+            u32x4 held = *at;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] = rescaled4(c[e], by);
-            *at = c;
+            for (int e = 0; e < 4; ++e) held[e] = rescaled4(held[e], by);
+            *at = held;
         }
     }
     if (lane == 0) *scale = s;
 }
 
 template <int D>
-__device__ __forceinline__ void append_values(const Kv8AppendArgs& a, const Kv8Unit& w, int head) {
-    constexpr int E = D == 256 ? 4 : 2;  // elements of a lane, of all 16 tokens
+__device__ __forceinline__ void append_values(const Kv8AppendArgs& a, const Kv8Unit& w, int head, const AppendRows<D>& rows) {
+    constexpr int E = AppendRows<D>::E;  // elements of a lane, of all 16 tokens
     const int lane = threadIdx.x & 63, d0 = lane * E;
     const bool live = d0 < D;
     const int64_t grp = w.group + (int64_t)head * (a.cache.page_size >> 4);
-    const uint16_t* src = a.src[2] + (w.first - w.from) * a.stride[2] + head * D + d0;
-    uint32_t raw[16][E / 2];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) raw[j][e] = 0u;
-        if (live && j >= w.from && j < w.to)
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) raw[j][e] = ((const uint32_t*)(src + j * a.stride[2]))[e];
-    }
+    float* const scale = a.cache.v_scales + grp;
+    const float held_scale = w.from > 0 ? *scale : 0.f;
+    const uint32_t(&raw)[16][E / 2] = rows.value;
     float top = 0.f;
 #pragma unroll
     for (int j = 0; j < 16; ++j)
@@ -211,8 +258,7 @@ __device__ __forceinline__ void append_values(const Kv8AppendArgs& a, const Kv8U
         for (int e = 0; e < E / 2; ++e)
             top = fmaxf(top, fmaxf(finite_size(bf16_lo(raw[j][e])), finite_size(bf16_hi(raw[j][e]))));
     float by;
-    float* const scale = a.cache.v_scales + grp;
-    const float s = joined_scale(scale, w.from > 0, wave_max(top), by), inv = 1.f / s;
+    const float s = joined_scale(held_scale, w.from > 0, wave_max(top), by), inv = 1.f / s;
     const bool whole = w.from == 0 && w.to == 16;
     if (live) {
 #pragma unroll
@@ -253,25 +299,42 @@ __device__ __forceinline__ void append_values(const Kv8AppendArgs& a, const Kv8U
 template <int D>
 __device__ __forceinline__ void append_body(const Kv8AppendArgs& a, int64_t units, int parts) {
     __shared__ double2 turn[16][D / 2];  // cos, sin of the tokens' angles
+    __shared__ __align__(16) char lds[kAppendWaves * 16 * D];
     const int half = a.rot_dim / 2, heads = a.cache.num_kv_heads;
     const int64_t id = grid_block();
     const int wave = threadIdx.x >> 6;
     if (id < units * parts) {
         const int64_t u = id / parts;
         const int part = (int)(id - u * parts);
+        const bool keys = part * kAppendWaves < heads && half > 0;  // some wave has keys to turn
+        // (frequencies first: loads return in order, and the angles need not wait for the rows)
+        constexpr int kRuns = 4, kLong = 16 / kRuns, kEach = (kRuns * (D / 2) + kAppendThreads - 1) / kAppendThreads;
+        float freq[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = threadIdx.x + k * kAppendThreads;
+            freq[k] = keys && i < kRuns * half ? a.inv_freq[i % half] : 0.f;
+        }
         const Kv8Unit w = kv8_unit(a.cache, a.batch, u, true);
         if (w.group < 0) return;
-        if (part * kAppendWaves < heads && half > 0) {  // some wave has keys
-            constexpr int kRuns = 4, kLong = 16 / kRuns;
-            for (int i = threadIdx.x; i < kRuns * half; i += kAppendThreads) {
-                const int run = i / half, f = i - run * half;
-                const double by = (double)a.inv_freq[f];
-                double sn, cs, s1, c1;
-                sincos((double)(w.block * 16 + run * kLong) * by, &sn, &cs);
-                sincos(by, &s1, &c1);
+        const int unit = part * kAppendWaves + wave;
+        AppendRows<D> raw;
+        if (unit < heads)
+            raw.load_keys(a, w, unit);
+        else if (unit < 2 * heads)
+            raw.load_values(a, w, unit - heads);
+        if (keys) {
 #pragma unroll
-                for (int j = 0; j < kLong; ++j) {
-                    turn[run * kLong + j][f] = make_double2(cs, sn);
+            for (int k = 0; k < kEach; ++k) {
+                const int i = threadIdx.x + k * kAppendThreads, run = i / half, f = i - run * half;
+                const int j0 = max(w.from, run * kLong), j1 = min(w.to, run * kLong + kLong);
+                if (i >= kRuns * half || j0 >= j1) continue;
+                const double by = (double)freq[k] * kPerTurn;
+                double sn, cs, s1 = 0., c1 = 1.;
+                sincospi(2. * ((double)(w.block * 16 + j0) * by), &sn, &cs);
+                if (j1 > j0 + 1) sincospi(2. * by, &s1, &c1);
+                for (int j = j0; j < j1; ++j) {
+                    turn[j][turn_place(f, half)] = make_double2(cs, sn);
                     const double c = cs * c1 - sn * s1;
                     sn = sn * c1 + cs * s1;
                     cs = c;
@@ -279,11 +342,10 @@ __device__ __forceinline__ void append_body(const Kv8AppendArgs& a, int64_t unit
             }
             __syncthreads();
         }
-        const int unit = part * kAppendWaves + wave;
         if (unit < heads)
-            append_keys<D>(a, w, unit, turn);
+            append_keys<D>(a, w, unit, raw, turn, lds + wave * (16 * D));
         else if (unit < 2 * heads)
-            append_values<D>(a, w, unit - heads);
+            append_values<D>(a, w, unit - heads, raw);
         return;
     }
     const int64_t t = id - units * parts;
@@ -291,8 +353,8 @@ __device__ __forceinline__ void append_body(const Kv8AppendArgs& a, int64_t unit
     const int pos = kv8_position(a.cache, a.batch, t);
     for (int i = threadIdx.x; i < half; i += kAppendThreads) {
         double sn, cs;
-        sincos((double)(pos < 0 ? 0 : pos) * (double)a.inv_freq[i], &sn, &cs);
-        turn[0][i] = make_double2(cs, sn);
+        sincospi(2. * ((double)(pos < 0 ? 0 : pos) * ((double)a.inv_freq[i] * kPerTurn)), &sn, &cs);
+        turn[0][turn_place(i, half)] = make_double2(cs, sn);
     }
     __syncthreads();
     for (int c = threadIdx.x; c < a.num_q_heads * (D / 8); c += kAppendThreads) {
@@ -322,7 +384,7 @@ int64_t kv8_append_blocks(const ple_kv8_cache& cache, const ple_kv8_batch& batch
     return kv8_units(batch, true) * kv8_parts(cache) + (num_q_heads > 0 ? batch.num_tokens : 0);
 }
 int64_t kv8_read_blocks(const ple_kv8_cache& cache, const ple_kv8_batch& batch) {
-    return kv8_units(batch, false) * kv8_parts(cache) + batch.num_tokens;
+    return kv8_units(batch, false) * kv8_parts(cache);
 }
 
 hipError_t launch_kv8_append(const Kv8AppendArgs& a, hipStream_t s) {
@@ -354,23 +416,29 @@ __device__ __forceinline__ void unpack4(uint32_t w, float s, float (&v)[4]) {
     v[3] = hi[1] * s;
 }
 
+__device__ __forceinline__ void clear_row(const Kv8ReadArgs& a, int64_t t, int row) {
+    for (int e = threadIdx.x * 8; e < row; e += kAppendThreads * 8)
+        *(u32x4*)(a.k_out + t * row + e) = *(u32x4*)(a.v_out + t * row + e) = u32x4{0u, 0u, 0u, 0u};
+}
+
 // A block of 16 tokens, a wave a head's keys or values, as append; tokens that stand on no page are zeros.
 template <int D>
 __device__ __forceinline__ void read_body(const Kv8ReadArgs& a) {
-    const int64_t id = grid_block(), T = a.batch.num_tokens;
-    if (id >= a.units * a.parts) {  // a block per token: those of no request and of no place in the table
-        const int64_t t = id - a.units * a.parts;
-        if (t >= T) return;
-        if (kv8_position(a.cache, a.batch, t) >= 0) return;
-        const int row = a.cache.num_kv_heads * D;
-        for (int e = threadIdx.x * 8; e < row; e += kAppendThreads * 8)
-            *(u32x4*)(a.k_out + t * row + e) = *(u32x4*)(a.v_out + t * row + e) = u32x4{0u, 0u, 0u, 0u};
-        return;
-    }
+    const int64_t id = grid_block();
+    if (id >= a.units * a.parts) return;
     const int64_t u = id / a.parts;
     const int lane = threadIdx.x & 63, heads = a.cache.num_kv_heads;
     const int unit = (int)(id - u * a.parts) * kAppendWaves + (threadIdx.x >> 6);
     const Kv8Unit w = kv8_unit(a.cache, a.batch, u, false);
+    if (id - u * a.parts == 0) {  // tokens that stand on no place: of no request, here by the launch's units in turn, and of this one
+        const int64_t T = a.batch.num_tokens, first = min(max((int64_t)a.batch.query_start_loc[0], (int64_t)0), T);
+        const int64_t last = min(max((int64_t)a.batch.query_start_loc[a.batch.num_reqs], first), T);
+        for (int64_t i = u; i < first + (T - last); i += a.units) clear_row(a, i < first ? i : last + (i - first), heads * D);
+        if (w.index == 0) {
+            for (int64_t i = 0; i < w.lo; ++i) clear_row(a, w.q0 + i, heads * D);
+            for (int64_t i = w.hi; i < w.n; ++i) clear_row(a, w.q0 + i, heads * D);
+        }
+    }
     if (!w.any || unit >= 2 * heads) return;
     const int head = unit < heads ? unit : unit - heads;
     const int64_t grp = w.group + (int64_t)head * (a.cache.page_size >> 4), tokens = (int64_t)heads * D;

@@ -14,33 +14,45 @@ __device__ __forceinline__ void load8(const uint16_t* __restrict__ p, float (&v)
     }
 }
 
-// Elements d0 .. d0 + 7 of a head's row, turned by the token's angles (turn[i]: cosine and sine of angle i) where they lie
-// in its first rot_dim.  In 64 bits and rounded once to fp32, so that an element next to a code's border falls on the side
-// that the definition says.
-__device__ __forceinline__ void load_rotated(const uint16_t* __restrict__ src, int d0, int rot_dim, bool interleaved,
-                                             const double2* turn, float (&v)[8]) {
-    load8(src + d0, v);
-    if (d0 >= rot_dim) return;
+// Where angle f of a token's `half` (a multiple of 8) stands in LDS: lanes that turn neighbouring eights of a head read
+// neighbouring places.
+__device__ __forceinline__ int turn_place(int f, int half) { return (f & 7) * (half >> 3) + (f >> 3); }
+
+// Elements d0 .. d0 + 7 of a head's row (v, inside its first 2 half), turned by the token's angles (turn[turn_place(i)]:
+// cosine and sine of angle i); other: the row's elements half a rotation away, if pairs are not neighbours.  In 64 bits and rounded once to
+// fp32, so that an element next to a code's border falls on the side that the definition says.
+__device__ __forceinline__ void turn8(float (&v)[8], u32x4 other, int d0, int half, bool interleaved, const double2* turn) {
+    const int step = half >> 3;  // (from an angle to the next one of the same eight, or four)
     if (interleaved) {
+        turn += turn_place(d0 / 2, half);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const double2 w = turn[d0 / 2 + i];
+            const double2 w = turn[i * step];
             const double x = v[2 * i], y = v[2 * i + 1];
             v[2 * i] = (float)(x * w.x - y * w.y);
             v[2 * i + 1] = (float)(y * w.x + x * w.y);
         }
     } else {
-        const int half = rot_dim / 2;
         const bool upper = d0 >= half;  // half is a multiple of 8
-        float o[8];
-        load8(src + (upper ? d0 - half : d0 + half), o);
+        turn += turn_place(upper ? d0 - half : d0, half);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const double2 w = turn[(upper ? d0 - half : d0) + i];
-            const double x = v[i], y = o[i];
+            const double2 w = turn[i * step];
+            const double x = v[i], y = i % 2 ? bf16_hi(other[i / 2]) : bf16_lo(other[i / 2]);
             v[i] = (float)(upper ? x * w.x + y * w.y : x * w.x - y * w.y);
         }
     }
+}
+
+// Elements d0 .. d0 + 7 of a head's row in memory, turned where they lie in its first rot_dim.
+__device__ __forceinline__ void load_rotated(const uint16_t* __restrict__ src, int d0, int rot_dim, bool interleaved,
+                                             const double2* turn, float (&v)[8]) {
+    load8(src + d0, v);
+    if (d0 >= rot_dim) return;
+    const int half = rot_dim / 2;
+    u32x4 other = {0u, 0u, 0u, 0u};
+    if (!interleaved) other = *(const u32x4*)(src + (d0 >= half ? d0 - half : d0 + half));
+    turn8(v, other, d0, half, interleaved, turn);
 }
 
 }  // namespace ple

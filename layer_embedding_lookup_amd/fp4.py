@@ -41,8 +41,9 @@ def _on(stream, device):
 
 
 def _new(shape, dtype, device, stream=None):
-    """torch.empty for two or three dimensions, in 1.3 us where that takes 2.0, for a call on `stream`."""
-    strides = (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1)
+    """torch.empty for one to three dimensions, in 1.3 us where that takes 2.0, for a call on `stream`."""
+    n = len(shape)
+    strides = (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1) if n == 3 else (1,)
     if stream is None:
         return torch.empty_strided(shape, strides, dtype=dtype, device=device)
     with _on(stream, device):
