@@ -27,6 +27,11 @@ struct RmsNorm8Args {
     float* scales;
     uint16_t* residual_out;  // or NULL
 };
+// The kernel of a call: waves a row and chunks of 8 elements a lane; 0 waves: rows that registers do not hold.
+struct RmsNorm8Shape {
+    int waves, chunks;
+};
+RmsNorm8Shape rms_norm8_shape(int32_t n);
 hipError_t launch_rms_norm8(const RmsNorm8Args& a, hipStream_t s);
 
 struct W8Args {

@@ -178,17 +178,23 @@ __global__ __launch_bounds__(kLongThreads) void rms_norm8_long_kernel(RmsNorm8Ar
 PLE_NORM_SHAPES(PLE_NORM_KERNEL)
 #undef PLE_NORM_KERNEL
 
+RmsNorm8Shape rms_norm8_shape(int32_t n) {
+#define PLE_NORM_FITS(WAVES, CH) \
+    if (n <= WAVES * kWave * CH * 8) return {WAVES, CH};
+    PLE_NORM_SHAPES(PLE_NORM_FITS)
+#undef PLE_NORM_FITS
+    return {0, 0};
+}
+
 hipError_t launch_rms_norm8(const RmsNorm8Args& a, hipStream_t s) {
-    const int chunks = a.n / 8;
+    const RmsNorm8Shape f = rms_norm8_shape(a.n);
+    const dim3 grid = block_grid(f.waves == 1 ? (a.T + 3) / 4 : a.T);
 #define PLE_NORM_LAUNCH(WAVES, CH)                                                                                        \
-    if (chunks <= WAVES * kWave * CH) {                                                                                   \
-        const dim3 grid = block_grid(WAVES == 1 ? (a.T + 3) / 4 : a.T);                                                   \
-        hipLaunchKernelGGL(rms_norm8_##WAVES##x##CH##_kernel, grid, dim3(WAVES == 1 ? 256 : WAVES * kWave), 0, s, a);     \
-        return hipGetLastError();                                                                                         \
-    }
+    if (f.waves == WAVES && f.chunks == CH)                                                                               \
+        hipLaunchKernelGGL(rms_norm8_##WAVES##x##CH##_kernel, grid, dim3(WAVES == 1 ? 256 : WAVES * kWave), 0, s, a);
     PLE_NORM_SHAPES(PLE_NORM_LAUNCH)
 #undef PLE_NORM_LAUNCH
-    hipLaunchKernelGGL(rms_norm8_long_kernel, block_grid(a.T), dim3(kLongThreads), 0, s, a);
+    if (f.waves == 0) hipLaunchKernelGGL(rms_norm8_long_kernel, grid, dim3(kLongThreads), 0, s, a);
     return hipGetLastError();
 }
 
