@@ -72,10 +72,13 @@ __device__ __forceinline__ void kv8_queries(const Kv8AttentionArgs& a, const Att
 }
 
 // The scales of a lane's block in a tile: what turns its products into base-2 exponents, log2 of the values' scale, and
-// one over it.
+// one over it.  (A block that no token was written to may have any scale; its loaded one is looked at only here, since a
+// load in a branch of its own makes the waits for those around it wait for it too.)
 struct BlockScales {
     float key, log_value, per_value;
-    __device__ __forceinline__ void set(float base, float k, float v) {
+    __device__ __forceinline__ void set(float base, float k, float v, bool bad) {
+        k = bad ? 1.f : k;
+        v = bad ? 1.f : v;
         key = base * k;
         log_value = __builtin_amdgcn_logf(v);
         per_value = __builtin_amdgcn_rcpf(v);
@@ -293,9 +296,8 @@ __device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
         walk.fetch();
         bad_next = grp < 0;
         block = grp < 0 ? 0 : grp;
-        // (a block that no token was written to may have any scale)
-        ks = grp < 0 ? 1.f : a.cache.k_scales[block];
-        vs = grp < 0 ? 1.f : a.cache.v_scales[block];
+        ks = a.cache.k_scales[block];
+        vs = a.cache.v_scales[block];
         // keys: block n / 4, token 4 i + n % 4
         const int64_t kg = __shfl((int)block, (n >> 2) * 16, kWave);
         const uint8_t* kc = a.cache.k_codes + kg * (16 * D) + g * (D / 64) * 256 + (n & 3) * 16;
@@ -321,7 +323,7 @@ __device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
         const int tg = t0 + 16 * g;  // this lane's block g of the tile
         const bool bad = bad_next;
         BlockScales c;
-        c.set(base, ks, vs);
+        c.set(base, ks, vs, bad);
 
         f32x4 s[MT][4];
 #pragma unroll
@@ -391,14 +393,33 @@ PLE_ATTN_SHAPES(PLE_ATTN_KERNEL)
 // go through the cache tiles together; each wave dequantises a quarter of a
 // tile (16 tokens of the keys, a quarter of the value elements) and leaves it
 // in LDS as finished MFMA fragments, one 16-byte read per lane each, so a tile
-// is dequantised once for 128 rows.  Two tiles in LDS: the next one is filled
-// while this one is used, with one barrier a tile.
+// is dequantised once for 128 rows.
+//
+// A wave works on half a tile (8 tokens of each of its blocks) at a time and
+// takes products and the rest in turns: beside the scores of one half stand
+// the weights of the half before it, beside the value product of a half the
+// next one's maxima, and the dequantising of the next tile.  The order is the
+// source's, step by step (each step two MFMAs, a fragment's read three steps
+// ahead, and its share of the other work): left to itself the compiler put
+// every read right in front of its use, with the whole latency of LDS between
+// MFMAs.  Two tiles in LDS, two barriers a tile.
+//
+// 1289 and 1455 tokens behind 5403 and 2004, 32 + 8 heads of 128: 237 us with
+// products and the rest one after the other and reads not ahead, 217 with
+// reads ahead, 209 in turns, 204 with the scales' loads out of their branch,
+// 197 with row tiles that move on each by themselves and the join's loads all
+// at once.  The SIMDs then issue vector instructions for 56% of the cycles and
+// their matrix cores are busy for 33%: two waves a SIMD, with all registers,
+// overlap little more.  64 rows a wave, one wave a SIMD, halve the reads of LDS
+// but take 277 us.
 // ---------------------------------------------------------------------------
 template <int D>
 struct Kv8ChunkShape {
+    static constexpr int MT = 2;
     static constexpr int KS = D / 32, NB = D / 16, WB = D / 64;  // WB: element blocks that a wave dequantises
     static constexpr int K_BYTES = 4 * KS * 1024, V_BYTES = NB * 2 * 1024;
     static constexpr int BUF = K_BYTES + V_BYTES;
+    static constexpr int AHEAD = 3;             // fragments that a wave reads ahead
     static constexpr int NANS_AT = 2 * BUF;  // whether some wave has met NaN values
     static constexpr int LDS = NANS_AT + 16;
 };
@@ -409,7 +430,7 @@ template <int D>
 __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const AttnTile& w, int r, int head, int begin,
                                                 int end, int at) {
     using Sh = Kv8ChunkShape<D>;
-    constexpr int MT = 2;
+    constexpr int MT = Sh::MT, KS = Sh::KS, NB = Sh::NB, AHEAD = Sh::AHEAD;
     extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -419,23 +440,24 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
     const int common_hi = min(end, w.before + w.row0 / a.group + 1);
     const int32_t* table_row = a.batch.page_table + (int64_t)r * a.batch.table_width;
 
-    // a tile's quarter, as loaded
+    // a tile's quarter, as loaded, and its scales
     u32x4 kraw[D / 64], vraw[Sh::WB];
     float ks, vs;
-    bool bad_next = false;
     PageWalk walk(a, table_row, head, begin + 16 * g, kTile / 16, end);
+    // of the tile to load next: the lane's block (-1: none), and block n / 4 of the tile
     int grp = -1;
-    int64_t kg = 0;  // of the tile to load next: this lane's block, and block n / 4 of the tile
+    int64_t kg = 0;
+    bool bad_loaded = false;
     auto aim = [&](int t0) {
         grp = walk.number(t0 + 16 * g, end);
         walk.fetch();
         kg = __shfl(max(grp, 0), (n >> 2) * 16, kWave);
     };
     auto load = [&]() {
-        bad_next = grp < 0;
+        bad_loaded = grp < 0;
         const int64_t safe = max(grp, 0);
-        ks = grp < 0 ? 1.f : a.cache.k_scales[safe];
-        vs = grp < 0 ? 1.f : a.cache.v_scales[safe];
+        ks = a.cache.k_scales[safe];
+        vs = a.cache.v_scales[safe];
         // keys: token 4 wave + n % 4 of block n / 4
         const uint8_t* kc = a.cache.k_codes + kg * (16 * D) + g * (D / 64) * 256 + (4 * wave + (n & 3)) * 16;
         // values: elements 16 (wave WB + b) + n of block g
@@ -446,6 +468,19 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
             vraw[c] = *(const u32x4*)(vc + c * 256);
         }
     };
+
+    f32x4 o[MT][NB];
+    float m[MT], l[MT];
+    float limit[MT], shift[MT];  // m and the slack; what brings an exponent beside m to the weights' (without a maximum: 0)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        m[mt] = limit[mt] = -__builtin_inff();
+        l[mt] = shift[mt] = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) o[mt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    bool wide = false, nans = false;  // wide: see kWide
+    if (threadIdx.x == 0) *(volatile int*)(lds + Sh::NANS_AT) = 0;
     // the first tile is on its way before the queries are
     if (begin < end) {
         walk.fetch();
@@ -453,105 +488,214 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
         load();
         aim(begin + kTile);
     }
-    BFrag q[MT][Sh::KS];
+    BFrag q[MT][KS];
     int see_lo[MT], see_hi[MT];
     kv8_queries<D, MT>(a, w, w.row0 + wave * (16 * MT), head, begin, end, q, see_lo, see_hi);
-    f32x4 o[MT][Sh::NB];
-    float m[MT], l[MT];
-    bool wide = false, nans = false;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        m[mt] = -__builtin_inff();
-        l[mt] = 0.f;
-#pragma unroll
-        for (int b = 0; b < Sh::NB; ++b) o[mt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
 
-    // whether some row does not see the whole tile (the same for the block: `bad` is the tile's four blocks)
+    // not every row of the block sees the whole tile at t0 (the same for all its waves: `bad` is the tile's four blocks)
     auto partial = [&](int t0, bool bad) {
         return t0 < common_lo || t0 < begin || t0 + kTile > common_hi || __ballot(bad) != 0;
     };
-    auto fill = [&](int t0, int buf) {
-        char* kb = lds + buf * Sh::BUF + (wave * Sh::KS) * 1024 + lane * 16;
-        char* vb = lds + buf * Sh::BUF + Sh::K_BYTES + (wave * Sh::WB * 2) * 1024 + lane * 16;
-#pragma unroll
-        for (int k = 0; k < Sh::KS; ++k) {
+    // the quarter that is loaded, into a buffer: group c of KS + 2 WB of 16 bytes a lane
+    auto fill = [&](int buf, int c) {
+        if (c < KS) {
             BFrag f;
-            fp8_to_bf16(kraw[k / 2][2 * (k & 1)], kraw[k / 2][2 * (k & 1) + 1], f);
-            *(bf16x8*)(kb + k * 1024) = f.v;
+            fp8_to_bf16(kraw[c / 2][2 * (c & 1)], kraw[c / 2][2 * (c & 1) + 1], f);
+            *(bf16x8*)(lds + buf * Sh::BUF + lane * 16 + (wave * KS + c) * 1024) = f.v;
+        } else {
+            const int b = (c - KS) / 2, h = (c - KS) & 1;
+            Frag f;
+            fp8_to_f16(vraw[b][2 * h], vraw[b][2 * h + 1], f);
+            *(u32x4*)(lds + buf * Sh::BUF + Sh::K_BYTES + lane * 16 + ((wave * Sh::WB + b) * 2 + h) * 1024) = f.u;
         }
-        if (partial(t0, bad_next)) {
-            nans |= kv8_clear<Sh::WB>(vraw, bad_next, t0 + 16 * g, w.first_seen, end);
+    };
+    constexpr int FILLS = KS + 2 * Sh::WB;
+    f32x4 s[MT][2];
+    // the scores of half h of a buffer's tile (fragment 4 i + k: tokens of MFMA i), with `beside(step)` beside them
+    auto scores = [&](int buf, int h, f32x4 (&to)[MT][2], auto beside) {
+        const char* kb = lds + buf * Sh::BUF + lane * 16 + 2 * h * KS * 1024;
+        constexpr int N = 2 * KS;
+        bf16x8 f[AHEAD];
+#pragma unroll
+        for (int c = 0; c < AHEAD; ++c) f[c] = *(const bf16x8*)(kb + c * 1024);
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                to[mt][c / KS] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    f[c % AHEAD], q[mt][c % KS].v, c % KS == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : to[mt][c / KS], 0, 0, 0);
+            if (c + AHEAD < N) f[c % AHEAD] = *(const bf16x8*)(kb + (c + AHEAD) * 1024);
+            beside(c, N);
         }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto mask = [&](int t0, int h, bool bad, f32x4 (&x)[MT][2]) {
 #pragma unroll
-        for (int b = 0; b < Sh::WB; ++b)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                Frag f;
-                fp8_to_f16(vraw[b][2 * h], vraw[b][2 * h + 1], f);
-                *(u32x4*)(vb + (b * 2 + h) * 1024) = f.u;
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int tok = t0 + 16 * g + 8 * h + 4 * i + e;
+                    if (bad || tok < see_lo[mt] || tok >= see_hi[mt]) x[mt][i][e] = -__builtin_inff();
+                }
+    };
+    // the maxima of scores that are here: step c of n
+    auto maxima = [&](const f32x4 (&x)[MT][2], float (&top)[MT], int c, int n) {
+#pragma unroll
+        for (int k = 0; k < 4 * MT; ++k)
+            if (k * n / (4 * MT) == c) {
+                const f32x4& y = x[k / 4][k / 2 % 2];
+                top[k / 4] = k % 4 == 0 ? fmaxf(y[0], y[1]) : fmaxf(fmaxf(top[k / 4], y[k % 2 * 2]), y[k % 2 * 2 + 1]);
+                asm volatile("" : "+v"(top[k / 4]));  // (at its step)
             }
     };
-
-    bool bad = false;
-    BlockScales c = {};
-    if (threadIdx.x == 0) *(volatile int*)(lds + Sh::NANS_AT) = 0;
-    if (begin < end) {
-        fill(begin, 0);
-        bad = bad_next;
-        c.set(base, ks, vs);
-    } else {
-        __syncthreads();
-    }
-    int buf = 0;
-    for (int t0 = begin; t0 < end; t0 += kTile, buf ^= 1) {
-        const bool more = t0 + kTile < end;
-        __syncthreads();  // this tile is whole; every read of the other buffer is done
-        if (more) load();
-        const char* kb = lds + buf * Sh::BUF + lane * 16;
-        const char* vb = kb + Sh::K_BYTES;
-        const bool some = partial(t0, bad);
-        f32x4 s[MT][4];
+    // Rows whose maximum passes the running one by more than the slack move on, each by itself, whatever the wave's others
+    // do (their four lanes' maxima are joined only there).
+    auto move_on = [&](const float (&top)[MT], const BlockScales& c) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int mt = 0; mt < MT; ++mt) {
+            if (__ballot(fmaf(top[mt], c.key, c.log_value) > limit[mt]) == 0) continue;
+            const float mn = quad_max(fmaf(top[mt], c.key, c.log_value));
+            const float next = mn > limit[mt] ? mn : m[mt];
+            const float by = m[mt] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m[mt] - next);
+            l[mt] *= by;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) s[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < Sh::KS; ++k) {
-                const bf16x8 f = *(const bf16x8*)(kb + (i * Sh::KS + k) * 1024);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    s[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[mt][k].v, s[mt][i], 0, 0, 0);
-            }
+            for (int b = 0; b < NB; ++b) o[mt][b] *= by;
+            m[mt] = next;
+            limit[mt] = next + kSlack;
+            shift[mt] = next == -__builtin_inff() ? 0.f : kWeightShift - next;
+            wide |= __ballot(fabsf(next) >= kWide && next != -__builtin_inff()) != 0;
         }
-        reads_ahead<4 * Sh::KS, MT>();
-        aim(t0 + 2 * kTile);
-        Frag p[MT][2];
-        kv8_softmax<Sh::NB, MT>(s, c, some, bad, t0 + 16 * g, see_lo, see_hi, m, l, o, wide, p);
+    };
+    // of the half that is weighed: weights are 2^(product * key + sub)
+    float key[MT], sub[MT], sum[MT];
+    auto weigh = [&](f32x4 (&x)[MT][2], const BlockScales& c) {
 #pragma unroll
-        for (int b = 0; b < Sh::NB; ++b)
+        for (int mt = 0; mt < MT; ++mt) {
+            key[mt] = c.key;
+            sub[mt] = c.log_value + shift[mt];
+        }
+        if (wide)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const f16x8 f = *(const f16x8*)(vb + (b * 2 + h) * 1024);
+            for (int mt = 0; mt < MT; ++mt) {
+                if (!(fabsf(m[mt]) >= kWide && m[mt] != -__builtin_inff())) continue;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    o[mt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[mt][h].v, o[mt][b], 0, 0, 0);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[mt][i][e] = fmaf(x[mt][i][e], key[mt], c.log_value) - m[mt];
+                key[mt] = 1.f;
+                sub[mt] = kWeightShift;
             }
-        reads_ahead<2 * Sh::NB, MT>();
-        if (more) {
-            fill(t0 + kTile, buf ^ 1);
+    };
+    // two of a lane's weights of each row tile at a time: step c of n
+    auto weights = [&](const f32x4 (&x)[MT][2], Frag (&p)[MT], int c, int n) {
+#pragma unroll
+        for (int k = 0; k < 4 * MT; ++k)
+            if (k * n / (4 * MT) == c) {
+                const int mt = k / 4, i = k / 2 % 2, e = k % 2 * 2;
+                const float y = __builtin_amdgcn_exp2f(fmaf(x[mt][i][e], key[mt], sub[mt]));
+                const float z = __builtin_amdgcn_exp2f(fmaf(x[mt][i][e + 1], key[mt], sub[mt]));
+                sum[mt] = k % 4 == 0 ? y + z : sum[mt] + (y + z);
+                p[mt].p[i * 2 + e / 2] = f16x2{(_Float16)y, (_Float16)z};
+                uint32_t here = p[mt].u[i * 2 + e / 2];
+                asm volatile("" : "+v"(here), "+v"(sum[mt]));  // (at their step)
+                p[mt].u[i * 2 + e / 2] = here;
+            }
+    };
+    auto weighed = [&](const BlockScales& c) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) l[mt] = fmaf(sum[mt], c.per_value, l[mt]);
+    };
+    // the value product of half h
+    auto values = [&](int buf, int h, const Frag (&p)[MT], auto beside) {
+        const char* vb = lds + buf * Sh::BUF + Sh::K_BYTES + lane * 16 + h * 1024;
+        f16x8 f[AHEAD];
+#pragma unroll
+        for (int b = 0; b < AHEAD; ++b) f[b] = *(const f16x8*)(vb + b * 2048);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                o[mt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[b % AHEAD], p[mt].v, o[mt][b], 0, 0, 0);
+            if (b + AHEAD < NB) f[b % AHEAD] = *(const f16x8*)(vb + (b + AHEAD) * 2048);
+            beside(b, NB);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto nothing = [](int, int) {};
+    if (begin < end) {
+        BlockScales c, c_next;
+        float top[MT];
+        bool bad = bad_loaded, some = partial(begin, bad), bad_next, some_next;
+        const auto clear = [&](int t0) {
+            int tg = t0 + 16 * g;
+            asm volatile("" : "+v"(tg));  // (what follows from it is formed here, not for every tile)
+            nans |= kv8_clear<Sh::WB>(vraw, bad_loaded, tg, w.first_seen, end);
+        };
+        c.set(base, ks, vs, bad);
+        if (some) clear(begin);
+#pragma unroll
+        for (int i = 0; i < FILLS; ++i) fill(0, i);
+        load();  // (past the last tile: the cache's first block, which nothing comes of)
+        aim(begin + 2 * kTile);
+        __syncthreads();
+        scores(0, 0, s, nothing);
+        if (some) mask(begin, 0, bad, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) maxima(s, top, i, 4);
+        move_on(top, c);
+        int buf = 0;
+        for (int t0 = begin;; t0 += kTile) {
+            f32x4 x[MT][2];
+            Frag p[MT];
+            // first half's weights, second half's scores
+            weigh(s, c);
+            scores(buf, 1, x, [&](int i, int n) { weights(s, p, i, n); });
+            weighed(c);
+            if (some) mask(t0, 1, bad, x);
+            bad_next = bad_loaded;
+            some_next = partial(t0 + kTile, bad_next);
+            c_next.set(base, ks, vs, bad_next);
+            if (some_next) clear(t0 + kTile);
+            __syncthreads();  // every read of the other buffer is done
+            // first half's values; second half's maxima and the next tile into LDS
+            values(buf, 0, p, [&](int i, int n) {
+                maxima(x, top, i, n);
+#pragma unroll
+                for (int k = 0; k < FILLS; ++k)
+                    if (k * n / FILLS == i) fill(buf ^ 1, k);
+            });
+            move_on(top, c);
+            load();
+            aim(t0 + 3 * kTile);
+            __syncthreads();  // the next tile is whole
+            // second half's weights, the next tile's first half's scores (where there is none: of no use)
+            weigh(x, c);
+            scores(buf ^ 1, 0, s, [&](int i, int n) { weights(x, p, i, n); });
+            weighed(c);
+            if (some_next) mask(t0 + kTile, 0, bad_next, s);
+            // second half's values, the next tile's first half's maxima
+            values(buf, 1, p, [&](int i, int n) { maxima(s, top, i, n); });
+            if (t0 + kTile >= end) break;
+            move_on(top, c_next);
+            c = c_next;
             bad = bad_next;
-            c.set(base, ks, vs);
+            some = some_next;
+            buf ^= 1;
         }
     }
 
     // (a wave has met its quarter of the elements alone)
     if (nans) *(volatile int*)(lds + Sh::NANS_AT) = 1;
     __syncthreads();
-    if (*(volatile int*)(lds + Sh::NANS_AT) != 0) {
+    nans = *(volatile int*)(lds + Sh::NANS_AT) != 0;
+    if (nans) {
         uint64_t nan[MT] = {};
         kv8_find_nans<D, MT>(a, table_row, head, begin, kTile, end, see_lo, see_hi, nan);
-        kv8_give_nans<Sh::NB>(nan, o);
+        kv8_give_nans<NB>(nan, o);
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -566,12 +710,12 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
         const int64_t orow = (w.first + i) * a.num_q_heads + hq;
         const int64_t place = at + (row - w.row0);
 #pragma unroll
-        for (int b = 0; b < Sh::NB; ++b) {
-            const f32x4 x = o[mt][b] * inv;
+        for (int b = 0; b < NB; ++b) {
+            const f32x4 v = o[mt][b] * inv;
             if (at < 0)
-                *(u32x2*)(a.out + orow * D + b * 16 + g * 4) = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+                *(u32x2*)(a.out + orow * D + b * 16 + g * 4) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
             else
-                *(f32x4*)(a.part + place * D + b * 16 + g * 4) = x;
+                *(f32x4*)(a.part + place * D + b * 16 + g * 4) = v;
         }
         if (g == 0) {
             if (at >= 0)

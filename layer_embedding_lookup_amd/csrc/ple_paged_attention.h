@@ -360,41 +360,68 @@ __device__ __forceinline__ void attn_join_waves(const A& a, const AttnTile& w, i
     }
 }
 
+// The same in scalar registers: all of it is the wave's.
+__device__ __forceinline__ AttnTile uniform(const AttnTile& w) {
+    const auto u = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+    return {u((int)w.first), u(w.n), u(w.len), u(w.before), u(w.row0), u(w.row1), u(w.first_seen), u(w.lo), u(w.hi)};
+}
+
 // The pieces (each by `piece`) of share b of the line; the line without shares (flat = 0): one whole query tile.
 template <class A, class Piece>
 __device__ __forceinline__ void attn_chunk_body(const A& a, Piece piece) {
     AttnTile w;
-    int r, head, tile, count, k0 = 0, line = 0, stop = 1;
+    int r, head, tile, k0 = 0, left = 1;
     // blocks of an XCD (block number mod 8) take neighbouring shares, which read the same heads
     const int share = (a.flat & 7) == 0 ? (int)(blockIdx.x & 7) * (a.flat >> 3) + (int)(blockIdx.x >> 3) : (int)blockIdx.x;
-    AttnFlat f;
     attn_idle_tokens(a);
     if (a.flat == 0) {
         attn_block(a, r, head, tile);
         attn_request(a, r, w);
         if (!attn_tile(a, tile, w)) return;
     } else {
+        AttnFlat f;
         f.lay_out(a);
-        line = share * f.quota;
-        stop = min(f.total, line + f.quota);
+        const int line = share * f.quota;
+        left = min(f.total - line, f.quota);
+        if (left <= 0) return;
+        int count;
+        f.find(a, line, r, head, w, k0, count);
+        tile = w.row0 / kChunkRows;
     }
-    while (line < stop) {
-        int begin = w.lo, end = w.hi, at = -1, take = 1;
+    r = __builtin_amdgcn_readfirstlane(r);
+    head = __builtin_amdgcn_readfirstlane(head);
+    tile = __builtin_amdgcn_readfirstlane(tile);
+    k0 = __builtin_amdgcn_readfirstlane(k0);
+    left = __builtin_amdgcn_readfirstlane(left);
+    for (;;) {
+        w = uniform(w);
+        int begin = w.lo, end = w.hi, at = -1;
         if (a.flat != 0) {
-            f.find(a, line, r, head, w, k0, count);
-            if (k0 < 0) {
-                line -= k0;
+            if (k0 < 0) {  // places in front of the query tile's cache tiles
+                left += k0;
                 k0 = 0;
-                if (line >= stop) break;
+                if (left <= 0) return;
             }
-            take = max(1, min(count - k0, stop - line));
+            const int count = AttnFlat::count(w), take = max(1, min(count - k0, left));
             begin = w.lo + k0 * kTile;
             end = min(w.hi, begin + take * kTile);
             if (take != count) at = (2 * share + (k0 == 0)) * kChunkRows;
+            left -= take;
         }
         __syncthreads();  // the last piece's reads of LDS
         piece(w, r, head, begin, end, at);
-        line += take;
+        if (a.flat == 0 || left <= 0) return;
+        // the next query tile of the line
+        k0 = -kFlatStart;
+        ++tile;
+        while (tile >= a.tiles || !attn_tile(a, tile, w)) {
+            tile = 0;
+            if (++head == a.cache.num_kv_heads) {
+                head = 0;
+                if (++r == a.batch.num_reqs) return;
+                attn_request(a, r, w);
+            }
+        }
     }
 }
 
@@ -533,20 +560,45 @@ __device__ __forceinline__ void attn_flat_join_body(const A& a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) v[i][e] = 0.f;
     }
-    for (int k = 0; k < pieces; ++k)
+    const auto place = [&](int k, int i) {
+        return (int64_t)(2 * (s0 + k) + (k == 0)) * kChunkRows + min(in0 + i, most);
+    };
+    const auto add = [&](int i, float l, const float (&x)[E]) {
+        const float by = l == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(l - top[i]);  // NaN stays
+        total[i] += by;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            top[i] = fmaxf(top[i], all_lse[(int64_t)(2 * (s0 + k) + (k == 0)) * kChunkRows + min(in0 + i, most)]);
-    for (int k = 0; k < pieces; ++k)
+        for (int e = 0; e < E; ++e) v[i][e] = fmaf(x[e], by, v[i][e]);
+    };
+    if (pieces == 2) {  // (nearly all) everything on its way at once
+        float l[2][N], x[2][N][E];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                l[k][i] = all_lse[place(k, i)];
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[k][i][e] = a.part[place(k, i) * D + lane * E + e];
+            }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int64_t place = (int64_t)(2 * (s0 + k) + (k == 0)) * kChunkRows + min(in0 + i, most);
-            const float l = all_lse[place];
-            const float by = l == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(l - top[i]);  // NaN stays
-            total[i] += by;
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[i][e] = fmaf(a.part[place * D + lane * E + e], by, v[i][e]);
+            top[i] = fmaxf(fmaxf(top[i], l[0][i]), l[1][i]);
+            add(i, l[0][i], x[0][i]);
+            add(i, l[1][i], x[1][i]);
         }
+    } else {
+        for (int k = 0; k < pieces; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) top[i] = fmaxf(top[i], all_lse[place(k, i)]);
+        for (int k = 0; k < pieces; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float l = all_lse[place(k, i)];
+                float x[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] = a.part[place(k, i) * D + lane * E + e];
+                add(i, l, x);
+            }
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int row = w.row0 + in0 + i;
