@@ -752,6 +752,23 @@ PLE_ATTN_KERNEL(128)
 PLE_ATTN_KERNEL(256)
 #undef PLE_ATTN_KERNEL
 
+// Many rows: their query tiles are cut into equal shares where the shortest of a call go through many cache tiles.  Shares
+// cost finding and joining, 25 to 45 us; a block a query tile leaves CUs to wait for the last ones, which are the shortest
+// since the longest go first.  In shares and a block each, by how far the new tokens stand into the cache at most: 100 and
+// 2 x 1000 new tokens behind 1000 40 and 40, 122 and 119 us; 8 x 200 behind 1200 70 and 59; 8 x 500 behind 1500 146 and 128;
+// 16 x 300 behind 2000 177 and 196; 3 x 500 behind 2500 67 and 79; 2 x 1500 behind 5000 197 and 269; 8 x 1000, 2000 and 4000
+// behind nothing 220 and 183, 89 and 69, 204 and 178; 4 x 800 behind 900, D = 64, 101 and 79.  (100 behind 1400 44 and 49: on
+// the wrong side of it.)  With heads of 256, one block per CU, shares gain from fewer on: 4 x 1000 behind 500, 1000 and 1500
+// 144 and 174, 162 and 239, 238 and 271, 100 behind 600 and 1200 52 and 48, 55 and 76, 2 x 500 behind 400 58 and 52.  Beyond
+// 2048 query tiles a block each: 30 x 300 behind 3000 (2400 tiles) 460 and 435.
+constexpr int kFlatPast = 1536, kFlatPastWide = 384, kFlatMostTiles = 2048;
+
+// Few rows: splits of at least 1024 tokens (8 requests of up to 2500 tokens 15.9 us, with 512 15.6, 2048 16.3; one of 777
+// 11.0, 15.4, 11.3; one of 10000 16.5, 16.1, 18.1; 8 x 4 windows over 9000 19.1, 19.1, 23.6).  Up to one block per CU blocks of
+// eight waves (one of 100100 tokens 45.3 us, of four in more splits 49.0; verify windows 64 x 4 18.3 and 23.9; 32 over 2000
+// 17.3 and 21.1; two of eight waves per CU: the windows 30.7, 4 over 20000 22.7 for 18.5).  Blocks of four waves in as many
+// splits as two to four of them per CU: 16 rows and 512, 768 or 1024 slots: 33 requests over 8000 65.6, 69.7 and 61.4 us, 40
+// over 4000 47.5, 41.5 and 40.3, 64 over 8000 109.4, 109.5 and 112.4.
 void plan_kv8_attention(Kv8AttentionArgs& a) {
     const int64_t T = a.batch.num_tokens, R = a.batch.num_reqs;
     const int64_t cover = (int64_t)a.batch.table_width * a.cache.page_size;
@@ -761,13 +778,16 @@ void plan_kv8_attention(Kv8AttentionArgs& a) {
     const int64_t rows = new_max * a.group;
     a.rows = rows <= 16 || (rows <= 64 && a.cache.head_dim == 256) ? 16 : (rows <= 64 ? 32 : kChunkRows);
     a.tiles = (int)((rows + a.rows - 1) / a.rows);
+    int64_t past = len - new_max;  // cache tokens of the shortest query tiles
     if (a.window > 0) {
         const int64_t span = (int64_t)a.window + a.rows / a.group + 1 + 15;
         len = len < span ? len : span;
+        past = past < len ? past : len;
     }
     const int64_t blocks = R * a.cache.num_kv_heads * a.tiles;
     // (the line's length has to fit 32 bits whatever the hints say)
-    if (a.rows == kChunkRows && R <= kWave && blocks > 0 && blocks <= kFlatUnits &&
+    if (a.rows == kChunkRows && R <= kWave && blocks > 0 && blocks <= kFlatMostTiles &&
+        past >= (a.cache.head_dim == 256 ? kFlatPastWide : kFlatPast) &&
         blocks * (cover / kTile + 2 + kFlatStart) < ((int64_t)1 << 30)) {
         const int64_t most = blocks * ((len + kTile - 1) / kTile + 1 + kFlatStart), slots = a.cache.head_dim == 256 ? 256 : 512;
         const int64_t shares = (most + kFlatLeast - 1) / kFlatLeast;

@@ -11,9 +11,14 @@ import bits8_util as U
 import test_bits8_gpu as G
 from layer_embedding_lookup_amd import build as B
 from layer_embedding_lookup_amd import capi
-from test_fp4_kernels import ATTENTION, hints, width
+from test_fp4_kernels import ATTENTION as OF_4_BITS
+from test_fp4_kernels import Case, hints, width
 
 BF = torch.bfloat16
+# (many rows far into the cache, in shares: with two and with three pieces of a query tile)
+ATTENTION = OF_4_BITS + [c for D in (64, 128, 256) for c in (
+    Case(D, 8, 2, [90, 33], [1900, 700], bad=((0, 20, 40),)), Case(D, 8, 1, [60, 33], [9000, 1100]),
+    Case(D, 4, 1, [200], [4000], window=1700, bad=((0, 200, 210),)))]
 NORM = [16, 512, 528, 2048, 2064, 4096, 4112, 8192, 8208, 16384, 16400]
 
 
