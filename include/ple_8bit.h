@@ -92,6 +92,8 @@ typedef ple_kv4_batch ple_kv8_batch;
  *   code = e4m3(x / s) to nearest, ties to even, beyond 448 to 448; NaN for infinities and NaN.
  * Where the scale grows, the codes of those earlier tokens become
  * e4m3(value / s); between powers of two that changes only values below 2^-6 s.
+ * Scales that this call makes are powers of two; one that a caller brought along
+ * and that is not enters as fp32 quotients, x * (1 / s) and code * (its / s).
  * Tokens of the block behind the new ones are as good as gone (their scale may
  * have changed).  A page that two requests of the batch write to holds
  * unspecified values.  Other arguments as for ple_kv4_append;

@@ -18,6 +18,14 @@
 // the angle, needs no reduction by pi.  A thread forms sine and cosine of its
 // first new token of four and of the step from one token to the next; the
 // others follow by products (2^-51 after three).
+//
+// Bound by bytes where tokens are many: 8178 tokens, 32 + 8 heads of 128, half
+// of each rotated: 42 us for 184 MB in and out (4.4 TB/s), back out of the cache
+// 13.6 us for 50 MB.  256 single tokens 10.6 and 9.6 us: a chain of loads that
+// depend on each other (offsets, length, page, scale, codes), each to memory,
+// and a whole 2 KiB block of a head's values where one token is read or its
+// scale grows, since a lane's 16 bytes are one element of 16 tokens, as
+// attention takes them.
 #include "ple_8bit_launch.h"
 #include "ple_rotate.h"
 

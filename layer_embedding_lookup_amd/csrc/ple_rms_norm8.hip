@@ -11,8 +11,10 @@
 // from it, half a step of the quotient, which lies below 2^(8+d); the
 // corrected quotient is off by 2^-22 of a step before its rounding.)
 //
-// Bound by bytes.  A row stays in its block's registers between the sums and
-// the codes; sum and maximum of a row are joined in one exchange.
+// Bound by bytes: 7984 rows of 4096 with a residual 43.4 us, 5.3 TB/s (a copy
+// reaches 6.3); a single row 2.9 us, launch and two rounds of memory latency.
+// A row stays in its block's registers between the sums and the codes; sum and
+// maximum of a row are joined in one exchange.
 #include "ple_8bit_launch.h"
 
 namespace ple {
@@ -169,8 +171,11 @@ __global__ __launch_bounds__(kLongThreads) void rms_norm8_long_kernel(RmsNorm8Ar
     if (threadIdx.x == 0) a.scales[t] = s.scale;
 }
 
-// Waves a row, chunks a lane: rows of up to 512 elements a wave each, then four waves, up to 16384 eight.
-#define PLE_NORM_SHAPES(X) X(1, 1) X(4, 1) X(4, 2) X(4, 4) X(8, 4)
+// Waves a row, chunks a lane: as many waves as leave a lane one chunk up to 4096 elements, then two (4000 rows of 8192 in
+// eight waves 44.1 us, in four 48.6; 2000 of 16384 in sixteen 45.7, in eight 47.8; 7984 of 4096 in eight 43.4, four 44.5, two
+// 49.2, one 54.5; one of 4096 2.9, 3.1, 3.9, 5.4; but 8000 of 2048 in four 23.9, in eight, half of whose lanes idle, 27.7; 8000
+// of 512 in one 8.4, in four 11.9).  Longer rows are read again: 500 of 32000 29 us.
+#define PLE_NORM_SHAPES(X) X(1, 1) X(4, 1) X(8, 1) X(8, 2) X(16, 2)
 #define PLE_NORM_KERNEL(WAVES, CH)                                                                                         \
     __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * kWave) void rms_norm8_##WAVES##x##CH##_kernel(RmsNorm8Args a) { \
         norm_body<WAVES, CH>(a);                                                                                           \
