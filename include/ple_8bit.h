@@ -95,8 +95,8 @@ typedef ple_kv4_batch ple_kv8_batch;
  * Scales that this call makes are powers of two; one that a caller brought along
  * and that is not enters as fp32 quotients, x * (1 / s) and code * (its / s).
  * Tokens of the block behind the new ones are as good as gone (their scale may
- * have changed).  A page that two requests of the batch write to holds
- * unspecified values.  Other arguments as for ple_kv4_append;
+ * have changed).  A page that the batch writes to in two places, of two requests
+ * or twice in one's table row, holds unspecified values.  Other arguments as for ple_kv4_append;
  * max_request_tokens sizes the launch.
  */
 int ple_kv8_append(const ple_kv8_cache* cache, const ple_kv8_batch* batch, const uint16_t* k, int64_t k_stride,
