@@ -159,7 +159,7 @@ struct PageWalk {
 // tiles (at least one each), in the order request, key head, query tile, are one line that `flat` blocks cut into equal
 // shares; a query tile has kFlatStart places in front of its cache tiles.  A query tile whose cache tiles a cut goes
 // through is joined by a second kernel: of its pieces the one that begins it is partial result 2 * share + 1, every
-// other 2 * share of its share.
+// other 2 * share of its share.  The share that begins it leaves word of it (AttnCut) behind the partial results.
 // A chunk of 1289 + 1455 tokens at 5403 and 2004: 308 us with a block a query tile (CUs busy for 53% of it).
 struct AttnFlat {
     // of lane r:
@@ -360,6 +360,20 @@ __device__ __forceinline__ void attn_join_waves(const A& a, const AttnTile& w, i
     }
 }
 
+// The query tile that a share begins and does not finish: its pieces (0: there is none), its request's first new token, its
+// key head, first row and rows.
+struct AttnCut {
+    int pieces, first, head, row0, rows, unused[3];
+};
+template <class A>
+__host__ __device__ __forceinline__ size_t attn_flat_floats(const A& a) {
+    return (size_t)2 * a.flat * kChunkRows * (a.cache.head_dim + 1);
+}
+template <class A>
+__device__ __forceinline__ AttnCut* attn_cuts(const A& a) {
+    return (AttnCut*)(a.part + attn_flat_floats(a));
+}
+
 // The same in scalar registers: all of it is the wave's.
 __device__ __forceinline__ AttnTile uniform(const AttnTile& w) {
     const auto u = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
@@ -370,7 +384,7 @@ __device__ __forceinline__ AttnTile uniform(const AttnTile& w) {
 template <class A, class Piece>
 __device__ __forceinline__ void attn_chunk_body(const A& a, Piece piece) {
     AttnTile w;
-    int r, head, tile, k0 = 0, left = 1;
+    int r, head, tile, k0 = 0, left = 1, quota = 0;
     // blocks of an XCD (block number mod 8) take neighbouring shares, which read the same heads
     const int share = (a.flat & 7) == 0 ? (int)(blockIdx.x & 7) * (a.flat >> 3) + (int)(blockIdx.x >> 3) : (int)blockIdx.x;
     attn_idle_tokens(a);
@@ -379,10 +393,12 @@ __device__ __forceinline__ void attn_chunk_body(const A& a, Piece piece) {
         attn_request(a, r, w);
         if (!attn_tile(a, tile, w)) return;
     } else {
+        if (threadIdx.x == 0) attn_cuts(a)[share].pieces = 0;
         AttnFlat f;
         f.lay_out(a);
-        const int line = share * f.quota;
-        left = min(f.total - line, f.quota);
+        quota = __builtin_amdgcn_readfirstlane(f.quota);
+        const int line = share * quota;
+        left = min(f.total - line, quota);
         if (left <= 0) return;
         int count;
         f.find(a, line, r, head, w, k0, count);
@@ -407,6 +423,8 @@ __device__ __forceinline__ void attn_chunk_body(const A& a, Piece piece) {
             end = min(w.hi, begin + take * kTile);
             if (take != count) at = (2 * share + (k0 == 0)) * kChunkRows;
             left -= take;
+            if (k0 == 0 && take != count && threadIdx.x == 0)
+                attn_cuts(a)[share] = {1 + (count - take + quota - 1) / quota, (int)w.first, head, w.row0, w.row1 - w.row0, {}};
         }
         __syncthreads();  // the last piece's reads of LDS
         piece(w, r, head, begin, end, at);
@@ -528,30 +546,15 @@ template <int D, class A>
 __device__ __forceinline__ void attn_flat_join_body(const A& a) {
     constexpr int E = D / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int r, head, tile;
-    attn_block(a, r, head, tile);
-    AttnTile w;
-    attn_request(a, r, w);
-    if (!attn_tile(a, tile, w)) return;
-    if (w.row0 + (int)blockIdx.y * kFlatJoinRows >= w.row1) return;
-    const int count = AttnFlat::count(w);
-    AttnFlat f;
-    f.lay_out(a);
-    int sum = 0;
-    {
-        AttnTile u = w;
-        for (int t = lane; t < tile; t += kWave) sum += AttnFlat::places(a, t, u);
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
-    }
-    const int at = __builtin_amdgcn_readlane(f.before, r) + head * __builtin_amdgcn_readlane(f.tiles_of, r) + sum;
-    const int s0 = (at + kFlatStart) / f.quota, pieces = (at + kFlatStart + count - 1) / f.quota - s0 + 1;
-    if (pieces == 1) return;
+    const int s0 = blockIdx.x;
+    const AttnCut cut = attn_cuts(a)[s0];
+    const int pieces = cut.pieces, head = cut.head;
+    if (pieces == 0 || (int)blockIdx.y * kFlatJoinRows >= cut.rows) return;
     const float* const all_lse = a.part + (int64_t)2 * a.flat * kChunkRows * D;
     const float vscale = value_scale(a, head);
     // a wave takes eight rows at once, so that their loads are in flight together (rows past the tile's end repeat its last)
     constexpr int N = kFlatJoinRows / kAttnWaves;
-    const int in0 = (int)blockIdx.y * kFlatJoinRows + wave * N, most = w.row1 - w.row0 - 1;
+    const int in0 = (int)blockIdx.y * kFlatJoinRows + wave * N, most = cut.rows - 1;
     float top[N], total[N], v[N][E];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -601,10 +604,9 @@ __device__ __forceinline__ void attn_flat_join_body(const A& a) {
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int row = w.row0 + in0 + i;
-        if (row >= w.row1) break;
-        const int t = row / a.group, hq = head * a.group + (row - t * a.group);
-        attn_join_store<D>(a, (w.first + t) * a.num_q_heads + hq, top[i], total[i], vscale, v[i]);
+        if (in0 + i > most) break;
+        const int row = cut.row0 + in0 + i, t = row / a.group, hq = head * a.group + (row - t * a.group);
+        attn_join_store<D>(a, ((int64_t)cut.first + t) * a.num_q_heads + hq, top[i], total[i], vscale, v[i]);
     }
 }
 
@@ -621,7 +623,7 @@ int64_t join_blocks(const A& a) {
 
 template <class A>
 size_t attention_part_bytes(const A& a) {
-    if (a.flat > 0) return (size_t)2 * a.flat * kChunkRows * (a.cache.head_dim + 1) * sizeof(float);
+    if (a.flat > 0) return attn_flat_floats(a) * sizeof(float) + a.flat * sizeof(AttnCut);
     if (a.splits <= 1) return 0;
     return (size_t)a.batch.num_tokens * a.num_q_heads * a.splits * (a.cache.head_dim + 1) * sizeof(float);
 }
@@ -629,8 +631,8 @@ size_t attention_part_bytes(const A& a) {
 // Most threads along x of the call's launches.
 template <class A>
 int64_t attention_threads(const A& a) {
-    // (the shares are at most 512 blocks, their join a block per unit)
-    const int64_t own = attention_units(a) * (a.flat > 0 ? 256 : a.waves * kWave);
+    // (shares and their join are at most 512 blocks)
+    const int64_t own = a.flat > 0 ? a.flat * 256 : attention_units(a) * a.waves * kWave;
     const int64_t join = a.splits > 1 ? join_blocks(a) * 256 : 0;
     return own > join ? own : join;
 }
@@ -648,7 +650,7 @@ hipError_t launch_attention(const A& a, int threads, hipStream_t s) {
 template <class A>
 hipError_t launch_attention_join(const A& a, void (*few)(A), void (*many)(A), void (*flat)(A), hipStream_t s) {
     if (a.flat > 0)
-        hipLaunchKernelGGL(flat, dim3((unsigned)attention_units(a), kChunkRows / kFlatJoinRows), dim3(256), 0, s, a);
+        hipLaunchKernelGGL(flat, dim3((unsigned)a.flat, kChunkRows / kFlatJoinRows), dim3(256), 0, s, a);
     else if (a.splits > 1)
         hipLaunchKernelGGL(a.splits <= kFewSplits ? few : many, dim3((unsigned)join_blocks(a)), dim3(256), 0, s, a);
     return hipGetLastError();
