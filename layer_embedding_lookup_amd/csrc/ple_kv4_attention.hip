@@ -397,7 +397,7 @@ PLE_ATTN_SHAPES(PLE_ATTN_KERNEL)
 // dequantised once for 128 rows.  Two tiles in LDS: the next one is filled
 // while this one is used, with one barrier a tile.  Two blocks per CU cover
 // each other's softmax (D = 256: one).  1289 + 1455 tokens at 5403 and 2004,
-// 32 heads of 128: 225 us, 0.58 PFLOP/s, 24 of them the join of cut tiles.  A
+// 32 heads of 128: 223 us, 0.59 PFLOP/s, 20 of them the join of cut tiles.  A
 // CU's eight waves take about 7300 cycles for a tile each.  In those a SIMD's
 // products are 2048 and its other vector instructions (softmax, dequantising)
 // about 3300; LDS is busy for 1750, almost without bank conflicts.  Without

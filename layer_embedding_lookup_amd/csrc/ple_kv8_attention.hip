@@ -413,10 +413,11 @@ PLE_ATTN_SHAPES(PLE_ATTN_KERNEL)
 // products and the rest one after the other and reads not ahead, 217 with
 // reads ahead, 209 in turns, 204 with the scales' loads out of their branch,
 // 197 with row tiles that move on each by themselves and the join's loads all
-// at once (0.67 PFLOP/s, 28 of them the join).  The SIMDs then issue vector
-// instructions for 55% of the cycles that a CU is busy and their matrix cores
-// are for 34%: two waves a SIMD, with all registers, overlap little more.  64 rows a wave, one wave a SIMD, halve the reads of LDS
-// but take 277 us.
+// at once, 188 with the join told where cuts are (0.7 PFLOP/s, 20 of them the
+// join).  The SIMDs then issue vector instructions for 55% of the cycles that a
+// CU is busy and their matrix cores are for 34%: two waves a SIMD, with all
+// registers, overlap little more.  64 rows a wave, one wave a SIMD, halve the
+// reads of LDS but take 277 us.
 // ---------------------------------------------------------------------------
 template <int D>
 struct Kv8ChunkShape {
@@ -757,16 +758,17 @@ PLE_ATTN_KERNEL(128)
 PLE_ATTN_KERNEL(256)
 #undef PLE_ATTN_KERNEL
 
-// Many rows: their query tiles are cut into equal shares where the shortest of a call go through many cache tiles.  Shares
-// cost finding and joining, 25 to 45 us; a block a query tile leaves CUs to wait for the last ones, which are the shortest
-// since the longest go first.  In shares and a block each, by how far the new tokens stand into the cache at most: 100 and
-// 2 x 1000 new tokens behind 1000 40 and 40, 122 and 119 us; 8 x 200 behind 1200 70 and 59; 8 x 500 behind 1500 146 and 128;
-// 16 x 300 behind 2000 177 and 196; 3 x 500 behind 2500 67 and 79; 2 x 1500 behind 5000 197 and 269; 8 x 1000, 2000 and 4000
-// behind nothing 220 and 183, 89 and 69, 204 and 178; 4 x 800 behind 900, D = 64, 101 and 79.  (100 behind 1400 44 and 49: on
-// the wrong side of it.)  With heads of 256, one block per CU, shares gain from fewer on: 4 x 1000 behind 500, 1000 and 1500
-// 144 and 174, 162 and 239, 238 and 271, 100 behind 600 and 1200 52 and 48, 55 and 76, 2 x 500 behind 400 58 and 52.  Beyond
-// 2048 query tiles a block each: 30 x 300 behind 3000 (2400 tiles) 460 and 435.
-constexpr int kFlatPast = 1536, kFlatPastWide = 384, kFlatMostTiles = 2048;
+// Many rows: their query tiles are cut into equal shares where the shortest of a call go through many cache tiles, or where
+// there are many.  Shares cost finding and joining, 15 to 30 us; a block a query tile leaves CUs to wait for the last ones,
+// which are the shortest since the longest go first.  In shares and a block each, new tokens behind cached ones: 100 behind
+// 1000 and 1400 38.2 and 39.6, 42.1 and 48.3 us; 2 x 1000 behind 1000 119 and 122; 8 x 200 behind 1200 65 and 59; 8 x 500
+// behind 1500 122 and 127; 16 x 300 behind 2000 160 and 196; 2 x 1500 behind 5000 200 and 269; 100, 1000, 2000 and 4000 behind
+// nothing (32 to 1000 query tiles) 28 and 14, 53 and 39, 87 and 69, 196 and 175; 8 x 1000 behind nothing and 16 x 480 behind
+// 500 (2000 tiles) 175 and 183, 148 and 160; 30 x 300 behind 3000 (2400) 424 and 432; 4 x 800 behind 900, D = 64, 88 and 80.
+// With heads of 256, one block per CU, shares gain from fewer on: 2000 and 4 x 1000 behind nothing (250 and 500 tiles) 100 and
+// 111, 105 and 122; 4 x 1000 behind 1000 153 and 245; 100 behind 600 and 1200 50 and 49, 52 and 78; 2 x 500 behind 400 56 and 53.
+constexpr int kFlatPast = 1280, kFlatPastWide = 384;  // cache tokens of the shortest query tiles
+constexpr int kFlatTiles = 1536, kFlatTilesWide = 192;
 
 // Few rows: splits of at least 1024 tokens (8 requests of up to 2500 tokens 15.9 us, with 512 15.6, 2048 16.3; one of 777
 // 11.0, 15.4, 11.3; one of 10000 16.5, 16.1, 18.1; 8 x 4 windows over 9000 19.1, 19.1, 23.6).  Up to one block per CU blocks of
@@ -791,8 +793,9 @@ void plan_kv8_attention(Kv8AttentionArgs& a) {
     }
     const int64_t blocks = R * a.cache.num_kv_heads * a.tiles;
     // (the line's length has to fit 32 bits whatever the hints say)
-    if (a.rows == kChunkRows && R <= kWave && blocks > 0 && blocks <= kFlatMostTiles &&
-        past >= (a.cache.head_dim == 256 ? kFlatPastWide : kFlatPast) &&
+    const bool wide = a.cache.head_dim == 256;
+    if (a.rows == kChunkRows && R <= kWave && blocks > 0 && blocks <= kFlatUnits &&
+        (past >= (wide ? kFlatPastWide : kFlatPast) || blocks >= (wide ? kFlatTilesWide : kFlatTiles)) &&
         blocks * (cover / kTile + 2 + kFlatStart) < ((int64_t)1 << 30)) {
         const int64_t most = blocks * ((len + kTile - 1) / kTile + 1 + kFlatStart), slots = a.cache.head_dim == 256 ? 256 : 512;
         const int64_t shares = (most + kFlatLeast - 1) / kFlatLeast;
