@@ -589,18 +589,33 @@ __device__ __forceinline__ void attn_flat_join_body(const A& a) {
             add(i, l[1][i], x[1][i]);
         }
     } else {
-        for (int k = 0; k < pieces; ++k)
+        // (two pieces' loads on their way at a time; past the last one it is read again, which a maximum does not mind)
+        for (int k = 0; k < pieces; k += 2) {
+            float l[2][N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) top[i] = fmaxf(top[i], all_lse[place(k, i)]);
-        for (int k = 0; k < pieces; ++k)
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < N; ++i) l[u][i] = all_lse[place(min(k + u, pieces - 1), i)];
+#pragma unroll
+            for (int i = 0; i < N; ++i) top[i] = fmaxf(fmaxf(top[i], l[0][i]), l[1][i]);
+        }
+        for (int k = 0; k < pieces; k += 2) {
+            float l[2][N], x[2][N][E];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int64_t at = place(min(k + u, pieces - 1), i);
+                    l[u][i] = all_lse[at];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) x[u][i][e] = a.part[at * D + lane * E + e];
+                }
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float l = all_lse[place(k, i)];
-                float x[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) x[e] = a.part[place(k, i) * D + lane * E + e];
-                add(i, l, x);
+                add(i, l[0][i], x[0][i]);
+                if (k + 1 < pieces) add(i, l[1][i], x[1][i]);
             }
+        }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
