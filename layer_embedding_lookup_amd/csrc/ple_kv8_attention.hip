@@ -413,8 +413,8 @@ PLE_ATTN_SHAPES(PLE_ATTN_KERNEL)
 // products and the rest one after the other and reads not ahead, 217 with
 // reads ahead, 209 in turns, 204 with the scales' loads out of their branch,
 // 197 with row tiles that move on each by themselves and the join's loads all
-// at once, 188 with the join told where cuts are (0.7 PFLOP/s, 20 of them the
-// join).  The SIMDs then issue vector instructions for 55% of the cycles that a
+// at once, 188 with the join told where cuts are, 184 with two pieces of it at a
+// time (0.71 PFLOP/s, 17 of them the join).  The SIMDs then issue vector instructions for 55% of the cycles that a
 // CU is busy and their matrix cores are for 34%: two waves a SIMD, with all
 // registers, overlap little more.  64 rows a wave, one wave a SIMD, halve the
 // reads of LDS but take 277 us.
@@ -759,15 +759,15 @@ PLE_ATTN_KERNEL(256)
 #undef PLE_ATTN_KERNEL
 
 // Many rows: their query tiles are cut into equal shares where the shortest of a call go through many cache tiles, or where
-// there are many.  Shares cost finding and joining, 15 to 30 us; a block a query tile leaves CUs to wait for the last ones,
+// there are many.  Shares cost finding and joining, 10 to 25 us; a block a query tile leaves CUs to wait for the last ones,
 // which are the shortest since the longest go first.  In shares and a block each, new tokens behind cached ones: 100 behind
-// 1000 and 1400 38.2 and 39.6, 42.1 and 48.3 us; 2 x 1000 behind 1000 119 and 122; 8 x 200 behind 1200 65 and 59; 8 x 500
-// behind 1500 122 and 127; 16 x 300 behind 2000 160 and 196; 2 x 1500 behind 5000 200 and 269; 100, 1000, 2000 and 4000 behind
-// nothing (32 to 1000 query tiles) 28 and 14, 53 and 39, 87 and 69, 196 and 175; 8 x 1000 behind nothing and 16 x 480 behind
-// 500 (2000 tiles) 175 and 183, 148 and 160; 30 x 300 behind 3000 (2400) 424 and 432; 4 x 800 behind 900, D = 64, 88 and 80.
-// With heads of 256, one block per CU, shares gain from fewer on: 2000 and 4 x 1000 behind nothing (250 and 500 tiles) 100 and
-// 111, 105 and 122; 4 x 1000 behind 1000 153 and 245; 100 behind 600 and 1200 50 and 49, 52 and 78; 2 x 500 behind 400 56 and 53.
-constexpr int kFlatPast = 1280, kFlatPastWide = 384;  // cache tokens of the shortest query tiles
+// 1000 and 1400 33 and 40, 34 and 48 us; 2 x 1000 behind 1000 114 and 118; 8 x 200 behind 1200 62 and 59; 8 x 500 behind 1500
+// 122 and 127; 16 x 300 behind 2000 160 and 195; 2 x 1500 behind 5000 196 and 269; 100, 1000, 2000 and 4000 behind nothing (32
+// to 1000 query tiles) 28 and 14, 50 and 39, 84 and 70, 192 and 172; 8 x 1000 behind nothing and 16 x 480 behind 500 (2000
+// tiles) 175 and 183, 146 and 158; 30 x 300 behind 3000 (2400) 428 and 435; 4 x 800 behind 900, D = 64, 88 and 80.  With heads
+// of 256, one block per CU, shares gain from fewer on: 2000 and 4 x 1000 behind nothing (250 and 500 tiles) 101 and 111, 107
+// and 122; 4 x 1000 behind 1000 156 and 244; 100 behind 600 and 1200 48 and 49, 50 and 78; 2 x 500 behind 400 55 and 54.
+constexpr int kFlatPast = 896, kFlatPastWide = 384;  // cache tokens of the shortest query tiles
 constexpr int kFlatTiles = 1536, kFlatTilesWide = 192;
 
 // Few rows: splits of at least 1024 tokens (8 requests of up to 2500 tokens 15.9 us, with 512 15.6, 2048 16.3; one of 777
