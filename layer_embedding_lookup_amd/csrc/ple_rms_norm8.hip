@@ -9,7 +9,12 @@
 // never on the wrong side of a border.  (u = U 2^i, a = A 2^j, U and A below
 // 2^16, d = i - j: a quotient that is not on a border is 2^d / 2A > 2^(d-17)
 // from it, half a step of the quotient, which lies below 2^(8+d); the
-// corrected quotient is off by 2^-22 of a step before its rounding.)
+// corrected quotient is off by 2^-22 of a step before its rounding.)  That
+// takes products that fp32 does not round: where a is at least 2^-100 those
+// that get a code other than 0 lie above 2^-108, with all 16 bits, and their
+// remainders are multiples of 2^-139.  Rows with a smaller a (rows of zeros
+// too, which have nothing to lose by it) are read again
+// and formed in 64 bits.
 //
 // Bound by bytes: 7984 rows of 4096 with a residual 43.4 us, 5.3 TB/s (a copy
 // reaches 6.3); a single row 2.9 us, launch and two rounds of memory latency.
@@ -27,15 +32,19 @@ __device__ __forceinline__ void unpack8(u32x4 w, float (&v)[8]) {
     }
 }
 
+constexpr float kTiny = 0x1p-100f;  // largest products below it: see above
+
 // What turns the products of a row into codes, from its sum of squares and largest product.
 struct RowScale {
-    float top, inv, scale;
-    bool bad;
+    float top, inv, rsqrt, scale;
+    bool bad, tiny;  // tiny: not for these codes and this scale
     __device__ __forceinline__ RowScale(float sum, float largest, const RmsNorm8Args& a) {
         top = largest;
         bad = !(sum < __builtin_inff()) || !(127.f * largest < __builtin_inff());
-        inv = bad || top == 0.f ? 0.f : 1.0f / top;
-        scale = bad ? __builtin_nanf("") : top * (1.0f / sqrtf(sum / (float)a.n + a.eps)) / 127.0f;
+        tiny = !bad && top < kTiny;
+        inv = bad || tiny ? 0.f : 1.0f / top;
+        rsqrt = 1.0f / sqrtf(sum / (float)a.n + a.eps);
+        scale = bad ? __builtin_nanf("") : top * rsqrt / 127.0f;
     }
     // the codes of four products, in a word
     __device__ __forceinline__ uint32_t codes(float u0, float u1, float u2, float u3) const {
@@ -75,6 +84,44 @@ __device__ __forceinline__ void join_row(float& sum, float& top) {
             top = fmaxf(top, tops[i]);
         }
     }
+}
+
+// A row whose products fp32 does not hold, by the WAVES waves that hold it: its products in 64 bits, where they and 127 of
+// them are exact and a quotient is off by 2^-53, read from where h stands by now (a lane reads what it wrote itself).
+template <int WAVES>
+__device__ __forceinline__ void tiny_row(const RmsNorm8Args& a, int64_t t, int tid, float rsqrt) {
+    constexpr int kThreads = WAVES * kWave;
+    const int chunks = a.n / 8;
+    const uint16_t* row = a.residual != nullptr ? a.residual_out + t * a.n : a.x + t * a.x_stride;
+    double top = 0.;
+    for (int c = tid; c < chunks; c += kThreads) {
+        float h[8], g[8];
+        unpack8(*(const u32x4*)(row + c * 8), h);
+        unpack8(*(const u32x4*)(a.weight + c * 8), g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmax(top, fabs((double)h[e] * (double)g[e]));
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) top = fmax(top, __shfl_xor(top, d, kWave));
+    if constexpr (WAVES > 1) {
+        __shared__ double tops[WAVES];
+        if ((tid & 63) == 0) tops[tid >> 6] = top;
+        __syncthreads();
+        for (int i = 0; i < WAVES; ++i) top = fmax(top, tops[i]);
+    }
+    for (int c = tid; c < chunks; c += kThreads) {
+        float h[8], g[8];
+        unpack8(*(const u32x4*)(row + c * 8), h);
+        unpack8(*(const u32x4*)(a.weight + c * 8), g);
+        u32x2 codes = {0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const double q = top == 0. ? 0. : 127. * ((double)h[e] * (double)g[e]) / top;
+            codes[e / 4] |= ((uint32_t)(int)rint(q) & 0xFFu) << (e % 4 * 8);
+        }
+        *(u32x2*)(a.codes + t * a.n + c * 8) = codes;
+    }
+    if (tid == 0) a.scales[t] = (float)(top * (double)rsqrt / 127.);
 }
 
 // WAVES waves a row, CH chunks of 8 elements a lane; one wave a row: four rows a block.
@@ -120,6 +167,7 @@ __device__ __forceinline__ void norm_body(const RmsNorm8Args& a) {
     }
     join_row<WAVES>(sum, top);
     const RowScale s(sum, top, a);
+    if (s.tiny) return tiny_row<WAVES>(a, t, tid, s.rsqrt);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int c = i * kThreads + tid;
@@ -159,6 +207,7 @@ __global__ __launch_bounds__(kLongThreads) void rms_norm8_long_kernel(RmsNorm8Ar
     }
     join_row<kLongThreads / kWave>(sum, top);
     const RowScale s(sum, top, a);
+    if (s.tiny) return tiny_row<kLongThreads / kWave>(a, t, threadIdx.x, s.rsqrt);
     if (a.residual != nullptr) row = a.residual_out + t * a.n;  // (a lane reads what it wrote itself)
     for (int c = threadIdx.x; c < chunks; c += kLongThreads) {
         float h[8], g[8];
