@@ -30,7 +30,7 @@ extern "C" {
  *   scales[t] = a * r / 127,  codes[t][c] = round(127 * u[c] / a)  (to nearest, ties to even; 0 where a = 0)
  * so codes * scales stands for the normalised row, as ple_w8_linear takes it.
  * Each code is the nearest one of its exact quotient.  Sums are fp32.  A row
- * whose h holds a NaN or an infinity, or whose sum of squares or 127 * a
+ * whose h or u holds a NaN or an infinity, or whose sum of squares or 127 * a
  * leaves fp32's range, has scale NaN and codes of zero.
  * x: device bf16, row t at x + t * x_stride elements (x_stride >= n, a
  * multiple of 8); residual, residual_out: device bf16 [T][n], both or neither

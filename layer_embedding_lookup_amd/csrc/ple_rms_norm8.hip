@@ -13,8 +13,7 @@
 // takes products that fp32 does not round: where a is at least 2^-100 those
 // that get a code other than 0 lie above 2^-108, with all 16 bits, and their
 // remainders are multiples of 2^-139.  Rows with a smaller a (rows of zeros
-// too, which have nothing to lose by it) are read again
-// and formed in 64 bits.
+// too, which have nothing to lose by it) are read again and formed in 64 bits.
 //
 // Bound by bytes: 7984 rows of 4096 with a residual 43.4 us, 5.3 TB/s (a copy
 // reaches 6.3); a single row 2.9 us, launch and two rounds of memory latency.
@@ -40,7 +39,7 @@ struct RowScale {
     bool bad, tiny;  // tiny: not for these codes and this scale
     __device__ __forceinline__ RowScale(float sum, float largest, const RmsNorm8Args& a) {
         top = largest;
-        bad = !(sum < __builtin_inff()) || !(127.f * largest < __builtin_inff());
+        bad = !(sum < __builtin_inff()) || !(127.f * largest < __builtin_inff());  // (or either is NaN)
         tiny = !bad && top < kTiny;
         inv = bad || tiny ? 0.f : 1.0f / top;
         rsqrt = 1.0f / sqrtf(sum / (float)a.n + a.eps);
@@ -61,13 +60,17 @@ private:
     }
 };
 
-// The wave's, then the block's sum and maximum.  A NaN among the values makes the sum NaN.
+// The larger one, NaN if either is: a weight that is no number, or an infinite one over an h of 0, is not lost.
+__device__ __forceinline__ float larger(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+
+// The wave's, then the block's sum and maximum.  A NaN among the values makes the sum NaN, one among the products the
+// maximum.
 template <int WAVES>
 __device__ __forceinline__ void join_row(float& sum, float& top) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) {
         sum += __shfl_xor(sum, d, kWave);
-        top = fmaxf(top, __shfl_xor(top, d, kWave));
+        top = larger(top, __shfl_xor(top, d, kWave));
     }
     if constexpr (WAVES > 1) {
         __shared__ float sums[WAVES], tops[WAVES];
@@ -81,7 +84,7 @@ __device__ __forceinline__ void join_row(float& sum, float& top) {
 #pragma unroll
         for (int i = 0; i < WAVES; ++i) {
             sum += sums[i];
-            top = fmaxf(top, tops[i]);
+            top = larger(top, tops[i]);
         }
     }
 }
@@ -162,7 +165,7 @@ __device__ __forceinline__ void norm_body(const RmsNorm8Args& a) {
         for (int e = 0; e < 8; ++e) {
             sum = fmaf(u[i][e], u[i][e], sum);
             u[i][e] *= g[e];
-            top = fmaxf(top, fabsf(u[i][e]));
+            top = larger(top, fabsf(u[i][e]));
         }
     }
     join_row<WAVES>(sum, top);
@@ -202,7 +205,7 @@ __global__ __launch_bounds__(kLongThreads) void rms_norm8_long_kernel(RmsNorm8Ar
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             sum = fmaf(h[e], h[e], sum);
-            top = fmaxf(top, fabsf(h[e] * g[e]));
+            top = larger(top, fabsf(h[e] * g[e]));
         }
     }
     join_row<kLongThreads / kWave>(sum, top);

@@ -69,3 +69,21 @@ def test_norm_tiny_rows_in_place_and_strided():
             dx, dres = x.to(DEV), res.to(DEV)
             got = ple.ple_rms_norm8(dx, w.to(DEV), residual=dres, residual_out=dx if into == "x" else dres)
             check_tiny(x, w, res, 1e-6, got)
+
+
+@pytest.mark.parametrize("N", [16, 512, 2064, 4096, 8208, 20000])
+def test_norm_weights_of_no_number(N):
+    """A NaN or an infinity in the weight is in every row's products, as 0 * infinity too: scales of NaN, codes of zero, the
+    residual as ever."""
+    g = G.gen(N)
+    x, res = torch.randn((5, N), generator=g).to(BF), torch.randn((5, N), generator=g).to(BF)
+    x[3] = res[3] = 0
+    for at in (0, 7, N // 2, N - 1):
+        x[1, at] = res[1, at] = 0
+        for value in (math.nan, -math.nan, math.inf, -math.inf):
+            w = torch.randn(N, generator=g).to(BF)
+            w[at] = value
+            for r in (None, res):
+                codes, scales, h = ple.ple_rms_norm8(x.to(DEV), w.to(DEV), residual=None if r is None else r.to(DEV))
+                assert torch.isnan(scales).all() and (codes == 0).all()
+                assert r is None or torch.equal(h.cpu(), (x.float() + r.float()).to(BF))
