@@ -43,7 +43,8 @@ struct RowScale {
         tiny = !bad && top < kTiny;
         inv = bad || tiny ? 0.f : 1.0f / top;
         rsqrt = 1.0f / sqrtf(sum / (float)a.n + a.eps);
-        scale = bad ? __builtin_nanf("") : top * rsqrt / 127.0f;
+        const float all = top * rsqrt;  // (may be beyond fp32 where its 127th part is not)
+        scale = bad ? __builtin_nanf("") : all < __builtin_inff() ? all / 127.0f : top / 127.0f * rsqrt;
     }
     // the codes of four products, in a word
     __device__ __forceinline__ uint32_t codes(float u0, float u1, float u2, float u3) const {

@@ -87,3 +87,19 @@ def test_norm_weights_of_no_number(N):
                 codes, scales, h = ple.ple_rms_norm8(x.to(DEV), w.to(DEV), residual=None if r is None else r.to(DEV))
                 assert torch.isnan(scales).all() and (codes == 0).all()
                 assert r is None or torch.equal(h.cpu(), (x.float() + r.float()).to(BF))
+
+
+@pytest.mark.parametrize("N", [48, 4096, 20000])
+def test_norm_scales_whose_products_overflow(N):
+    """A largest product below fp32's 127th part, times a norm's factor far above 127: the scale itself is in range."""
+    g = G.gen(N)
+    x = (torch.randn((4, N), generator=g).clamp(-4, 4).double() * 2.0 ** -9).to(BF)
+    x[:, 3] = 2.0 ** -7
+    w = (torch.rand(N, generator=g).double() * 2.0 ** 126).to(BF)
+    w[3] = 2.0 ** 127
+    top = (x.double() * w.double()).abs().amax(1)
+    factor = 1 / (x.double().square().mean(1) + 1e-6).sqrt()
+    assert (127 * top < 3.4e38).all() and (top * factor > 3.5e38).all()
+    got = ple.ple_rms_norm8(x.to(DEV), w.to(DEV))
+    G.check_norm(x, w, None, 1e-6, got)
+    assert torch.isfinite(got[1]).all()
