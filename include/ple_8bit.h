@@ -110,7 +110,11 @@ int ple_kv8_read(const ple_kv8_cache* cache, const ple_kv8_batch* batch, uint16_
 /*
  * Causal attention of the new tokens over the cache; definition, arguments and
  * workspace as for ple_kv4_attention.  A NaN key makes NaN the rows that see
- * it, a NaN element of a value that element of them.
+ * it, a NaN element of a value that element of them.  Weights are rounded to
+ * fp16 or better: a token's part of an output element is off by at most 2^-11
+ * of itself or 2^-27 of its value, whatever the other blocks' scales are.
+ * (Where the scales of a request's blocks lie more than 2^6 apart, the call
+ * goes through the tiles around them twice.)
  */
 int ple_kv8_attention(const uint16_t* q, int64_t q_stride, int32_t num_q_heads, const ple_kv8_cache* cache,
                       const ple_kv8_batch* batch, int32_t window, float scale, uint16_t* out, float* lse,

@@ -13,7 +13,10 @@
 //   z_ij = s_ij log2 e + log2 s_v(j),  p_ij = 2^(z_ij - m_i),  m_i = max_j z_ij
 //   out_i = sum_j p_ij code_j / sum_j p_ij / s_v(j)
 // so that the weights of the value product (fp16) carry it without a product
-// per element, whatever the scales' range, and codes enter as they are.
+// per element, and codes enter as they are.  Where the scales of the blocks
+// that a wave goes through lie more than kFar apart, the light ones' weights
+// would leave fp16 below the heavy ones': such a wave goes through its tiles
+// once more with weights of two bf16 parts (FarWeights).
 //
 // Layouts, chosen so that nothing crosses lanes:
 //  - MFMA i of a tile takes its token rows in the order row ρ <-> token
@@ -29,6 +32,8 @@
 // average 289 us, 5.6 TB/s, 89% of a copy's rate; one of 100100 tokens 43 us
 // with the join of its 32 splits; 64 verify windows of four tokens 17.7, a
 // chain of two to three tiles a wave.  Many rows: see there.
+#include <type_traits>
+
 #include "ple_8bit_launch.h"
 #include "ple_paged_attention.h"
 
@@ -94,12 +99,57 @@ struct BlockScales {
 // is taken from the rounded products, not in one step with them.  `wide`: the wave has such rows.
 constexpr float kWide = 4194304.0f;  // 2^22
 
-// The weights of one tile: s (products, lane (n, g) holding tokens tg .. tg + 15 of MT rows) becomes the fp16 weights p;
+// A lane's eight weights of a value product and the product itself.  In fp16: relative 2^-11, or 2^-24 beside weights of
+// 2^8 and more (ple_paged_attention.h).
+struct NearWeights {
+    Frag p;
+    __device__ __forceinline__ void set(int i, float x, float y) { p.p[i] = f16x2{(_Float16)x, (_Float16)y}; }
+    __device__ __forceinline__ void unpack(uint32_t lo, uint32_t hi, Frag& f) const { fp8_to_f16(lo, hi, f); }
+    __device__ __forceinline__ f32x4 product(const Frag& f, f32x4 c) const {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(f.v, p.v, c, 0, 0, 0);
+    }
+    typedef Frag Codes;
+};
+// As two bf16 each: relative 2^-16 down to fp32's least exponent, twice the products.
+struct FarWeights {
+    BFrag p, rest;
+    __device__ __forceinline__ void set(int i, float x, float y) {
+        p.u[i] = pack_bf16x2(x, y);
+        rest.u[i] = pack_bf16x2(x - bf16_lo(p.u[i]), y - bf16_hi(p.u[i]));
+    }
+    __device__ __forceinline__ void unpack(uint32_t lo, uint32_t hi, BFrag& f) const { fp8_to_bf16(lo, hi, f); }
+    __device__ __forceinline__ f32x4 product(const BFrag& f, f32x4 c) const {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.v, rest.v, c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.v, p.v, c, 0, 0, 0);
+    }
+    typedef BFrag Codes;
+};
+
+// How far apart the values' scales of a lane's blocks lie.  A block's weights are below those of equal softmax weight of the
+// heaviest block by the scales' ratio r, so in fp16 a token's part of an element is off by 2^-33 r of its value beyond its
+// rounding: by 2^-27 with the ratios that are left to it.  (A block has the largest of 16 tokens' values for its scale,
+// which seldom differ by 2^4.)  Going through every tile twice takes 1.5 times as long for few rows (256 requests over 3084
+// 495 us for 294), 2.1 times for many; watching the scales 0 to 2% (verify windows 18.5 us, 18.2 without).
+constexpr float kFar = 64.0f;
+struct ScaleRange {
+    uint32_t low = 0x7F800000u, high = 0u;  // (as bits, which are in the order of the positive numbers)
+    __device__ __forceinline__ void add(float v, bool bad) {
+        low = min(low, bad ? 0x7F800000u : __float_as_uint(v));
+        high = max(high, bad ? 0u : __float_as_uint(v));
+    }
+    // the wave's blocks (lanes n + 16 g all have those of block g)
+    __device__ __forceinline__ bool far() const {
+        const float least = __uint_as_float(low), most = __uint_as_float(high);
+        return __ballot(quad_max(most) > -quad_max(-least) * kFar) != 0;
+    }
+};
+
+// The weights of one tile: s (products, lane (n, g) holding tokens tg .. tg + 15 of MT rows) becomes the weights p;
 // m, l and o (the rows' running maxima, sums and outputs) move on.  `some`: not every row sees the whole tile.
-template <int NB, int MT>
+template <int NB, int MT, class Weights>
 __device__ __forceinline__ void kv8_softmax(f32x4 (&s)[MT][4], const BlockScales& c, bool some, bool bad, int tg,
                                             const int (&see_lo)[MT], const int (&see_hi)[MT], float (&m)[MT], float (&l)[MT],
-                                            f32x4 (&o)[MT][NB], bool& wide, Frag (&p)[MT][2]) {
+                                            f32x4 (&o)[MT][NB], bool& wide, Weights (&p)[MT][2]) {
     if (some) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -162,7 +212,7 @@ __device__ __forceinline__ void kv8_softmax(f32x4 (&s)[MT][4], const BlockScales
                 const float x = __builtin_amdgcn_exp2f(fmaf(s[mt][i][e], key, sub));
                 const float y = __builtin_amdgcn_exp2f(fmaf(s[mt][i][e + 1], key, sub));
                 sum += x + y;
-                p[mt][i >> 1].p[(i & 1) * 2 + e / 2] = f16x2{(_Float16)x, (_Float16)y};
+                p[mt][i >> 1].set((i & 1) * 2 + e / 2, x, y);
             }
         l[mt] = fmaf(sum, c.per_value, l[mt]);
     }
@@ -250,51 +300,34 @@ __device__ __forceinline__ void kv8_give_nans(const uint64_t (&nan)[MT], f32x4 (
     }
 }
 
-template <int D, int WAVES>
-struct Kv8Shape {
-    static constexpr int KS = D / 32;  // k-steps of the first product
-    static constexpr int NB = D / 16;  // element blocks
-    static constexpr int LDS = kAttnWaves * 16 * kJoinRow<D> * 4;  // the join's
-};
-
-// Few rows: the waves of a block take the tiles of a cache range in turn and join through LDS.  The next tile is on its
-// way while this one is used, its page-table entry a tile before that.
-template <int D, int MT, int WAVES>
-__device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
-    using Sh = Kv8Shape<D, WAVES>;
-    extern __shared__ __align__(16) char lds[];
-    const int split = blockIdx.y;
-    int r, head, tile;
-    attn_block(a, r, head, tile);
-    AttnTile w;
-    attn_request(a, r, w);
-    attn_idle_tokens(a);
-    if (!attn_tile(a, tile, w)) return;
-    const int splits = attn_splits(a, w);
-    if (split >= splits) return;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// A wave's MT x 16 rows through the cache tiles at first, first + step .. below end: running maxima m, sums l and outputs o,
+// NaN values found.  The next tile is on its way while this one is used, its page-table entry a tile before that, the
+// queries (by `queries`) behind the first one.  Returns whether its blocks' scales are too far apart for NearWeights.
+template <int D, int MT, class Weights, class Queries>
+__device__ __forceinline__ bool kv8_tiles(const Kv8AttentionArgs& a, const AttnTile& w, const int32_t* table_row, int head,
+                                          int first, int step, int end, BFrag (&q)[MT][D / 32], int (&see_lo)[MT],
+                                          int (&see_hi)[MT], float (&m)[MT], float (&l)[MT], f32x4 (&o)[MT][D / 16],
+                                          Queries queries) {
+    constexpr int KS = D / 32, NB = D / 16;
+    int lane = threadIdx.x & 63;
+    // (the second pass's addresses are formed there, not held through the first one)
+    if constexpr (std::is_same<Weights, FarWeights>::value) asm volatile("" : "+v"(lane));
     const int n = lane & 15, g = lane >> 4;
-    const int begin = w.lo + split * a.chunk;
-    const int end = split == splits - 1 ? w.hi : min(w.hi, begin + a.chunk);
     const float base = a.scale * 1.44269504088896341f;
-
-    f32x4 o[MT][Sh::NB];
-    float m[MT], l[MT];
     bool wide = false, nans = false;
+    ScaleRange range;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         m[mt] = -__builtin_inff();
         l[mt] = 0.f;
 #pragma unroll
-        for (int b = 0; b < Sh::NB; ++b) o[mt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int b = 0; b < NB; ++b) o[mt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    const int32_t* table_row = a.batch.page_table + (int64_t)r * a.batch.table_width;
     bool bad_next = false;
-    u32x4 kraw[4][D / 64], vraw[Sh::NB];
+    u32x4 kraw[4][D / 64], vraw[NB];
     float ks, vs;
-    const int first = begin + wave * kTile;
-    PageWalk walk(a, table_row, head, first + 16 * g, WAVES * kTile / 16, end);
+    PageWalk walk(a, table_row, head, first + 16 * g, step / 16, end);
     int64_t block = 0;  // of the tile whose keys are on their way: this lane's
     auto load_keys = [&](int t0) {
         const int grp = walk.number(t0 + 16 * g, end);
@@ -314,60 +347,58 @@ __device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
     auto load_values = [&]() {
         const uint8_t* vc = a.cache.v_codes + block * (16 * D) + n * 16;
 #pragma unroll
-        for (int b = 0; b < Sh::NB; ++b) vraw[b] = *(const u32x4*)(vc + b * 256);
+        for (int b = 0; b < NB; ++b) vraw[b] = *(const u32x4*)(vc + b * 256);
     };
     if (first < end) {
         walk.fetch();
         load_keys(first);
         load_values();
     }
-    BFrag q[MT][Sh::KS];
-    int see_lo[MT], see_hi[MT];
-    kv8_queries<D, MT>(a, w, w.row0, head, begin, end, q, see_lo, see_hi);
-    for (int t0 = first; t0 < end; t0 += WAVES * kTile) {
+    queries();
+    for (int t0 = first; t0 < end; t0 += step) {
         const int tg = t0 + 16 * g;  // this lane's block g of the tile
         const bool bad = bad_next;
         BlockScales c;
         c.set(base, ks, vs, bad);
+        range.add(vs, bad);
 
         f32x4 s[MT][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            BFrag f[Sh::KS];
+            BFrag f[KS];
 #pragma unroll
-            for (int k = 0; k < Sh::KS; ++k) fp8_to_bf16(kraw[i][k / 2][2 * (k & 1)], kraw[i][k / 2][2 * (k & 1) + 1], f[k]);
+            for (int k = 0; k < KS; ++k) fp8_to_bf16(kraw[i][k / 2][2 * (k & 1)], kraw[i][k / 2][2 * (k & 1) + 1], f[k]);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 s[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < Sh::KS; ++k)
+                for (int k = 0; k < KS; ++k)
                     s[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[k].v, q[mt][k].v, s[mt][i], 0, 0, 0);
             }
             __builtin_amdgcn_sched_barrier(0);  // (dequantised keys of one MFMA at a time: registers)
         }
-        const bool more = t0 + WAVES * kTile < end;
-        if (more) load_keys(t0 + WAVES * kTile);
+        const bool more = t0 + step < end;
+        if (more) load_keys(t0 + step);
 
         // a tile that not every row sees as a whole
         bool every = t0 >= w.first_seen && t0 + kTile <= end && __ballot(bad) == 0;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) every = every && t0 >= see_lo[mt] && t0 + kTile <= see_hi[mt];
         const bool some = __ballot(!every) != 0;
-        Frag p[MT][2];
+        Weights p[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)  // (one after the other: fewer registers than all of them together)
-            kv8_softmax<Sh::NB, 1>((f32x4(&)[1][4])s[mt], c, some, bad, tg, (int(&)[1])see_lo[mt], (int(&)[1])see_hi[mt],
-                                   (float(&)[1])m[mt], (float(&)[1])l[mt], (f32x4(&)[1][Sh::NB])o[mt], wide, (Frag(&)[1][2])p[mt]);
-        if (some) nans |= __ballot(kv8_clear<Sh::NB>(vraw, bad, tg, w.first_seen, end)) != 0;
+            kv8_softmax<NB, 1>((f32x4(&)[1][4])s[mt], c, some, bad, tg, (int(&)[1])see_lo[mt], (int(&)[1])see_hi[mt],
+                               (float(&)[1])m[mt], (float(&)[1])l[mt], (f32x4(&)[1][NB])o[mt], wide, (Weights(&)[1][2])p[mt]);
+        if (some) nans |= __ballot(kv8_clear<NB>(vraw, bad, tg, w.first_seen, end)) != 0;
 #pragma unroll
-        for (int b = 0; b < Sh::NB; ++b) {
+        for (int b = 0; b < NB; ++b) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                Frag f;
-                fp8_to_f16(vraw[b][2 * h], vraw[b][2 * h + 1], f);
+                typename Weights::Codes f;
+                p[0][h].unpack(vraw[b][2 * h], vraw[b][2 * h + 1], f);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    o[mt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.v, p[mt][h].v, o[mt][b], 0, 0, 0);
+                for (int mt = 0; mt < MT; ++mt) o[mt][b] = p[mt][h].product(f, o[mt][b]);
             }
             if (b % 2 == 1) __builtin_amdgcn_sched_barrier(0);
         }
@@ -375,16 +406,60 @@ __device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
     }
     if (nans) {
         uint64_t nan[MT] = {};
-        kv8_find_nans<D, MT>(a, table_row, head, first, WAVES * kTile, end, see_lo, see_hi, nan);
-        kv8_give_nans<Sh::NB>(nan, o);
+        kv8_find_nans<D, MT>(a, table_row, head, first, step, end, see_lo, see_hi, nan);
+        kv8_give_nans<NB>(nan, o);
     }
+    return range.far();
+}
+
+// The same with FarWeights, from the start, 16 rows after the other (registers).
+template <int D, int MT>
+__device__ __forceinline__ void kv8_far_tiles(const Kv8AttentionArgs& a, const AttnTile& w, const int32_t* table_row, int head,
+                                              int first, int step, int end, BFrag (&q)[MT][D / 32], int (&see_lo)[MT],
+                                              int (&see_hi)[MT], float (&m)[MT], float (&l)[MT], f32x4 (&o)[MT][D / 16]) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+        kv8_tiles<D, 1, FarWeights>(a, w, table_row, head, first, step, end, (BFrag(&)[1][D / 32])q[mt], (int(&)[1])see_lo[mt],
+                                    (int(&)[1])see_hi[mt], (float(&)[1])m[mt], (float(&)[1])l[mt],
+                                    (f32x4(&)[1][D / 16])o[mt], [] {});
+}
+
+// Few rows: the waves of a block take the tiles of a cache range in turn and join through LDS.
+template <int D, int MT, int WAVES>
+__device__ __forceinline__ void kv8_body(const Kv8AttentionArgs& a) {
+    extern __shared__ __align__(16) char lds[];
+    const int split = blockIdx.y;
+    int r, head, tile;
+    attn_block(a, r, head, tile);
+    AttnTile w;
+    attn_request(a, r, w);
+    attn_idle_tokens(a);
+    if (!attn_tile(a, tile, w)) return;
+    const int splits = attn_splits(a, w);
+    if (split >= splits) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int begin = w.lo + split * a.chunk;
+    const int end = split == splits - 1 ? w.hi : min(w.hi, begin + a.chunk);
+    const int first = begin + wave * kTile, step = WAVES * kTile;
+    const int32_t* table_row = a.batch.page_table + (int64_t)r * a.batch.table_width;
+
+    f32x4 o[MT][D / 16];
+    float m[MT], l[MT];
+    BFrag q[MT][D / 32];
+    int see_lo[MT], see_hi[MT];
+    const auto queries = [&]() { kv8_queries<D, MT>(a, w, w.row0, head, begin, end, q, see_lo, see_hi); };
+    const bool far = kv8_tiles<D, MT, NearWeights>(a, w, table_row, head, first, step, end, q, see_lo, see_hi, m, l, o, queries);
+    if (__builtin_expect(far, false))  // (its code out of the way)
+        kv8_far_tiles<D, MT>(a, w, table_row, head, first, step, end, q, see_lo, see_hi, m, l, o);
     const uint32_t none[MT] = {};
     attn_join_waves<D, MT, WAVES>(a, w, head, split, splits, lds, m, l, o, none);
 }
 
+template <int D>
+constexpr int kJoinLds = kAttnWaves * 16 * kJoinRow<D> * 4;
 // D, row tiles, waves, waves per SIMD that registers allow
 #define PLE_ATTN_SHAPES(X)                                                                                        \
-    X(64, 1, 4, 3) X(64, 1, 8, 2) X(64, 2, 4, 2) X(64, 2, 8, 2) X(128, 1, 4, 2) X(128, 1, 8, 2) X(128, 2, 4, 2) \
+    X(64, 1, 4, 4) X(64, 1, 8, 2) X(64, 2, 4, 2) X(64, 2, 8, 2) X(128, 1, 4, 2) X(128, 1, 8, 2) X(128, 2, 4, 2) \
     X(128, 2, 8, 2) X(256, 1, 4, 1)
 #define PLE_ATTN_KERNEL(D, MT, WAVES, OCC)                                                                                  \
     __global__ __launch_bounds__(WAVES * kWave, OCC) void kv8_attention_##D##_##MT##x##WAVES##_kernel(Kv8AttentionArgs a) { \
@@ -486,6 +561,7 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
         for (int b = 0; b < NB; ++b) o[mt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     bool wide = false, nans = false;  // wide: see kWide
+    ScaleRange range;
     if (threadIdx.x == 0) *(volatile int*)(lds + Sh::NANS_AT) = 0;
     // the first tile is on its way before the queries are
     if (begin < end) {
@@ -642,6 +718,7 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
             nans |= kv8_clear<Sh::WB>(vraw, bad_loaded, tg, w.first_seen, end);
         };
         c.set(base, ks, vs, bad);
+        range.add(vs, bad);
         if (some) clear(begin);
 #pragma unroll
         for (int i = 0; i < FILLS; ++i) fill(0, i);
@@ -665,6 +742,7 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
             bad_next = bad_loaded;
             some_next = partial(t0 + kTile, bad_next);
             c_next.set(base, ks, vs, bad_next);
+            range.add(vs, bad_next);
             if (some_next) clear(t0 + kTile);
             __syncthreads();  // every read of the other buffer is done
             // first half's values; second half's maxima and the next tile into LDS
@@ -694,6 +772,9 @@ __device__ __forceinline__ void kv8_chunk_piece(const Kv8AttentionArgs& a, const
         }
     }
 
+    // (all waves agree: each has gone by the scales of all blocks)
+    if (__builtin_expect(range.far(), false))
+        kv8_far_tiles<D, MT>(a, w, table_row, head, begin, kTile, end, q, see_lo, see_hi, m, l, o);
     // (a wave has met its quarter of the elements alone)
     if (nans) *(volatile int*)(lds + Sh::NANS_AT) = 1;
     __syncthreads();
@@ -831,7 +912,7 @@ hipError_t launch_kv8_attention(const Kv8AttentionArgs& a, hipStream_t s) {
                        : launch_attention<Kv8AttentionArgs, kv8_attention_chunk_256_kernel, Kv8ChunkShape<256>::LDS>(a, kAttnThreads, s);
 #define PLE_ATTN_LAUNCH(DD, MT, WAVES, OCC)                                                                              \
     if (D == DD && mt == MT && a.waves == WAVES)                                                                         \
-        e = launch_attention<Kv8AttentionArgs, kv8_attention_##DD##_##MT##x##WAVES##_kernel, Kv8Shape<DD, WAVES>::LDS>(  \
+        e = launch_attention<Kv8AttentionArgs, kv8_attention_##DD##_##MT##x##WAVES##_kernel, kJoinLds<DD>>(  \
             a, WAVES * kWave, s);
     PLE_ATTN_SHAPES(PLE_ATTN_LAUNCH)
 #undef PLE_ATTN_LAUNCH

@@ -103,3 +103,78 @@ def test_norm_scales_whose_products_overflow(N):
     got = ple.ple_rms_norm8(x.to(DEV), w.to(DEV))
     G.check_norm(x, w, None, 1e-6, got)
     assert torch.isfinite(got[1]).all()
+
+
+# ---- attention ----
+
+def far_cache(c):
+    """A case's cache in which some blocks of each head have values 2^10 .. 2^50 times the others', and zeros in the first half
+    of their elements: there only the light blocks count."""
+    cache, q, qsl, seq = K.attention_inputs(c)
+    g = G.gen(sum(c.lens))
+    heavy = torch.rand(cache.scales["v"].shape, generator=g) < 0.2
+    for r in range(len(c.lens)):                              # (the first block and the last whole one too)
+        for j in (0, (c.lens[r] - 1) // 16 * 16):
+            at = cache.place(r, j)
+            if c.lens[r] and at:
+                heavy[at[0], 0, at[1] // 16] = True
+    by = torch.pow(2.0, torch.randint(10, 41, heavy.shape, generator=g).to(F64))
+    cache.scales["v"] = torch.where(heavy, cache.scales["v"] * by, cache.scales["v"] * 2.0 ** -10).clamp(U.LEAST, U.MOST)
+    codes = cache.codes["v"]
+    gone = heavy.repeat_interleave(16, 2)[..., None] & (torch.arange(c.D) < c.D // 2)
+    cache.codes["v"] = torch.where(gone & (codes & 0x7F != 0x7F), torch.zeros_like(codes), codes)
+    return cache, q, qsl, seq
+
+
+def far_bound(cache, q, qsl, seq, window):
+    """out, lse and bounds as U.attention gives them, but each token's part of an element for itself: a weight is rounded by
+    2^-11 of itself, or, where it is less than 2^-14 of what fp16 has at a time, by 2^-25 of the heaviest (of 2^8 at least)
+    over the scales' ratio, 2^6 at most: 2^-27 of the token's own value."""
+    class Near(U.Cache):
+        def most(self, k, r, n):
+            return torch.zeros(self.H, dtype=F64)
+    near, size = Near.__new__(Near), U.Cache.__new__(U.Cache)
+    near.__dict__.update(cache.__dict__)
+    size.__dict__.update(cache.__dict__)
+    size.codes = {"k": cache.codes["k"], "v": cache.codes["v"] & 0x7F}
+    want, lse, tol, tol_lse = U.attention(near, q, qsl, seq, window)
+    mean = U.attention(size, torch.zeros_like(q), qsl, seq, window)[0]       # of the sizes of the values that a row sees
+    tokens = torch.zeros(q.shape[0], dtype=F64)
+    for r in range(len(seq)):
+        tokens[int(qsl[r]):int(qsl[r + 1])] = max(0, int(seq[r]))
+    return want, lse, tol + 1.01 * 2.0 ** -27 * tokens[:, None, None] * mean, tol_lse
+
+
+@pytest.mark.parametrize("c", K.ATTENTION, ids=repr)
+def test_attention_light_blocks_beside_heavy_ones(c):
+    """Blocks whose values are 2^20 times those of others and more, by every kernel: what the light ones add to elements that
+    the heavy ones have zeros in comes out as the definition says."""
+    print(f"kv8 attention, blocks far apart: {c}", flush=True)
+    cache, q, qsl, seq = far_cache(c)
+    out, lse = G.run_attention(cache, q, qsl, seq, window=c.window, **K.hints(c))
+    want, want_lse, tol, tol_lse = far_bound(cache, q, qsl, seq, c.window)
+    assert ((out - want).abs() <= tol).all(), float(((out - want).abs() - tol).max())
+    empty = want_lse == -math.inf
+    assert torch.equal(lse == -math.inf, empty) and (out[empty] == 0).all()
+    assert ((lse - want_lse).abs() <= tol_lse)[~empty].all()
+
+
+@pytest.mark.parametrize("c", K.ATTENTION, ids=repr)
+def test_attention_nan_beside_blocks_far_apart(c):
+    """A NaN element of one value there: that element of the rows that see it, nothing else."""
+    print(f"kv8 attention, a NaN beside blocks far apart: {c}", flush=True)
+    cache, q, qsl, seq = far_cache(c)
+    clean, clean_lse = G.run_attention(cache, q, qsl, seq, window=c.window, **K.hints(c))
+    r = c.lens.index(max(c.lens))
+    before = c.lens[r] - c.news[r]
+    first = 0 if c.window == 0 else max(0, c.lens[r] - c.window)
+    j = next(j for j in range((first + before) // 2, before + 1) if 0 <= int(cache.table[r, j // c.page]))
+    head, d = c.H - 1, 5
+    cache.codes["v"][int(cache.table[r, j // c.page]), head, j % c.page, d] = 0x7F
+    out, lse = G.run_attention(cache, q, qsl, seq, window=c.window, **K.hints(c))
+    mine = torch.zeros(out.shape, dtype=torch.bool)
+    p = before + torch.arange(c.news[r])
+    sees = (p >= j) & (p - c.window < j if c.window else True)
+    mine[int(qsl[r]):int(qsl[r + 1]), head * (c.Hq // c.H):, d] = sees[:, None]
+    assert mine.any() and torch.isnan(out[mine]).all()
+    assert torch.equal(out[~mine], clean[~mine]) and torch.equal(lse, clean_lse)
