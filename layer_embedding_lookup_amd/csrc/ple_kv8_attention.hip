@@ -89,7 +89,7 @@ struct BlockScales {
     __device__ __forceinline__ void set(float base, float k, float v, bool bad) {
         k = bad ? 1.f : k;
         v = bad ? 1.f : v;
-        key = base * k;
+        key = fminf(base * k, 3.4028234e38f);  // (an infinity would make NaN of products of 0)
         log_value = __builtin_amdgcn_logf(v);
         per_value = __builtin_amdgcn_rcpf(v);
     }

@@ -178,3 +178,16 @@ def test_attention_nan_beside_blocks_far_apart(c):
     mine[int(qsl[r]):int(qsl[r + 1]), head * (c.Hq // c.H):, d] = sees[:, None]
     assert mine.any() and torch.isnan(out[mine]).all()
     assert torch.equal(out[~mine], clean[~mine]) and torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("D,news", [(64, [1, 1]), (128, [3, 1]), (256, [1, 2]), (64, [90, 3]), (128, [90, 3]), (256, [40, 3])])
+def test_attention_scale_beyond_the_products_range(D, news):
+    """The largest `scale` of the call over keys of the largest scale, whose product fp32 does not hold: rows of zeros still
+    see every token alike."""
+    g = G.gen(D + news[0])
+    lens = [200, 90]
+    cache = U.Cache(g, lens, H=2, D=D, page=16)
+    cache.scales["k"] = torch.where(torch.isnan(cache.scales["k"]), math.nan, 2.0 ** 32)
+    qsl, seq = G.batch(news, lens)
+    q = torch.zeros((int(qsl[-1]), 4, D), dtype=BF)
+    G.check_attention(cache, q, qsl, seq, scale=1e30, max_request_tokens=max(news), max_seq_len=max(lens))
