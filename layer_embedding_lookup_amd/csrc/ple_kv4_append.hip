@@ -50,13 +50,14 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArg
     __shared__ double2 turn[128];  // cos, sin of the token's angles
     const int64_t t = blockIdx.x + blockIdx.y * kAppendAcross;
     if (t >= a.batch.num_tokens) return;
-    const int D = a.cache.head_dim, half = a.rot_dim / 2;
+    const int D = a.cache.head_dim;
     const int per_head = D / 8, shift = D == 64 ? 3 : (D == 128 ? 4 : 5);  // chunks of a head
     int r;
     const int pos = kv4_position(a.cache, a.batch, t, r);
+    const int rot = pos < 0 ? 0 : a.rot_dim, half = rot / 2;  // (a token that stands nowhere may hold anything, and keeps it)
     for (int i = threadIdx.x; i < half; i += kAppendThreads) {
         // (a position of 30 bits times a 24-bit frequency: rounded at most in its 54th bit, 2^-53 of the angle)
-        const double angle = (double)(pos < 0 ? 0 : pos) * (double)a.inv_freq[i];
+        const double angle = (double)pos * (double)a.inv_freq[i];
         double sn, cs;
         sincos(angle, &sn, &cs);
         turn[turn_place(i, half)] = make_double2(cs, sn);
@@ -71,7 +72,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArg
         const int head = at >> shift, d0 = (at & (per_head - 1)) * 8;
         const uint16_t* src = a.src[which] + t * a.stride[which] + head * D;
         float v[8];
-        load_rotated(src, d0, which != 2 ? a.rot_dim : 0, a.interleaved, turn, v);
+        load_rotated(src, d0, which != 2 ? rot : 0, a.interleaved, turn, v);
         if (which == 0) {
             u32x4 o;
 #pragma unroll

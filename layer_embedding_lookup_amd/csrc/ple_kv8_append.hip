@@ -359,16 +359,17 @@ __device__ __forceinline__ void append_body(const Kv8AppendArgs& a, int64_t unit
     const int64_t t = id - units * parts;
     if (t >= a.batch.num_tokens || a.num_q_heads == 0) return;
     const int pos = kv8_position(a.cache, a.batch, t);
-    for (int i = threadIdx.x; i < half; i += kAppendThreads) {
+    const int rot = pos < 0 ? 0 : a.rot_dim;  // (a token that stands nowhere may hold anything, and keeps it)
+    for (int i = threadIdx.x; i < rot / 2; i += kAppendThreads) {
         double sn, cs;
-        sincospi(2. * ((double)(pos < 0 ? 0 : pos) * ((double)a.inv_freq[i] * kPerTurn)), &sn, &cs);
+        sincospi(2. * ((double)pos * ((double)a.inv_freq[i] * kPerTurn)), &sn, &cs);
         turn[0][turn_place(i, half)] = make_double2(cs, sn);
     }
     __syncthreads();
     for (int c = threadIdx.x; c < a.num_q_heads * (D / 8); c += kAppendThreads) {
         const int head = c / (D / 8), d0 = c % (D / 8) * 8;
         float v[8];
-        load_rotated(a.src[0] + t * a.stride[0] + head * D, d0, a.rot_dim, a.interleaved, turn[0], v);
+        load_rotated(a.src[0] + t * a.stride[0] + head * D, d0, rot, a.interleaved, turn[0], v);
         u32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);

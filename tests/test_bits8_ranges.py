@@ -191,3 +191,35 @@ def test_attention_scale_beyond_the_products_range(D, news):
     qsl, seq = G.batch(news, lens)
     q = torch.zeros((int(qsl[-1]), 4, D), dtype=BF)
     G.check_attention(cache, q, qsl, seq, scale=1e30, max_request_tokens=max(news), max_seq_len=max(lens))
+
+
+# ---- append ----
+
+def fp4_cache():
+    codes = [torch.zeros((3, 2, 16, 64), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    scales = [torch.zeros((3, 2, 1, 8, 16), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    return ple.KV4Cache(codes[0], scales[0], codes[1], scales[1], *(torch.ones(2, device=DEV) for _ in range(2)))
+
+
+def bits8_cache():
+    codes = [torch.zeros(s, dtype=torch.uint8, device=DEV) for s in ((3, 2, 1, 8, 16, 16), (3, 2, 1, 128, 16))]
+    return ple.KV8Cache(codes[0], torch.ones((3, 2, 1), device=DEV), codes[1], torch.ones((3, 2, 1), device=DEV))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("append,make", [(ple.ple_kv8_append, bits8_cache), (ple.ple_kv4_append, fp4_cache)], ids=["kv8", "kv4"])
+def test_queries_of_no_request_keep_what_they_hold(append, make, interleaved):
+    """A padded batch's rows may hold anything, infinities and NaN too: an element of such a row does not reach the one it
+    would be turned with, and zeros keep their sign."""
+    g = G.gen(3)
+    q, k = (torch.randn((9, h, 128), generator=g).to(BF) for h in (4, 2))
+    idle = [0, 1, 5, 6, 7, 8]                                 # requests have tokens 2 .. 4
+    q[0, :, 3], q[1, 1, 70], q[5, 2, ::7], q[6], q[7, 0, 1::2], q[8, :, :64] = math.inf, math.nan, -math.inf, math.nan, -0.0, -0.0
+    args = [torch.tensor(x, dtype=I32, device=DEV) for x in ([2, 3, 5], [4, 7], [[0], [1]])]
+    inv = torch.logspace(0, -4, 64).to(DEV)
+    out = append(make(), k.to(DEV), k.to(DEV), *args, inv_freq=inv, interleaved=interleaved, q=q.to(DEV)).cpu()
+    nan = torch.isnan(q[idle])
+    assert torch.equal(torch.isnan(out[idle]), nan)
+    assert torch.equal(out[idle].view(torch.int16)[~nan], q[idle].view(torch.int16)[~nan])
+    own = append(make(), k[2:5].to(DEV), k[2:5].to(DEV), args[0] - 2, *args[1:], inv_freq=inv, interleaved=interleaved, q=q[2:5].to(DEV))
+    assert torch.equal(out[2:5], own.cpu())
