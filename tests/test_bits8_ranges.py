@@ -223,3 +223,15 @@ def test_queries_of_no_request_keep_what_they_hold(append, make, interleaved):
     assert torch.equal(out[idle].view(torch.int16)[~nan], q[idle].view(torch.int16)[~nan])
     own = append(make(), k[2:5].to(DEV), k[2:5].to(DEV), args[0] - 2, *args[1:], inv_freq=inv, interleaved=interleaved, q=q[2:5].to(DEV))
     assert torch.equal(out[2:5], own.cpu())
+
+
+@pytest.mark.parametrize("hint,most", [(False, 24), (True, 24), (True, 18), (True, 2)])
+def test_append_and_read_of_more_than_1024_requests(hint, most):
+    """Past 1024 requests a unit's request is found by halving: ragged ones, some without new tokens, some over a block's end.
+    A hint of fewer tokens than 18 numbers the units by it instead."""
+    g = G.gen(8)
+    R = 1300
+    news = torch.where(torch.rand(R, generator=g) < 0.3, 0, torch.randint(1, most, (R,), generator=g))
+    lens = news + torch.randint(0, 40, (R,), generator=g)
+    lens[5::200] = news[5::200]
+    G.test_append_and_read(64, 2, 1, 16, news.tolist(), lens.tolist(), 32, False, hint)
