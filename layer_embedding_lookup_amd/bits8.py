@@ -19,8 +19,8 @@ import ctypes
 import torch
 
 from . import capi
-from . import _BF16, _F32, _ptr, _req, _same_device, _stream
-from .fp4 import (_BF, _FP8, _MOST, _attention, _attention_workspace_bytes, _fits, _append, _new, _raw_stream, _read)
+from . import _BF16, _F32, _ptr, _req, _same_device
+from .fp4 import (_BF, _FP8, _MOST, _attention, _attention_workspace_bytes, _fits, _append, _given, _new, _raw_stream, _read)
 
 _I8, _FLOAT = torch.int8, torch.float32
 
@@ -52,7 +52,7 @@ def ple_rms_norm8(x, weight, *, residual=None, eps: float = 1e-6, codes=None, sc
         scales = _new((T,), _FLOAT, device, stream)
     rc = capi.load().ple_rms_norm8(x.data_ptr(), x.stride(0) if T > 1 else N, _ptr(residual), _ptr(weight), T, N, eps,
                                    _ptr(codes), _ptr(scales), _ptr(residual_out),
-                                   _raw_stream(dev) if stream is None else _stream(stream))
+                                   _raw_stream(dev) if stream is None else _given(stream, dev))
     if rc:
         capi.check(rc, "ple_rms_norm8")
     return codes, scales, residual_out
@@ -89,7 +89,7 @@ def ple_w8_linear(x, x_scales, w: W8Weight, *, out=None, stream=None):
         _req("out", out, (T, w.out_dim), _BF16)
         _same_device(x, w.codes, out)
     rc = capi.load().ple_w8_linear(x.data_ptr(), x.stride(0) if T > 1 else w.k_dim, _ptr(x_scales), ctypes.byref(w.desc), T,
-                                   _ptr(out), _raw_stream(w.device) if stream is None else _stream(stream))
+                                   _ptr(out), _raw_stream(w.device) if stream is None else _given(stream, w.device))
     if rc:
         capi.check(rc, "ple_w8_linear")
     return out

@@ -25,10 +25,27 @@ _MOST = 2 ** 31 - 1  # ctypes would pass the low 32 bits of a larger window or h
 _BF, _INT = torch.bfloat16, torch.int32
 
 
+def _current(device: int) -> None:
+    """A default stream's handle is 0 on every device, which the library takes for the current one's: work on another
+    device's tensors would run beside that device's own work, on memory that the current device may not reach."""
+    now = torch._C._cuda_getDevice()
+    if now != device:
+        raise ValueError(f"tensors are on cuda:{device}, the current device is cuda:{now}: call under "
+                         f"torch.cuda.device({device})")
+
+
 def _raw_stream(device: int) -> int:
-    """The current stream's handle on the tensors' device (these calls are launch-bound at decode sizes, and building
-    a torch.cuda.Stream object for it costs more than the call)."""
+    """The current stream's handle on the tensors' device, which has to be the current one (these calls are launch-bound at
+    decode sizes, and building a torch.cuda.Stream object for it costs more than the call)."""
+    _current(device)
     return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _given(stream, device: int) -> int:
+    """The handle of the caller's stream, a default one only of the current device."""
+    if not isinstance(stream, int) and stream.cuda_stream == 0:
+        _current(device)
+    return _stream(stream)
 
 
 def _on(stream, device):
@@ -108,7 +125,7 @@ def ple_w4_linear(x, w: W4Weight, *, out=None, stream=None):
         _req("out", out, (T, w.out_dim), _BF16)
         _same_device(x, w.codes, out)
     rc = capi.load().ple_w4_linear(x.data_ptr(), x.stride(0) if T > 1 else w.k_dim, ctypes.byref(w.desc), T,
-                                   _ptr(out), _raw_stream(w.device) if stream is None else _stream(stream))
+                                   _ptr(out), _raw_stream(w.device) if stream is None else _given(stream, w.device))
     if rc:
         capi.check(rc, "ple_w4_linear")
     return out
@@ -197,7 +214,7 @@ def _append(name, cache, k, v, query_start_loc, seq_lens, page_table, inv_freq, 
         _same_device(cache.tensors[0], k, v, q)
     rc = getattr(capi.load(), name)(
         ctypes.byref(cache.desc), ctypes.byref(b), k.data_ptr(), ks, v.data_ptr(), vs, q_at, qs, hq, out_at, freq_at,
-        rot, 1 if interleaved else 0, _raw_stream(cache.device) if stream is None else _stream(stream))
+        rot, 1 if interleaved else 0, _raw_stream(cache.device) if stream is None else _given(stream, cache.device))
     if rc:
         capi.check(rc, name)
     return q_out
@@ -218,7 +235,7 @@ def _read(name, cache, query_start_loc, seq_lens, page_table, num_tokens, k_out,
     v_out = _out("v_out", v_out, shape, _BF16, cache, stream)
     b = _kv4_batch(cache, query_start_loc, seq_lens, page_table, T)
     rc = getattr(capi.load(), name)(ctypes.byref(cache.desc), ctypes.byref(b), _ptr(k_out), _ptr(v_out),
-                                    _raw_stream(cache.device) if stream is None else _stream(stream))
+                                    _raw_stream(cache.device) if stream is None else _given(stream, cache.device))
     if rc:
         capi.check(rc, name)
     return k_out, v_out
@@ -274,7 +291,7 @@ def _attention(name, q, cache, query_start_loc, seq_lens, page_table, window, sc
         q.data_ptr(), qs, hq, ctypes.byref(cache.desc), ctypes.byref(b), window,
         D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse),
         None if workspace is None else _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
-        _raw_stream(cache.device) if stream is None else _stream(stream))
+        _raw_stream(cache.device) if stream is None else _given(stream, cache.device))
     if rc:
         capi.check(rc, name)
     return out, lse
