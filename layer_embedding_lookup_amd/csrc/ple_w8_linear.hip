@@ -275,12 +275,12 @@ __device__ __forceinline__ void w8_tile(const W8Args& a) {
 }
 
 // ---------------------------------------------------------------------------
-// 256-wide tiles with eight waves (two per SIMD) on 16x16x32 MFMAs: wave
+// 256-wide tiles with eight waves (two per SIMD) on 16x16x64 MFMAs: wave
 // (wm, wn) holds a 128 x 64 block (x rows wm*128.., W rows wn*64..) as 8 x 4
 // accumulator tiles of 16 x 16 (128 accumulation registers), so a wave
 // waiting on its fragments leaves the matrix core to the other wave of its
 // SIMD.  Row layout in LDS and the copy instructions as the four-wave body; a
-// slice is two K-steps of 32 with 12 fragment reads each.  Instead of two
+// slice is two K-steps of 64 with 12 fragment reads each.  Instead of two
 // stages of both operands, the LDS holds a ring of five operand slices, which
 // gives the W copies a second slice of lead.  The tiles an XCD runs at once
 // are grouped four tile rows by eight tile columns, so each W panel is shared
@@ -380,7 +380,7 @@ __device__ __forceinline__ void w8_pipe8w(const W8Args& a) {
     auto wait_barrier = [&](W8WideFrag& f) {
         asm volatile("s_waitcnt vmcnt(%12) lgkmcnt(0)\n\ts_barrier" : PLE_W8_WIDE_FRAG_REGS(f) : "i"(NC) : "memory");
     };
-    // one K-step of 32: 32 MFMAs on cur; after MFMA t < 12, fragment read t of
+    // one K-step of 64: 32 MFMAs on cur; after MFMA t < 12, fragment read t of
     // (rkt, rks) into nxt; with ckt >= 0, the NC copies of x slice ckt after
     // MFMAs 2 and 10, then those of W slice ckt + 1 after MFMAs 18 and 26
     auto kstep = [&](const W8WideFrag& cur, W8WideFrag& nxt, int rkt, int rks, int ckt) {
@@ -465,11 +465,12 @@ PLE_W8_TILES(PLE_W8_KERNEL)
 #undef PLE_W8_KERNEL
 
 // The few-token kernel's LDS: a step's inputs and weights of every wave, then the joined sums.  ROWS: rows of x it has room
-// for (4, or 16 a token tile), STEP: bytes of K.
+// for (16 a token tile), STEP: bytes of K.
 constexpr int kRowsWaves = 8;
 template <int ROWS, int NT, int STEP>
 struct W8RowsShape {
-    static constexpr int MT = (ROWS + 15) / 16;
+    static_assert(ROWS % 16 == 0, "whole token tiles");
+    static constexpr int MT = ROWS / 16;
     static constexpr int X = ROWS * STEP;                 // bytes of a wave's inputs
     static constexpr int ALL = X + NT * 16 * STEP;        // and weights
     static constexpr int JOIN = 4;                        // waves whose sums are in LDS at once
@@ -527,7 +528,7 @@ __device__ __forceinline__ void w8_rows_body(const W8Args& a) {
             u32x4 x[MT], w[NT];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const int r = ROWS < 16 ? n % ROWS : mt * 16 + n;  // (tokens past ROWS: any row, not stored)
+                const int r = mt * 16 + n;
                 x[mt] = *(const u32x4*)(mine + r * STEP + (c ^ Sh::turn(r)) * 16);
                 if (k0 + STEP > a.K && k0 + c * 16 >= a.K) x[mt] = u32x4{0u, 0u, 0u, 0u};
             }
