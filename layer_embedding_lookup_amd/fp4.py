@@ -37,7 +37,8 @@ def _current(device: int) -> None:
 def _raw_stream(device: int) -> int:
     """The current stream's handle on the tensors' device, which has to be the current one (these calls are launch-bound at
     decode sizes, and building a torch.cuda.Stream object for it costs more than the call)."""
-    _current(device)
+    if torch._C._cuda_getDevice() != device:
+        _current(device)
     return torch._C._cuda_getCurrentRawStream(device)
 
 
