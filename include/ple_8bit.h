@@ -96,8 +96,8 @@ typedef ple_kv4_batch ple_kv8_batch;
  * and that is not enters as fp32 quotients, x * (1 / s) and code * (its / s).
  * Tokens of the block behind the new ones are as good as gone (their scale may
  * have changed).  A page that the batch writes to in two places, of two requests
- * or twice in one's table row, holds unspecified values.  Other arguments as for ple_kv4_append;
- * max_request_tokens sizes the launch.
+ * or twice in one's table row, holds unspecified values.  Other arguments as for ple_kv4_append.
+ * max_request_tokens sizes the launch: of a request with more new tokens than it says the last ones may not be stored.
  */
 int ple_kv8_append(const ple_kv8_cache* cache, const ple_kv8_batch* batch, const uint16_t* k, int64_t k_stride,
                    const uint16_t* v, int64_t v_stride, const uint16_t* q, int64_t q_stride, int32_t num_q_heads,
@@ -114,7 +114,10 @@ int ple_kv8_read(const ple_kv8_cache* cache, const ple_kv8_batch* batch, uint16_
  * fp16 or better: a token's part of an output element is off by at most 2^-11
  * of itself or 2^-27 of its value, whatever the other blocks' scales are.
  * (Where the scales of a request's blocks lie more than 2^6 apart, the call
- * goes through the tiles around them twice.)
+ * goes through the tiles around them twice.)  As there, a few long prefills
+ * beside many single tokens take less time as two calls (1000 tokens behind
+ * 1000 and 16 single ones over 6000 each 215 us as one, 107 as two; over 100000
+ * 3.1 ms and 0.6).
  */
 int ple_kv8_attention(const uint16_t* q, int64_t q_stride, int32_t num_q_heads, const ple_kv8_cache* cache,
                       const ple_kv8_batch* batch, int32_t window, float scale, uint16_t* out, float* lse,

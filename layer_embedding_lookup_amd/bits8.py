@@ -118,7 +118,7 @@ def ple_kv8_append(cache: KV8Cache, k, v, query_start_loc, seq_lens, page_table,
                    interleaved: bool = False, q=None, q_out=None, max_request_tokens: int = 0, stream=None):
     """New keys and values bf16 [T][heads][D] into the cache, keys (and q, if given) rotated by their positions over
     the first 2 * len(inv_freq) elements.  max_request_tokens (0: unknown): no request has more new tokens, which sizes the
-    launch.  Returns the rotated queries bf16 [T][q heads][D], or None without q."""
+    launch (of one that has more, the last ones may not be stored).  Returns the rotated queries bf16 [T][q heads][D], or None without q."""
     return _append("ple_kv8_append", cache, k, v, query_start_loc, seq_lens, page_table, inv_freq, interleaved, q, q_out,
                    stream, max_request_tokens)
 
@@ -141,6 +141,6 @@ def ple_kv8_attention(q, cache: KV8Cache, query_start_loc, seq_lens, page_table,
                       max_request_tokens: int = 0, max_seq_len: int = 0, want_lse: bool = False, out=None, lse=None,
                       workspace=None, stream=None):
     """Causal attention of the new tokens q bf16 [T][q heads][D] over the cache; arguments and results as for
-    ple_kv4_attention."""
+    ple_kv4_attention, long prefills and single tokens better in two calls too."""
     return _attention("ple_kv8_attention", q, cache, query_start_loc, seq_lens, page_table, window, scale,
                       max_request_tokens, max_seq_len, want_lse, out, lse, workspace, stream)

@@ -28,9 +28,9 @@
 //    neighbouring lanes' 64 contiguous bytes; its 16 bytes of value codes are
 //    one element of 16 tokens, 16 lanes' 256 contiguous bytes.
 //
-// Few rows are bound by reading the cache: 256 requests of 3164 tokens on
-// average 289 us, 5.6 TB/s, 89% of a copy's rate; one of 100100 tokens 43 us
-// with the join of its 32 splits; 64 verify windows of four tokens 17.7, a
+// Few rows are bound by reading the cache: 256 requests of 3084 tokens on
+// average 288 us, 5.6 TB/s, 89% of a copy's rate; one of 100100 tokens 43 us
+// with the join of its 32 splits; 64 verify windows of four tokens 17.9, a
 // chain of two to three tiles a wave.  Many rows: see there.
 #include <type_traits>
 
@@ -489,7 +489,7 @@ PLE_ATTN_SHAPES(PLE_ATTN_KERNEL)
 // reads ahead, 209 in turns, 204 with the scales' loads out of their branch,
 // 197 with row tiles that move on each by themselves and the join's loads all
 // at once, 188 with the join told where cuts are, 184 with two pieces of it at a
-// time (0.71 PFLOP/s, 17 of them the join).  The SIMDs then issue vector instructions for 55% of the cycles that a
+// time, 187 with the values' scales watched (0.70 PFLOP/s, 17 us of it the join).  The SIMDs then issue vector instructions for 55% of the cycles that a
 // CU is busy and their matrix cores are for 34%: two waves a SIMD, with all
 // registers, overlap little more.  64 rows a wave, one wave a SIMD, halve the
 // reads of LDS but take 277 us.
@@ -848,7 +848,11 @@ PLE_ATTN_KERNEL(256)
 // tiles) 175 and 183, 146 and 158; 30 x 300 behind 3000 (2400) 428 and 435; 4 x 800 behind 900, D = 64, 88 and 80.  With heads
 // of 256, one block per CU, shares gain from fewer on: 2000 and 4 x 1000 behind nothing (250 and 500 tiles) 101 and 111, 107
 // and 122; 4 x 1000 behind 1000 156 and 244; 100 behind 600 and 1200 48 and 49, 50 and 78; 2 x 500 behind 400 55 and 54.
-constexpr int kFlatPast = 896, kFlatPastWide = 384;  // cache tokens of the shortest query tiles
+// How long the shortest tiles are is not known here: it is taken for what the hints (or the table and T) leave, the most
+// cached tokens that a request with the most new ones can have.  Where one request has them and the others none: 4 x 500, one
+// behind 6000, 118 and 220, behind 1000 67 and 64; 2 x 1000, one behind 8000 212 and 290, behind 1000 85 and 77; 8 x 100, one
+// behind 2000, 49 and 64.
+constexpr int kFlatPast = 896, kFlatPastWide = 384;  // cache tokens in front of the new ones
 constexpr int kFlatTiles = 1536, kFlatTilesWide = 192;
 
 // Few rows: splits of at least 1024 tokens (8 requests of up to 2500 tokens 15.9 us, with 512 15.6, 2048 16.3; one of 777
@@ -866,7 +870,7 @@ void plan_kv8_attention(Kv8AttentionArgs& a) {
     const int64_t rows = new_max * a.group;
     a.rows = rows <= 16 || (rows <= 64 && a.cache.head_dim == 256) ? 16 : (rows <= 64 ? 32 : kChunkRows);
     a.tiles = (int)((rows + a.rows - 1) / a.rows);
-    int64_t past = len - new_max;  // cache tokens of the shortest query tiles
+    int64_t past = len - new_max;  // cache tokens in front of the new ones, by the largest of each
     if (a.window > 0) {
         const int64_t span = (int64_t)a.window + a.rows / a.group + 1 + 15;
         len = len < span ? len : span;

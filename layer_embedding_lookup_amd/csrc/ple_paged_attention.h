@@ -21,12 +21,13 @@ constexpr int kFewSplits = 8;  // up to which one wave joins a row
 // a tenth of the 1.65e-3 of its rounding to bf16: 0.00166 against 64 bits with it and 0.00165 without.
 constexpr float kWeightShift = 8.0f, kSlack = 7.0f;
 
-// Measured with 32 heads of 128 over 8 where nothing else is said, and where a value other than these does better too:
-//  kFlatLeast: 1289 + 1455 tokens at 5403 and 2004 232 us with 4, 8 and 16, 237 with 2; 100 behind 2000 43 (with 4 44, 2 54,
-//              16 58); 1000 behind nothing 54 (4 53, 16 70); but 100 behind nothing 30 (4 21), 50 behind 500 38 (4 30).
-//  kFlatStart: the first 232 us (with 0 278, 2 252, 8 242), the second 44.5 (51, 46, 43.7), the third 54 (86, 60, 56).
-//  kFlatUnits: 736 query tiles 233 us in shares, 401 a block each; 4864 of 32 requests 330 and 275, which the rule keeps
-//              apart; between them it takes the slower one (1920 tiles of 16 requests 165 and 155, 2560 of 32 162 and 146).
+// Measured in 4 bits with 32 heads of 128 over 8, and where a value other than these does better too:
+//  kFlatLeast: 1289 + 1455 tokens at 5403 and 2004 219 us with 2, 4, 8 and 16; 100 behind 2000 40.5 (with 4 42, 2 45, 16 57);
+//              1000 behind nothing 50 (4 51, 16 66); but 100 behind nothing 27 (4 18), 50 behind 500 33 (4 28).
+//  kFlatStart: the first 219 us (with 0 256, 2 238, 8 228), the second 40.5 (48, 43, 40), the third 50 (82, 58, 56).
+//  kFlatUnits: 736 query tiles 219 us in shares, 388 a block each; 4864 of 32 requests 419 and 388, which the rule keeps
+//              apart; but it takes the slower one for 1920 tiles of 16 requests (207 and 179), 2560 of 32 (243 and 211) and
+//              behind nothing (1000 tokens 50 and 47, 100 27 and 15).  The 8-bit plan has a rule of its own for those.
 constexpr int kFlatLeast = 8;        // places of a share at least
 constexpr int kFlatStart = 4;        // places that beginning a query tile counts for (queries in, results out)
 constexpr int kFlatUnits = 4096;     // query tiles (of all heads and requests) up to which the work is cut into shares
@@ -160,7 +161,7 @@ struct PageWalk {
 // shares; a query tile has kFlatStart places in front of its cache tiles.  A query tile whose cache tiles a cut goes
 // through is joined by a second kernel: of its pieces the one that begins it is partial result 2 * share + 1, every
 // other 2 * share of its share.  The share that begins it leaves word of it (AttnCut) behind the partial results.
-// A chunk of 1289 + 1455 tokens at 5403 and 2004: 308 us with a block a query tile (CUs busy for 53% of it).
+// A chunk of 1289 + 1455 tokens at 5403 and 2004: 388 us with a block a query tile, 219 in shares (in 4 bits).
 struct AttnFlat {
     // of lane r:
     int first, n, len, pos;  // request r's first new token, new tokens, length, position of the first new token

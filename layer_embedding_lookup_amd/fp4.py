@@ -303,7 +303,8 @@ def ple_kv4_attention(q, cache: KV4Cache, query_start_loc, seq_lens, page_table,
                       workspace=None, stream=None):
     """Causal attention of the new tokens q bf16 [T][q heads][D] over the cache (their own keys appended before).
     scale: 1/sqrt(D) if None.  window: tokens seen, the own one included (0: all).  max_request_tokens and
-    max_seq_len (0: unknown) let the call size its launch; pass them.  Returns (out bf16 [T][q heads][D], lse fp32
+    max_seq_len (0: unknown) let the call size its launch; pass them (the launch is that of the longest requests: long
+    prefills and many single tokens take less time in two calls).  Returns (out bf16 [T][q heads][D], lse fp32
     [T][q heads] or None)."""
     return _attention("ple_kv4_attention", q, cache, query_start_loc, seq_lens, page_table, window, scale,
                       max_request_tokens, max_seq_len, want_lse, out, lse, workspace, stream)
