@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArg
         const double angle = (double)pos * (double)a.inv_freq[i];
         double sn, cs;
         sincos(angle, &sn, &cs);
-        turn[turn_place(i, half)] = make_double2(cs, sn);
+        turn[Turns<false>::place(i, half)] = make_double2(cs, sn);
     }
     __syncthreads();
     const int64_t group0 = first_group(a.cache, a.batch.page_table + (int64_t)r * a.batch.table_width, pos);
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv4_append_kernel(Kv4AppendArg
         const int head = at >> shift, d0 = (at & (per_head - 1)) * 8;
         const uint16_t* src = a.src[which] + t * a.stride[which] + head * D;
         float v[8];
-        load_rotated(src, d0, which != 2 ? rot : 0, a.interleaved, turn, v);
+        load_rotated<Turns<false>>(src, d0, which != 2 ? rot : 0, a.interleaved, turn, v);
         if (which == 0) {
             u32x4 o;
 #pragma unroll

@@ -214,7 +214,7 @@ __device__ __forceinline__ void append_keys(const Kv8AppendArgs& a, const Kv8Uni
             const int from = a.interleaved ? lane : (c * 8 < half ? lane + half / 8 : (c * 8 < 2 * half ? lane - half / 8 : lane));
 #pragma unroll
             for (int e = 0; e < 4; ++e) other[e] = __shfl(raw.key[i][e], from, kWave);
-            if (c * 8 < a.rot_dim && token >= w.from && token < w.to) turn8(x[i], other, c * 8, half, a.interleaved, turn[token]);
+            if (c * 8 < a.rot_dim && token >= w.from && token < w.to) turn8<Turns<true>>(x[i], other, c * 8, half, a.interleaved, turn[token]);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_size(x[i][e]));
@@ -342,7 +342,7 @@ __device__ __forceinline__ void append_body(const Kv8AppendArgs& a, int64_t unit
                 sincospi(2. * ((double)(w.block * 16 + j0) * by), &sn, &cs);
                 if (j1 > j0 + 1) sincospi(2. * by, &s1, &c1);
                 for (int j = j0; j < j1; ++j) {
-                    turn[j][turn_place(f, half)] = make_double2(cs, sn);
+                    turn[j][Turns<true>::place(f, half)] = make_double2(cs, sn);
                     const double c = cs * c1 - sn * s1;
                     sn = sn * c1 + cs * s1;
                     cs = c;
@@ -363,13 +363,13 @@ __device__ __forceinline__ void append_body(const Kv8AppendArgs& a, int64_t unit
     for (int i = threadIdx.x; i < rot / 2; i += kAppendThreads) {
         double sn, cs;
         sincospi(2. * ((double)pos * ((double)a.inv_freq[i] * kPerTurn)), &sn, &cs);
-        turn[0][turn_place(i, half)] = make_double2(cs, sn);
+        turn[0][Turns<true>::place(i, half)] = make_double2(cs, sn);
     }
     __syncthreads();
     for (int c = threadIdx.x; c < a.num_q_heads * (D / 8); c += kAppendThreads) {
         const int head = c / (D / 8), d0 = c % (D / 8) * 8;
         float v[8];
-        load_rotated(a.src[0] + t * a.stride[0] + head * D, d0, rot, a.interleaved, turn[0], v);
+        load_rotated<Turns<true>>(a.src[0] + t * a.stride[0] + head * D, d0, rot, a.interleaved, turn[0], v);
         u32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);

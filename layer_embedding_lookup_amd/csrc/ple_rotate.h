@@ -14,17 +14,24 @@ __device__ __forceinline__ void load8(const uint16_t* __restrict__ p, float (&v)
     }
 }
 
-// Where angle f of a token's `half` (a multiple of 8) stands in LDS: lanes that turn neighbouring eights of a head read
-// neighbouring places.
-__device__ __forceinline__ int turn_place(int f, int half) { return (f & 7) * (half >> 3) + (f >> 3); }
+// Where angle f of a token's `half` (a multiple of 8) stands in LDS: spread, so that lanes that turn neighbouring eights of a
+// head read neighbouring places, or in order, where a lane's reads are one address and the next ones (a block per token, which
+// spends more on forming places than it saves: 4 bits, 7984 tokens, 42.6 us in order, 45.6 spread).
+template <bool SPREAD>
+struct Turns {
+    static __device__ __forceinline__ int place(int f, int half) { return SPREAD ? (f & 7) * (half >> 3) + (f >> 3) : f; }
+    // from an angle to the next one of the same eight, or four
+    static __device__ __forceinline__ int step(int half) { return SPREAD ? half >> 3 : 1; }
+};
 
-// Elements d0 .. d0 + 7 of a head's row (v, inside its first 2 half), turned by the token's angles (turn[turn_place(i)]:
+// Elements d0 .. d0 + 7 of a head's row (v, inside its first 2 half), turned by the token's angles (turn[At::place(i)]:
 // cosine and sine of angle i); other: the row's elements half a rotation away, if pairs are not neighbours.  In 64 bits and rounded once to
 // fp32, so that an element next to a code's border falls on the side that the definition says.
+template <class At>
 __device__ __forceinline__ void turn8(float (&v)[8], u32x4 other, int d0, int half, bool interleaved, const double2* turn) {
-    const int step = half >> 3;  // (from an angle to the next one of the same eight, or four)
+    const int step = At::step(half);
     if (interleaved) {
-        turn += turn_place(d0 / 2, half);
+        turn += At::place(d0 / 2, half);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const double2 w = turn[i * step];
@@ -34,7 +41,7 @@ __device__ __forceinline__ void turn8(float (&v)[8], u32x4 other, int d0, int ha
         }
     } else {
         const bool upper = d0 >= half;  // half is a multiple of 8
-        turn += turn_place(upper ? d0 - half : d0, half);
+        turn += At::place(upper ? d0 - half : d0, half);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const double2 w = turn[i * step];
@@ -45,6 +52,7 @@ __device__ __forceinline__ void turn8(float (&v)[8], u32x4 other, int d0, int ha
 }
 
 // Elements d0 .. d0 + 7 of a head's row in memory, turned where they lie in its first rot_dim.
+template <class At>
 __device__ __forceinline__ void load_rotated(const uint16_t* __restrict__ src, int d0, int rot_dim, bool interleaved,
                                              const double2* turn, float (&v)[8]) {
     load8(src + d0, v);
@@ -52,7 +60,7 @@ __device__ __forceinline__ void load_rotated(const uint16_t* __restrict__ src, i
     const int half = rot_dim / 2;
     u32x4 other = {0u, 0u, 0u, 0u};
     if (!interleaved) other = *(const u32x4*)(src + (d0 >= half ? d0 - half : d0 + half));
-    turn8(v, other, d0, half, interleaved, turn);
+    turn8<At>(v, other, d0, half, interleaved, turn);
 }
 
 }  // namespace ple
