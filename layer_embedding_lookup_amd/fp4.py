@@ -23,12 +23,13 @@ from . import _BF16, _BYTES, _F32, _I32, _nbytes, _ptr, _req, _req_bytes, _same_
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
 _MOST = 2 ** 31 - 1  # ctypes would pass the low 32 bits of a larger window or hint; all of them mean "no limit"
 _BF, _INT = torch.bfloat16, torch.int32
+_get_device, _get_raw_stream = (getattr(torch._C, n, None) for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
 
 
 def _current(device: int) -> None:
     """A default stream's handle is 0 on every device, which the library takes for the current one's: work on another
     device's tensors would run beside that device's own work, on memory that the current device may not reach."""
-    now = torch._C._cuda_getDevice()
+    now = _get_device()
     if now != device:
         raise ValueError(f"tensors are on cuda:{device}, the current device is cuda:{now}: call under "
                          f"torch.cuda.device({device})")
@@ -37,9 +38,9 @@ def _current(device: int) -> None:
 def _raw_stream(device: int) -> int:
     """The current stream's handle on the tensors' device, which has to be the current one (these calls are launch-bound at
     decode sizes, and building a torch.cuda.Stream object for it costs more than the call)."""
-    if torch._C._cuda_getDevice() != device:
+    if _get_device() != device:
         _current(device)
-    return torch._C._cuda_getCurrentRawStream(device)
+    return _get_raw_stream(device)
 
 
 def _given(stream, device: int) -> int:
@@ -248,13 +249,16 @@ def ple_kv4_read(cache: KV4Cache, query_start_loc, seq_lens, page_table, num_tok
     return _read("ple_kv4_read", cache, query_start_loc, seq_lens, page_table, num_tokens, k_out, v_out, stream)
 
 
+_WORKSPACE = {n: n + "_workspace_bytes" for n in ("ple_kv4_attention", "ple_kv8_attention")}
+
+
 def _attention_workspace_bytes(name, cache, num_q_heads, num_tokens, num_reqs, table_width, window, max_request_tokens,
                                max_seq_len) -> int:
     any_ptr = cache.desc.k_codes  # sizes alone matter here
     b = capi.ple_kv4_batch(any_ptr, any_ptr, any_ptr, int(num_tokens), int(num_reqs), int(table_width),
                            min(int(max_request_tokens), _MOST), min(int(max_seq_len), _MOST))
-    return int(getattr(capi.load(), name + "_workspace_bytes")(int(num_q_heads), ctypes.byref(cache.desc), ctypes.byref(b),
-                                                               min(int(window), _MOST)))
+    return int(getattr(capi.load(), _WORKSPACE[name])(int(num_q_heads), ctypes.byref(cache.desc), ctypes.byref(b),
+                                                      min(int(window), _MOST)))
 
 
 def ple_kv4_attention_workspace_bytes(cache: KV4Cache, num_q_heads: int, num_tokens: int, num_reqs: int,
@@ -277,7 +281,8 @@ def _attention(name, q, cache, query_start_loc, seq_lens, page_table, window, sc
     if q.get_device() != cache.device:
         _same_device(cache.tensors[0], q)
     lib = capi.load()
-    need = int(getattr(lib, name + "_workspace_bytes")(hq, ctypes.byref(cache.desc), ctypes.byref(b), window))
+    desc, batch = ctypes.byref(cache.desc), ctypes.byref(b)
+    need = getattr(lib, _WORKSPACE[name])(hq, desc, batch, window)
     if workspace is None:
         if need > 0:  # (given up on return, before the work has ended: taken in the order of the stream it runs on)
             if stream is None:
@@ -289,7 +294,7 @@ def _attention(name, q, cache, query_start_loc, seq_lens, page_table, window, sc
         _req_bytes("workspace", workspace, need)
         _same_device(cache.tensors[0], workspace)
     rc = getattr(lib, name)(
-        q.data_ptr(), qs, hq, ctypes.byref(cache.desc), ctypes.byref(b), window,
+        q.data_ptr(), qs, hq, desc, batch, window,
         D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse),
         None if workspace is None else _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
         _raw_stream(cache.device) if stream is None else _given(stream, cache.device))

@@ -40,9 +40,9 @@ def operators(kv4):
 @pytest.mark.parametrize("stream", [None, Default], ids=["current", "default"])
 def test_default_streams_of_other_devices(calls, cache, monkeypatch, stream):  # noqa: F811
     monkeypatch.setattr(bits8, "_same_device", lambda *t: None)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    monkeypatch.setattr(fp4, "_get_raw_stream", lambda device: 0)
     for now in (0, 1):
-        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now, raising=False)
+        monkeypatch.setattr(fp4, "_get_device", lambda: now)
         for name, call in operators(cache).items():
             if name == "ple_rms_norm8":                       # (goes by its tensors' own device, which is the CPU's -1 here)
                 continue
@@ -61,7 +61,7 @@ def test_default_streams_of_other_devices(calls, cache, monkeypatch, stream):  #
 def test_other_streams_know_their_device(calls, cache, monkeypatch):  # noqa: F811
     """A stream of one's own, or a handle, is taken as it is."""
     monkeypatch.setattr(bits8, "_same_device", lambda *t: None)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(fp4, "_get_device", lambda: 0)
     for name, call in operators(cache).items():
         call(9)
         assert calls[name][-1] == 9
