@@ -9,7 +9,8 @@ a paged 4-bit key/value cache and attention over it.
 
 Like the rest of the binding these only marshal tensors; the header states
 formats, layouts and limits.  Outputs and workspaces that a call makes itself
-belong to the stream it runs on (`stream`, or the current one).
+belong to the stream it runs on (`stream`, or the current one).  Tensors are on
+the current device, or on that of a `stream` that is not a default one.
 """
 from __future__ import annotations
 
